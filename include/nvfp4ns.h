@@ -350,6 +350,165 @@ ns_status ns_orthogonalize_grouped_on(int count, const void* const* G, const int
                                       ns_dtype ot, void* ws, size_t ws_bytes,
                                       void* const* streams, int nstreams, void* stream);
 
+/* ======================================================================
+ * MXFP4: 4-bit values with power-of-two block scales, the 4-bit format
+ * that gfx950's matrix instructions multiply themselves.
+ *
+ * A block is 32 consecutive elements along the blocked axis: E2M1 codes and
+ * one E8M0 byte b, value = x_E2M1 * 2^(b - 127); b = 255 makes the block
+ * NaN.  There is no tensor scale, so a block's encoding depends on the block
+ * alone (one pass; the same bytes whatever surrounds it):
+ *   b = max(floor(log2 max|x|) - 2 + 127, 0) (0 for an all-zero block),
+ *   code = sign | RNE_E2M1(|x| / 2^(b - 127)), ties to the even code, values
+ *   of 5 and more (up to 8 occur) becoming 6;
+ *   a block with a NaN or an infinity: b = 255, codes 0.
+ *
+ * Storage ("panels"): rows are cut along the blocked axis into panels of 256
+ * elements; codes are [panels][rows][128] bytes, two codes a byte, element
+ * 2i in the low nibble, scales [panels][rows][8] bytes, with
+ * panels = ceil(length / 256).  Behind a row's end a panel holds all-zero
+ * blocks (codes 0; b = 0 for blocks without elements).  NVFP4_COLS stores the
+ * transpose: its rows are the matrix's columns.
+ *
+ * Dimensions are 1 .. 2^24, of any parity.
+ * ====================================================================== */
+size_t mxfp4_codes_bytes(int64_t rows, int64_t cols, nvfp4_axis axis);
+size_t mxfp4_scales_bytes(int64_t rows, int64_t cols, nvfp4_axis axis);
+
+/*
+ * mxfp4_quantize — a rows x cols matrix to MXFP4, blocked along its rows
+ * (NVFP4_ROWS) or down its columns (NVFP4_COLS).
+ *   x       [rows][cols] FP32 or BF16 (xt), read only.
+ *   codes   out, mxfp4_codes_bytes();  scales  out, mxfp4_scales_bytes().
+ */
+ns_status mxfp4_quantize(const void* x, ns_dtype xt, int64_t rows, int64_t cols, nvfp4_axis axis,
+                         uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * mxfp4_quantize_both — both of the above in one pass over x: what training
+ * needs of activations, gradients and weights, which are contracted along one
+ * axis forward and along the other backward.  Same bytes as two calls.
+ */
+ns_status mxfp4_quantize_both(const void* x, ns_dtype xt, int64_t rows, int64_t cols,
+                              uint8_t* codes_rows, uint8_t* scales_rows, uint8_t* codes_cols,
+                              uint8_t* scales_cols, void* stream);
+
+/*
+ * mxfp4_dequantize — the values, [rows][cols] in the original orientation,
+ * FP32 or BF16 (ot); both hold every MXFP4 value exactly.
+ */
+ns_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                           nvfp4_axis axis, void* out, ns_dtype ot, void* stream);
+
+/*
+ * mxfp4_gemm — out = beta * addend + alpha * P Q^T, P [M][K] and Q [N][K] in
+ * MXFP4 blocked along K, products exact and accumulated in FP32.
+ *   addend  [M][N] FP32; NULL when beta == 0; may be out itself when ot is
+ *           NS_F32.
+ *   out     [M][N] FP32 or BF16 (ot), rounded once.
+ *   ws      device scratch of mxfp4_gemm_workspace_bytes(), through which
+ *           tiles split along K pass FP32 partials, summed in a fixed order;
+ *           NULL with ws_bytes 0 runs every tile whole.  Calls sharing one ws
+ *           must not overlap.
+ * A NaN block makes the rows (columns) of out that it meets NaN.
+ */
+size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+ns_status mxfp4_gemm(const uint8_t* codes_p, const uint8_t* scales_p, const uint8_t* codes_q,
+                     const uint8_t* scales_q, int64_t M, int64_t N, int64_t K, float alpha,
+                     float beta, const float* addend, void* out, ns_dtype ot, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/*
+ * mxfp4_linear — y = Q(x) w^T for T tokens: x [T][K] FP32 or BF16, quantized
+ * along K by the call, w [N][K] in MXFP4 (NVFP4_ROWS), y [T][N] FP32 or BF16.
+ *   kept_codes, kept_scales  both NULL, or out: x quantized along the tokens
+ *           (NVFP4_COLS), which mxfp4_linear_backward takes for the weights'
+ *           gradient.
+ *   ws      device scratch of mxfp4_linear_workspace_bytes().
+ */
+size_t mxfp4_linear_workspace_bytes(int64_t T, int64_t N, int64_t K);
+ns_status mxfp4_linear(const void* x, ns_dtype xt, int64_t T, int64_t K, const uint8_t* w_codes,
+                       const uint8_t* w_scales, int64_t N, void* y, ns_dtype yt,
+                       uint8_t* kept_codes, uint8_t* kept_scales, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/*
+ * mxfp4_linear_backward — the gradients of mxfp4_linear with the quantizers'
+ * own derivative taken as 1 (straight through):
+ *   dx [T][K] = Q_N(dy) w         Q_N: along N, w along N (wt)
+ *   dw [N][K] = beta dw + Q_T(dy)^T Q_T(x)   Q_T: along the tokens
+ *   dy      [T][N] FP32 or BF16.
+ *   wt      the weights quantized down their columns (NVFP4_COLS of [N][K]);
+ *           may be NULL when dx is.
+ *   kept    as written by mxfp4_linear; may be NULL when dw is.
+ *   dx, dw  FP32 or BF16; either may be NULL.  beta != 0 adds to what dw
+ *           holds and needs FP32.
+ *   ws      device scratch of mxfp4_linear_backward_workspace_bytes().
+ */
+size_t mxfp4_linear_backward_workspace_bytes(int64_t T, int64_t N, int64_t K);
+ns_status mxfp4_linear_backward(const void* dy, ns_dtype dyt, int64_t T, int64_t N, int64_t K,
+                                const uint8_t* wt_codes, const uint8_t* wt_scales,
+                                const uint8_t* kept_codes, const uint8_t* kept_scales, void* dx,
+                                ns_dtype dxt, void* dw, ns_dtype dwt, float beta, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* ======================================================================
+ * Newton–Schulz without quantization: f16 operands, FP32 accumulation.
+ *   X_0 = clamp(G, -clip, clip) / (||clamp(G)||_F + 1e-7)    (on G^T if m > n)
+ *   A = X X^T;  B = a I + b A + c A A;  X <- B X
+ * X (times 256), A and B are rounded to f16 once per step; BF16 sources enter
+ * without rounding.  Five quintic steps stay within 2e-3 of exact arithmetic
+ * (relative Frobenius norm) on matrices whose singular values span three
+ * decades or less; directions further below the norm are amplified together
+ * with the rounding of those above them.  |X| beyond 255 (divergent
+ * coefficients) overflows to infinity.  NaN or infinity in a matrix makes
+ * its result NaN; a zero matrix gives zero.  Dimensions are 1 .. 2^24, of any
+ * parity, m * n < 2^31.
+ * ====================================================================== */
+
+/* Workspace of the calls below for `count` matrices, in bytes (matrices of one
+ * shape run as a batch; different shapes share it one after another). */
+size_t ns_f16_workspace_bytes(int count, const int64_t* m, const int64_t* n);
+
+/* ns_orthogonalize_f16 — one matrix; arguments as ns_orthogonalize, workspace
+ * ns_f16_workspace_bytes(1, &m, &n). */
+ns_status ns_orthogonalize_f16(const void* G, ns_dtype gt, int64_t m, int64_t n, const float* coeffs,
+                               int k, float clip, void* out, ns_dtype ot, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/* ns_orthogonalize_f16_grouped — `count` matrices, arguments as
+ * ns_orthogonalize_grouped (clip may be NULL: no clipping), everything on
+ * `stream`.  A matrix's result may differ from its single call's in the last
+ * bits: products are split along K by the batch's size. */
+ns_status ns_orthogonalize_f16_grouped(int count, const void* const* G, const int64_t* m,
+                                       const int64_t* n, ns_dtype gt, const float* coeffs, int k,
+                                       const float* clip, void* const* out, ns_dtype ot, void* ws,
+                                       size_t ws_bytes, void* stream);
+
+/* Options of ns_muon_step. */
+typedef struct {
+  float lr, momentum, weight_decay;
+  int nesterov;             /* nonzero: U = G + momentum M, else U = M */
+} ns_muon_options;
+
+/*
+ * ns_muon_step — one Muon step on `count` weight matrices:
+ *   M <- momentum M + G                      (stored in M's type)
+ *   U = G + momentum M  or  M                (M as stored)
+ *   W <- (1 - lr weight_decay) W - lr scale_i NS(U)
+ * with NS the k steps above (no clipping).
+ *   W, M    HOST arrays of device pointers, updated in place, FP32 or BF16
+ *           (wt, mt); G likewise (gt), read only.  m, n  HOST arrays.
+ *   scale   HOST array of one factor per matrix (such as
+ *           0.2 sqrt(max(m, n))), or NULL: 1.
+ *   ws      device scratch of ns_f16_workspace_bytes().
+ * No array may overlap another.  A NaN or infinity in U makes W NaN.
+ */
+ns_status ns_muon_step(int count, void* const* W, ns_dtype wt, void* const* M, ns_dtype mt,
+                       const void* const* G, ns_dtype gt, const int64_t* m, const int64_t* n,
+                       const float* coeffs, int k, const ns_muon_options* opt, const float* scale,
+                       void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,7 +11,10 @@ Functions carry the C names:
     ns_orthogonalize, ns_orthogonalize_rht, ns_orthogonalize_ex,
     ns_abs_quantile_workspace_bytes, ns_abs_quantile,
     ns_grouped_workspace_bytes, ns_orthogonalize_grouped, ns_orthogonalize_grouped_ex,
-    ns_orthogonalize_grouped_on
+    ns_orthogonalize_grouped_on,
+    mxfp4_quantize, mxfp4_quantize_both, mxfp4_dequantize, mxfp4_gemm_workspace_bytes, mxfp4_gemm,
+    mxfp4_linear, mxfp4_linear_backward,
+    ns_f16_workspace_bytes, ns_orthogonalize_f16, ns_orthogonalize_f16_grouped, ns_muon_step
 """
 import ctypes
 import os
@@ -47,6 +50,12 @@ class NsOptions(ctypes.Structure):
     _fields_ = [("clip", ctypes.c_float), ("clip_quantile", ctypes.c_double),
                 ("rht_masks", ctypes.POINTER(ctypes.c_uint16)), ("adaptive46", ctypes.c_int)]
 
+class NsMuonOptions(ctypes.Structure):
+    """ns_muon_options of the C ABI."""
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float),
+                ("weight_decay", ctypes.c_float), ("nesterov", ctypes.c_int)]
+
+
 class NsWorkspaceMap(ctypes.Structure):
     """ns_workspace_map of the C ABI (byte offsets into an NS workspace)."""
     _fields_ = [("xm", ctypes.c_int64), ("xn", ctypes.c_int64),
@@ -81,6 +90,24 @@ _SIGS = {
                                          _vp]),
     "ns_orthogonalize_grouped_on": (_i, [_i, _vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _i, _vp, _sz,
                                          _vp, _i, _vp]),
+    "mxfp4_codes_bytes": (_sz, [_i64, _i64, _i]),
+    "mxfp4_scales_bytes": (_sz, [_i64, _i64, _i]),
+    "mxfp4_quantize": (_i, [_vp, _i, _i64, _i64, _i, _vp, _vp, _vp]),
+    "mxfp4_quantize_both": (_i, [_vp, _i, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "mxfp4_dequantize": (_i, [_vp, _vp, _i64, _i64, _i, _vp, _i, _vp]),
+    "mxfp4_gemm_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "mxfp4_gemm": (_i, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _f, _f, _vp, _vp, _i, _vp, _sz, _vp]),
+    "mxfp4_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "mxfp4_linear": (_i, [_vp, _i, _i64, _i64, _vp, _vp, _i64, _vp, _i, _vp, _vp, _vp, _sz, _vp]),
+    "mxfp4_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "mxfp4_linear_backward": (_i, [_vp, _i, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i,
+                                   _f, _vp, _sz, _vp]),
+    "ns_f16_workspace_bytes": (_sz, [_i, _vp, _vp]),
+    "ns_orthogonalize_f16": (_i, [_vp, _i, _i64, _i64, _vp, _i, _f, _vp, _i, _vp, _sz, _vp]),
+    "ns_orthogonalize_f16_grouped": (_i, [_i, _vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _i, _vp, _sz,
+                                          _vp]),
+    "ns_muon_step": (_i, [_i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _sz,
+                          _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -599,3 +626,305 @@ def ns_orthogonalize_grouped_on(Gs, coeffs, streams, clips=None, clip_quantile=0
                                                 len(streams), _stream(stream, dev)),
                "ns_orthogonalize_grouped_on")
     return outs
+
+
+# ----------------------------------------------------------------- MXFP4 --
+
+def _mx_panels(n):
+    return -(-n // 256)
+
+
+def _mx_buffers(rows, cols, codes, scales, dev):
+    """Codes and scales of an operand of `rows` rows blocked along `cols`."""
+    torch = _torch()
+    p = _mx_panels(cols)
+    if codes is None:
+        codes = torch.empty((p, rows, 128), dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty((p, rows, 8), dtype=torch.uint8, device=dev)
+    return codes, scales
+
+
+def _need_mx(codes, scales, name, rows, cols):
+    torch = _torch()
+    p = _mx_panels(cols)
+    _need(codes, f"{name} codes", (torch.uint8,), p * rows * 128)
+    _need(scales, f"{name} scales", (torch.uint8,), p * rows * 8)
+
+
+def _need_2d(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: a matrix is needed, got shape {tuple(t.shape)}")
+
+
+def mxfp4_quantize(x, axis=NVFP4_ROWS, codes=None, scales=None, stream=None):
+    """MXFP4 quantization of a 2-D float32/bfloat16 device tensor in one pass.
+
+    Returns (codes uint8 [panels][r][128], scales uint8 [panels][r][8]) of x
+    (NVFP4_ROWS, r = rows) or of x^T (NVFP4_COLS, r = columns), panels of 256
+    elements along the blocked axis.
+    """
+    torch = _torch()
+    _need_cuda(x)
+    _need_2d(x, "x")
+    rows, cols = x.shape
+    r, c = (rows, cols) if axis == NVFP4_ROWS else (cols, rows)
+    codes, scales = _mx_buffers(r, c, codes, scales, x.device)
+    _need_cuda(x, codes, scales)
+    _need_mx(codes, scales, "out", r, c)
+    with torch.cuda.device(x.device):
+        _check(_lib.mxfp4_quantize(_ptr(x), _dt(x), rows, cols, axis, _ptr(codes), _ptr(scales),
+                                   _stream(stream, x.device)), "mxfp4_quantize")
+    return codes, scales
+
+
+def mxfp4_quantize_both(x, along=None, down=None, stream=None):
+    """Both quantizations of x in one pass: ((codes, scales) of NVFP4_ROWS,
+    (codes, scales) of NVFP4_COLS)."""
+    torch = _torch()
+    _need_cuda(x)
+    _need_2d(x, "x")
+    rows, cols = x.shape
+    rc, rs = _mx_buffers(rows, cols, *(along or (None, None)), x.device)
+    cc, cs = _mx_buffers(cols, rows, *(down or (None, None)), x.device)
+    _need_cuda(x, rc, rs, cc, cs)
+    _need_mx(rc, rs, "along", rows, cols)
+    _need_mx(cc, cs, "down", cols, rows)
+    with torch.cuda.device(x.device):
+        _check(_lib.mxfp4_quantize_both(_ptr(x), _dt(x), rows, cols, _ptr(rc), _ptr(rs), _ptr(cc),
+                                        _ptr(cs), _stream(stream, x.device)), "mxfp4_quantize_both")
+    return (rc, rs), (cc, cs)
+
+
+def mxfp4_dequantize(codes, scales, rows, cols, axis=NVFP4_ROWS, out_dtype=NS_F32, out=None,
+                     stream=None):
+    """The values of an MXFP4 tensor, in the original rows x cols orientation."""
+    torch = _torch()
+    _need_cuda(codes, scales, out)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=_out_dtype(out_dtype), device=codes.device)
+    r, c = (rows, cols) if axis == NVFP4_ROWS else (cols, rows)
+    _need_mx(codes, scales, "in", r, c)
+    _need(out, "out", _floats(), rows * cols)
+    with torch.cuda.device(codes.device):
+        _check(_lib.mxfp4_dequantize(_ptr(codes), _ptr(scales), rows, cols, axis, _ptr(out), _dt(out),
+                                     _stream(stream, codes.device)), "mxfp4_dequantize")
+    return out
+
+
+def mxfp4_gemm_workspace_bytes(M, N, K):
+    return int(_lib.mxfp4_gemm_workspace_bytes(M, N, K))
+
+
+def _mx_workspace(need, workspace, dev):
+    torch = _torch()
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", (torch.uint8,), 0)
+    return workspace
+
+
+def mxfp4_gemm(p, q, M, N, K, alpha=1.0, beta=0.0, addend=None, out_dtype=NS_F32, out=None,
+               workspace=None, split=True, stream=None):
+    """out = beta*addend + alpha*(P Q^T); p, q = (codes, scales) along K.
+
+    With split=True (default) a workspace of mxfp4_gemm_workspace_bytes() is
+    allocated when none is given."""
+    torch = _torch()
+    (pc, ps), (qc, qs) = p, q
+    _need_cuda(pc, ps, qc, qs, addend, out)
+    dev = pc.device
+    if out is None:
+        out = torch.empty((M, N), dtype=_out_dtype(out_dtype), device=dev)
+    if workspace is not None or split:
+        workspace = _mx_workspace(mxfp4_gemm_workspace_bytes(M, N, K), workspace, dev)
+    _need_cuda(pc, workspace)
+    _need_mx(pc, ps, "p", M, K)
+    _need_mx(qc, qs, "q", N, K)
+    _need(out, "out", _floats(), M * N)
+    if float(beta) != 0.0:
+        _need(addend, "addend", (torch.float32,), M * N)
+    wsp, wsn = (_ptr(workspace), workspace.numel()) if workspace is not None else (_ptr(None), 0)
+    with torch.cuda.device(dev):
+        _check(_lib.mxfp4_gemm(_ptr(pc), _ptr(ps), _ptr(qc), _ptr(qs), M, N, K, float(alpha),
+                               float(beta), _ptr(addend), _ptr(out), _dt(out), wsp, wsn,
+                               _stream(stream, dev)), "mxfp4_gemm")
+    return out
+
+
+def mxfp4_linear_workspace_bytes(T, N, K):
+    return int(_lib.mxfp4_linear_workspace_bytes(T, N, K))
+
+
+def mxfp4_linear_backward_workspace_bytes(T, N, K):
+    return int(_lib.mxfp4_linear_backward_workspace_bytes(T, N, K))
+
+
+def mxfp4_linear(x, w, N, out=None, keep=False, kept=None, workspace=None, stream=None):
+    """y = Q(x) w^T for x [T][K] (float32/bfloat16) and MXFP4 weights w =
+    (codes, scales) of [N][K] along K; y takes x's dtype unless `out` is given.
+
+    keep=True (or a `kept` pair of buffers) also quantizes x along the tokens
+    and returns (y, kept), kept = (codes, scales) for mxfp4_linear_backward."""
+    torch = _torch()
+    wc, ws_ = w
+    _need_cuda(x, wc, ws_, out)
+    _need_2d(x, "x")
+    T, K = x.shape
+    dev = x.device
+    if out is None:
+        out = torch.empty((T, N), dtype=x.dtype, device=dev)
+    kc, ks = _mx_buffers(K, T, *(kept or (None, None)), dev) if keep or kept else (None, None)
+    workspace = _mx_workspace(mxfp4_linear_workspace_bytes(T, N, K), workspace, dev)
+    _need_cuda(x, kc, ks, workspace)
+    _need_mx(wc, ws_, "w", N, K)
+    _need(out, "out", _floats(), T * N)
+    if kc is not None:
+        _need_mx(kc, ks, "kept", K, T)
+    with torch.cuda.device(dev):
+        _check(_lib.mxfp4_linear(_ptr(x), _dt(x), T, K, _ptr(wc), _ptr(ws_), N, _ptr(out), _dt(out),
+                                 _ptr(kc), _ptr(ks), _ptr(workspace), workspace.numel(),
+                                 _stream(stream, dev)), "mxfp4_linear")
+    return (out, (kc, ks)) if kc is not None else out
+
+
+def mxfp4_linear_backward(dy, wt, kept, K, dx=None, dw=None, need_dx=True, need_dw=True, beta=0.0,
+                          workspace=None, stream=None):
+    """Gradients of mxfp4_linear for dy [T][N]: (dx [T][K], dw [N][K]).
+
+    wt = (codes, scales) of the weights along N (NVFP4_COLS of [N][K]), kept as
+    returned by mxfp4_linear.  need_dx / need_dw False leaves one out (None is
+    returned in its place).  dw = beta * dw + gradient (beta != 0 needs a
+    float32 `dw`); new tensors take dy's dtype."""
+    torch = _torch()
+    _need_cuda(dy, dx, dw)
+    _need_2d(dy, "dy")
+    T, N = dy.shape
+    dev = dy.device
+    if need_dx and dx is None:
+        dx = torch.empty((T, K), dtype=dy.dtype, device=dev)
+    if need_dw and dw is None:
+        if float(beta) != 0.0:
+            raise ValueError("beta != 0 adds to a dw that is given")
+        dw = torch.empty((N, K), dtype=dy.dtype, device=dev)
+    dx, dw = dx if need_dx else None, dw if need_dw else None
+    (wc, ws_), (kc, ks) = wt if need_dx else (None, None), kept if need_dw else (None, None)
+    workspace = _mx_workspace(mxfp4_linear_backward_workspace_bytes(T, N, K), workspace, dev)
+    _need_cuda(dy, wc, ws_, kc, ks, workspace)
+    if need_dx:
+        _need_mx(wc, ws_, "wt", K, N)
+        _need(dx, "dx", _floats(), T * K)
+    if need_dw:
+        _need_mx(kc, ks, "kept", K, T)
+        _need(dw, "dw", _floats(), N * K)
+    with torch.cuda.device(dev):
+        _check(_lib.mxfp4_linear_backward(_ptr(dy), _dt(dy), T, N, K, _ptr(wc), _ptr(ws_), _ptr(kc),
+                                          _ptr(ks), _ptr(dx), _dt(dx) if need_dx else NS_F32, _ptr(dw),
+                                          _dt(dw) if need_dw else NS_F32, float(beta),
+                                          _ptr(workspace), workspace.numel(), _stream(stream, dev)),
+               "mxfp4_linear_backward")
+    return dx, dw
+
+
+# ---------------------------------------------- 16-bit Newton–Schulz, Muon --
+
+def _shape_arrays(shapes):
+    cnt = len(shapes)
+    return ((ctypes.c_int64 * cnt)(*[s[0] for s in shapes]),
+            (ctypes.c_int64 * cnt)(*[s[1] for s in shapes]))
+
+
+def ns_f16_workspace_bytes(shapes):
+    """Workspace of the 16-bit calls for a list of (m, n)."""
+    ms, ns_ = _shape_arrays(shapes)
+    return int(_lib.ns_f16_workspace_bytes(len(shapes), ms, ns_))
+
+
+def _pointers(ts):
+    return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
+
+
+def ns_orthogonalize_f16(G, coeffs, clip=float("inf"), out_dtype=NS_F32, out=None, workspace=None,
+                         stream=None):
+    """k Newton–Schulz steps with f16 operands on one m x n float32/bfloat16
+    matrix of any shape."""
+    torch = _torch()
+    _need_cuda(G, out)
+    _need_2d(G, "G")
+    m, n = G.shape
+    if out is None:
+        out = torch.empty((m, n), dtype=_out_dtype(out_dtype), device=G.device)
+    workspace = _mx_workspace(ns_f16_workspace_bytes([(m, n)]), workspace, G.device)
+    _need_ns(G, out, workspace)
+    carr, k = _coeff_array(coeffs)
+    with torch.cuda.device(G.device):
+        _check(_lib.ns_orthogonalize_f16(_ptr(G), _dt(G), m, n, carr, k, float(clip), _ptr(out),
+                                         _dt(out), _ptr(workspace), workspace.numel(),
+                                         _stream(stream, G.device)), "ns_orthogonalize_f16")
+    return out
+
+
+def ns_orthogonalize_f16_grouped(Gs, coeffs, clips=None, out_dtype=NS_F32, outs=None,
+                                 workspace=None, stream=None):
+    """ns_orthogonalize_f16 over a list of matrices; those of one shape run as
+    one batch."""
+    torch = _torch()
+    cnt = len(Gs)
+    _need_cuda(*Gs)
+    dt = _dt(Gs[0])
+    if any(_dt(g) != dt for g in Gs):
+        raise TypeError("all inputs must share one dtype")
+    for i, g in enumerate(Gs):
+        _need_2d(g, f"Gs[{i}]")
+    shapes = [tuple(g.shape) for g in Gs]
+    dev = Gs[0].device
+    if outs is None:
+        outs = [torch.empty(s, dtype=_out_dtype(out_dtype), device=dev) for s in shapes]
+    workspace = _mx_workspace(ns_f16_workspace_bytes(shapes), workspace, dev)
+    _need_group(Gs, outs, workspace)
+    if clips is not None and len(clips) != cnt:
+        raise ValueError("one clip per matrix")
+    ms, ns_ = _shape_arrays(shapes)
+    cl = (ctypes.c_float * cnt)(*[float(c) for c in clips]) if clips is not None else None
+    carr, k = _coeff_array(coeffs)
+    with torch.cuda.device(dev):
+        _check(_lib.ns_orthogonalize_f16_grouped(cnt, _pointers(Gs), ms, ns_, dt, carr, k, cl,
+                                                 _pointers(outs), _dt(outs[0]), _ptr(workspace),
+                                                 workspace.numel(), _stream(stream, dev)),
+               "ns_orthogonalize_f16_grouped")
+    return outs
+
+
+def ns_muon_step(Ws, Ms, Gs, coeffs, lr, momentum=0.95, weight_decay=0.0, nesterov=True, scales=None,
+                 workspace=None, stream=None):
+    """One Muon step, in place on the weights Ws and momenta Ms (lists of
+    matrices, each list of one dtype): M <- momentum M + G; U = G + momentum M
+    (nesterov) or M; W <- (1 - lr weight_decay) W - lr scale NS(U)."""
+    torch = _torch()
+    cnt = len(Ws)
+    if cnt == 0 or len(Ms) != cnt or len(Gs) != cnt:
+        raise ValueError("one momentum and one gradient per weight matrix, at least one")
+    _need_cuda(*Ws, *Ms, *Gs)
+    shapes = []
+    for i, (w, m, g) in enumerate(zip(Ws, Ms, Gs)):
+        _need_2d(w, f"Ws[{i}]")
+        shapes.append(tuple(w.shape))
+        for t, first, name in ((w, Ws[0], "Ws"), (m, Ms[0], "Ms"), (g, Gs[0], "Gs")):
+            _need_shape(t, f"{name}[{i}]", w.shape)
+            if t.dtype != first.dtype:
+                raise TypeError(f"{name}: one dtype for all matrices")
+    if scales is not None and len(scales) != cnt:
+        raise ValueError("one scale per matrix")
+    dev = Ws[0].device
+    workspace = _mx_workspace(ns_f16_workspace_bytes(shapes), workspace, dev)
+    _need_cuda(Ws[0], workspace)
+    ms, ns_ = _shape_arrays(shapes)
+    sc = (ctypes.c_float * cnt)(*[float(c) for c in scales]) if scales is not None else None
+    carr, k = _coeff_array(coeffs)
+    opt = NsMuonOptions(float(lr), float(momentum), float(weight_decay), 1 if nesterov else 0)
+    with torch.cuda.device(dev):
+        _check(_lib.ns_muon_step(cnt, _pointers(Ws), _dt(Ws[0]), _pointers(Ms), _dt(Ms[0]),
+                                 _pointers(Gs), _dt(Gs[0]), ms, ns_, carr, k, ctypes.byref(opt), sc,
+                                 _ptr(workspace), workspace.numel(), _stream(stream, dev)),
+               "ns_muon_step")
+    return Ws
