@@ -202,7 +202,9 @@ __device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t
   asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
 }
 
-__device__ __forceinline__ int swizzle(int r) { return (r ^ (r >> 3)) & 7; }
+// Depends on r % 32 alone, so that a fragment's LDS address is one per-lane
+// offset for each step plus a constant for its 32-row block.
+__device__ __forceinline__ int swizzle(int r) { return (r ^ ((r & 31) >> 3)) & 7; }
 
 // Byte offsets of a lane's loads inside a panel.  Rows past the operand's end
 // read its last row: they feed only outputs that the epilogue does not write.
@@ -234,24 +236,32 @@ __device__ __forceinline__ void init_src(const Args& a, int m0, int n0, int wave
   }
 }
 
-// A wave's loads never straddle the operands: B rows are a multiple of a
-// wave's share.
+// Load number k of a wave's share of a stage.  A share never straddles the
+// operands: B rows are a multiple of it.
 template <class C, bool FP4>
-__device__ __forceinline__ void issue(const Args& a, const Src<C, FP4>& s, int g, uint32_t stage, int wave) {
-  const bool isP = wave * C::kCodeLoads * 8 < C::B;
-  const uint8_t* base = isP ? a.p.data + (int64_t)g * a.p.rows * 128 : a.q.data + (int64_t)g * a.q.rows * 128;
-#pragma unroll
-  for (int i = 0; i < C::kCodeLoads; ++i)
-    dma16(base, s.code[i], stage + (uint32_t)(wave * C::kCodeLoads + i) * 1024u);
-  if constexpr (FP4) {
-    const uint8_t* sb = isP ? a.p.scales + (int64_t)g * a.p.rows * 8 : a.q.scales + (int64_t)g * a.q.rows * 8;
-#pragma unroll
-    for (int i = 0; i < C::kScaleLoads; ++i)
-      dma4(sb, s.scale[i], stage + (uint32_t)C::kCodeBytes + (uint32_t)(wave * C::kScaleLoads + i) * 256u);
-  }
-}
+struct Issue {
+  static constexpr int kLoads = C::kCodeLoads + (FP4 ? C::kScaleLoads : 0);
+  const uint8_t *data, *scales;        // the wave's operand
+  int64_t rows;
+  uint32_t code0, scale0;              // LDS offsets of the wave's share in a stage
 
-// ---- multiply one stage --------------------------------------------------------
+  __device__ __forceinline__ Issue(const Args& a, int wave) {
+    const bool isP = wave * C::kCodeLoads * 8 < C::B;
+    data = isP ? a.p.data : a.q.data;
+    scales = isP ? a.p.scales : a.q.scales;
+    rows = isP ? a.p.rows : a.q.rows;
+    code0 = (uint32_t)(wave * C::kCodeLoads) * 1024u;
+    scale0 = (uint32_t)C::kCodeBytes + (uint32_t)(wave * C::kScaleLoads) * 256u;
+  }
+  __device__ __forceinline__ void load(const Src<C, FP4>& s, int g, uint32_t stage, int k) const {
+    if (k < C::kCodeLoads)
+      dma16(data + (int64_t)g * rows * 128, s.code[k], stage + code0 + 1024u * k);
+    else if constexpr (FP4)
+      dma4(scales + (int64_t)g * rows * 8, s.scale[k - C::kCodeLoads], stage + scale0 + 256u * (k - C::kCodeLoads));
+  }
+};
+
+// ---- multiply ------------------------------------------------------------------
 template <int S>
 __device__ __forceinline__ floatx16 mfma_fp4(intx4 a, intx4 b, floatx16 c, uint32_t sa, uint32_t sb) {
   const intx8 x = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, y = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
@@ -262,49 +272,55 @@ __device__ __forceinline__ floatx16 mfma_f16(intx4 a, intx4 b, floatx16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(x.h, y.h, c, 0, 0, 0);
 }
 
-template <class C, bool FP4, int S>
-__device__ __forceinline__ void step(const uint8_t* st, int wm, int wn, int lane, const uint32_t (&sp)[C::FM],
-                                     const uint32_t (&sq)[C::FN], floatx16 (&acc)[C::FM][C::FN]) {
-  const int r = lane & 31, h = lane >> 5;
-  // swizzle(32 k + r) == swizzle(r) ^ (4 k & 7): fold the block's part in
-  intx4 av[C::FM], bv[C::FN];
-#pragma unroll
-  for (int i = 0; i < C::FM; ++i) {
-    const int row = (wm * C::FM + i) * 32 + r;
-    av[i] = *reinterpret_cast<const intx4*>(st + row * 128 + 16 * ((4 * h + S) ^ swizzle(row)));
-  }
-#pragma unroll
-  for (int j = 0; j < C::FN; ++j) {
-    const int row = C::B + (wn * C::FN + j) * 32 + r;
-    bv[j] = *reinterpret_cast<const intx4*>(st + row * 128 + 16 * ((4 * h + S) ^ swizzle(row)));
-  }
+// One step's operands of a wave, and a stage's scales (four steps).
+template <class C>
+struct Frags {
+  intx4 q[C::FN], p[C::FM];
+};
+template <class C>
+struct Scales {
+  uint32_t q[C::FN], p[C::FM];
+};
+
+// Read number k of a step: Q's fragments, then P's, in the order of use.
+template <class C>
+__device__ __forceinline__ void read_frag(const uint8_t* st, uint32_t off, int wm, int wn, int k, Frags<C>& f) {
+  if (k < C::FN)
+    f.q[k] = *reinterpret_cast<const intx4*>(st + off + (C::B / 32 + wn * C::FN + k) * 4096);
+  else
+    f.p[k - C::FN] = *reinterpret_cast<const intx4*>(st + off + (wm * C::FM + k - C::FN) * 4096);
+}
+template <class C>
+__device__ __forceinline__ void read_scale(const uint8_t* st, uint32_t off, int wm, int wn, int k, Scales<C>& f) {
+  st += C::kCodeBytes;
+  if (k < C::FN)
+    f.q[k] = *reinterpret_cast<const uint32_t*>(st + off + (C::B / 32 + wn * C::FN + k) * 256);
+  else
+    f.p[k - C::FN] = *reinterpret_cast<const uint32_t*>(st + off + (wm * C::FM + k - C::FN) * 256);
+}
+
+// One step's MFMAs; `between(k)` puts memory operations behind the k-th, and
+// the compiler keeps this order: a step's fragments are read while the step
+// before multiplies.
+template <class C, bool FP4, int S, class F>
+__device__ __forceinline__ void step(const Frags<C>& f, const Scales<C>& sc, floatx16 (&acc)[C::FM][C::FN],
+                                     F&& between) {
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
       if constexpr (FP4)
-        acc[i][j] = mfma_fp4<S>(av[i], bv[j], acc[i][j], sp[i], sq[j]);
+        acc[i][j] = mfma_fp4<S>(f.p[i], f.q[j], acc[i][j], sc.p[i], sc.q[j]);
       else
-        acc[i][j] = mfma_f16(av[i], bv[j], acc[i][j]);
+        acc[i][j] = mfma_f16(f.p[i], f.q[j], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+      between(i * C::FN + j);
+      __builtin_amdgcn_sched_barrier(0);
     }
 }
 
-template <class C, bool FP4>
-__device__ __forceinline__ void multiply(const uint8_t* st, int wm, int wn, int lane, floatx16 (&acc)[C::FM][C::FN]) {
-  uint32_t sp[C::FM], sq[C::FN];
-  const int r = lane & 31, h = lane >> 5;
-#pragma unroll
-  for (int i = 0; i < C::FM; ++i)
-    sp[i] = FP4 ? *reinterpret_cast<const uint32_t*>(st + C::kCodeBytes + ((wm * C::FM + i) * 32 + r) * 8 + 4 * h) : 0u;
-#pragma unroll
-  for (int j = 0; j < C::FN; ++j)
-    sq[j] = FP4 ? *reinterpret_cast<const uint32_t*>(st + C::kCodeBytes + (C::B + (wn * C::FN + j) * 32 + r) * 8 + 4 * h)
-                : 0u;
-  step<C, FP4, 0>(st, wm, wn, lane, sp, sq, acc);
-  step<C, FP4, 1>(st, wm, wn, lane, sp, sq, acc);
-  step<C, FP4, 2>(st, wm, wn, lane, sp, sq, acc);
-  step<C, FP4, 3>(st, wm, wn, lane, sp, sq, acc);
-}
+// Part k of n of the work 0 .. total - 1.
+__device__ __forceinline__ constexpr int share(int total, int k, int n) { return total * k / n; }
 
 // ---- epilogues -----------------------------------------------------------------
 // acc[i][j][4 q + t] of a lane is row (wm FM + i) 32 + 8 q + 4 (lane / 32) + t,
@@ -344,8 +360,26 @@ struct Stage16 {
   static constexpr int kBytes = C::B * kPitch;
 };
 
-template <class C, class F>
-__device__ __forceinline__ void stage_rows(uint8_t* lds, int wm, int wn, int lane, F&& word) {
+template <class C>
+struct Words {
+  uint32_t w[C::FM][C::FN][4][2];
+};
+template <class C, Dt T>
+__device__ __forceinline__ void pack_tile(const floatx16 (&acc)[C::FM][C::FN], Words<C>& w) {
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        w.w[i][j][q >> 1][q & 1] = T == Dt::BF16 ? mx::pack_bf16(acc[i][j][2 * q], acc[i][j][2 * q + 1])
+                                                 : pack_f16(acc[i][j][2 * q], acc[i][j][2 * q + 1]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+template <class C>
+__device__ __forceinline__ void stage_rows(uint8_t* lds, int wm, int wn, int lane, const Words<C>& w) {
   const int h = lane >> 5, c = lane & 31;
   const bool odd = lane & 1;
 #pragma unroll
@@ -355,7 +389,7 @@ __device__ __forceinline__ void stage_rows(uint8_t* lds, int wm, int wn, int lan
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t first, second;
-        pair_columns(word(i, j, q, 0), word(i, j, q, 1), odd, first, second);
+        pair_columns(w.w[i][j][q][0], w.w[i][j][q][1], odd, first, second);
         const int row = (wm * C::FM + i) * 32 + 8 * q + 4 * h + (odd ? 2 : 0);
         const int col = (wn * C::FN + j) * 32 + (c & ~1);
         *reinterpret_cast<uint32_t*>(lds + row * Stage16<C>::kPitch + col * 2) = first;
@@ -364,8 +398,8 @@ __device__ __forceinline__ void stage_rows(uint8_t* lds, int wm, int wn, int lan
 }
 
 // The transposed tile: row = the tile's column.
-template <class C, class F>
-__device__ __forceinline__ void stage_cols(uint8_t* lds, int wm, int wn, int lane, F&& word) {
+template <class C>
+__device__ __forceinline__ void stage_cols(uint8_t* lds, int wm, int wn, int lane, const Words<C>& w) {
   const int h = lane >> 5, c = lane & 31;
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
@@ -375,7 +409,7 @@ __device__ __forceinline__ void stage_cols(uint8_t* lds, int wm, int wn, int lan
       for (int q = 0; q < 4; ++q) {
         const int row = (wn * C::FN + j) * 32 + c, col = (wm * C::FM + i) * 32 + 8 * q + 4 * h;
         *reinterpret_cast<uint2*>(lds + row * Stage16<C>::kPitch + col * 2) =
-            make_uint2(word(i, j, q, 0), word(i, j, q, 1));
+            make_uint2(w.w[i][j][q][0], w.w[i][j][q][1]);
       }
 }
 
@@ -429,11 +463,10 @@ __device__ __forceinline__ void epilogue(const Args& a, floatx16 (&acc)[C::FM][C
           }
         }
     if constexpr (kStaged) {
-      auto word = [&](int i, int j, int q, int p) {
-        return mx::pack_bf16(acc[i][j][4 * q + 2 * p], acc[i][j][4 * q + 2 * p + 1]);
-      };
+      Words<C> w;
+      pack_tile<C, Dt::BF16>(acc, w);
       lds_barrier();
-      stage_rows<C>(lds, wm, wn, lane, word);
+      stage_rows<C>(lds, wm, wn, lane, w);
       lds_barrier();
       uint16_t* out = reinterpret_cast<uint16_t*>(a.out);
       const bool vec = a.N % 8 == 0;
@@ -441,12 +474,12 @@ __device__ __forceinline__ void epilogue(const Args& a, floatx16 (&acc)[C::FM][C
         const int ch = k % (C::B / 8), r = k / (C::B / 8);
         const int row = m0 + r, col = n0 + 8 * ch;
         if (row >= a.M || col >= a.N) continue;
-        const uint4 w = *reinterpret_cast<const uint4*>(lds + r * Stage16<C>::kPitch + 16 * ch);
+        const uint4 v = *reinterpret_cast<const uint4*>(lds + r * Stage16<C>::kPitch + 16 * ch);
         uint16_t* o = out + (int64_t)row * a.N + col;
         if (vec) {
-          *reinterpret_cast<uint4*>(o) = w;
+          *reinterpret_cast<uint4*>(o) = v;
         } else {
-          const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int t = 0; t < 8; ++t)
             if (col + t < a.N) o[t] = (uint16_t)(e[t >> 1] >> (16 * (t & 1)));
@@ -472,6 +505,7 @@ __device__ __forceinline__ void epilogue(const Args& a, floatx16 (&acc)[C::FM][C
               float v = fmaf(a.cc, acc[i][j][4 * q + t], a.cb * av[t]);
               acc[i][j][4 * q + t] = row + t == col ? v + a.ca : v;
             }
+            if (q == 3) __builtin_amdgcn_sched_barrier(0);
           }
     } else {
 #pragma unroll
@@ -481,20 +515,19 @@ __device__ __forceinline__ void epilogue(const Args& a, floatx16 (&acc)[C::FM][C
 #pragma unroll
           for (int r = 0; r < 16; ++r) acc[i][j][r] *= alpha;
     }
-    auto word = [&](int i, int j, int q, int p) {
-      return pack_f16(acc[i][j][4 * q + 2 * p], acc[i][j][4 * q + 2 * p + 1]);
-    };
+    Words<C> w;
+    pack_tile<C, Dt::F32>(acc, w);                       // f16
     constexpr bool kIter = EP == PanelEp::Iter;
     uint8_t* tdst = kIter ? a.out_t : a.out;
     lds_barrier();
-    stage_cols<C>(lds, wm, wn, lane, word);
+    stage_cols<C>(lds, wm, wn, lane, w);
     lds_barrier();
     // the transpose: rows n0 .., columns m0 ..; a symmetric product's mirror
     // (a diagonal tile is its own)
     store_panels<C>(lds, tdst, n0, a.N, m0, a.M);
     if (kIter || I != J) {
       lds_barrier();
-      stage_rows<C>(lds, wm, wn, lane, word);
+      stage_rows<C>(lds, wm, wn, lane, w);
       lds_barrier();
       store_panels<C>(lds, a.out, m0, a.M, n0, a.N);
     }
@@ -536,26 +569,76 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks* C::kWaves / 4) void panel_
 
   Src<C, FP4> src;
   init_src<C, FP4>(a, I * C::B, J * C::B, wave, lane, src);
+  const Issue<C, FP4> dma(a, wave);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
-  constexpr int kLoads = C::kCodeLoads + (FP4 ? C::kScaleLoads : 0);
+  constexpr int kLoads = Issue<C, FP4>::kLoads, kReads = C::FM + C::FN, kMul = C::FM * C::FN;
+  uint32_t off[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    off[s] = (uint32_t)((lane & 31) * 128 + 16 * ((4 * (lane >> 5) + s) ^ swizzle(lane & 31)));
+  const uint32_t soff = (uint32_t)((lane & 31) * 8 + 4 * (lane >> 5));
+  Frags<C> f0, f1;
+  Scales<C> sc;
+  auto wait_loads = [&] { asm volatile("s_waitcnt vmcnt(%0)" ::"n"((C::NST - 2) * kLoads) : "memory"); };
+  auto read_first = [&](const uint8_t* st) {
+#pragma unroll
+    for (int k = 0; k < kReads; ++k) {
+      if constexpr (FP4) read_scale<C>(st, soff, wm, wn, k, sc);
+      read_frag<C>(st, off[0], wm, wn, k, f0);
+    }
+  };
+  // Stages g0 .. g0 + NST - 2 in flight, then always one more: a panel past
+  // the last is the last again, into a buffer that nothing reads.
+  auto panel = [&](int g) { return g < g1 ? g : g1 - 1; };
 #pragma unroll
   for (int s = 0; s < C::NST - 1; ++s)
-    if (g0 + s < g1) issue<C, FP4>(a, src, g0 + s, lds0 + s * kStage, wave);
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) dma.load(src, panel(g0 + s), lds0 + s * kStage, k);
+  wait_loads();
+  __builtin_amdgcn_s_barrier();
+  read_first(smem);
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) dma.load(src, panel(g0 + C::NST - 1), lds0 + (C::NST - 1) * kStage, k);
+
   int cur = 0;
-  for (int g = g0; g < g1; ++g) {
-    // this wave's loads of stage g (later ones stay in flight), then every
-    // wave's; the barrier also retires the reads of the buffer loaded next
-    if (g + C::NST - 2 < g1)
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"((C::NST - 2) * kLoads) : "memory");
-    else
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    int nxt = cur + C::NST - 1;
-    nxt = nxt >= C::NST ? nxt - C::NST : nxt;
-    if (g + C::NST - 1 < g1) issue<C, FP4>(a, src, g + C::NST - 1, lds0 + nxt * kStage, wave);
-    multiply<C, FP4>(smem + cur * kStage, wm, wn, lane, acc);
+  auto first_three = [&](const uint8_t* st) {
+    auto ahead = [&](int s, Frags<C>& f) {
+      return [&, s](int k) {
+#pragma unroll
+        for (int r = share(kReads, k, kMul); r < share(kReads, k + 1, kMul); ++r)
+          read_frag<C>(st, off[s], wm, wn, r, f);
+      };
+    };
+    step<C, FP4, 0>(f0, sc, acc, ahead(1, f1));
+    step<C, FP4, 1>(f1, sc, acc, ahead(2, f0));
+    step<C, FP4, 2>(f0, sc, acc, ahead(3, f1));
+  };
+  for (int g = g0; g + 1 < g1; ++g) {
+    first_three(smem + cur * kStage);
+    // every read of this stage has returned: its buffer is free once all
+    // waves are here, and the next stage's loads have landed
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    wait_loads();
+    __builtin_amdgcn_s_barrier();
+    const uint32_t freed = lds0 + cur * kStage;
     cur = cur + 1 == C::NST ? 0 : cur + 1;
+    const uint8_t* st = smem + cur * kStage;
+    const int gn = panel(g + C::NST);
+    Scales<C> nsc;
+    step<C, FP4, 3>(f1, sc, acc, [&](int k) {
+#pragma unroll
+      for (int r = share(kReads, k, kMul); r < share(kReads, k + 1, kMul); ++r) {
+        if constexpr (FP4) read_scale<C>(st, soff, wm, wn, r, nsc);
+        read_frag<C>(st, off[0], wm, wn, r, f0);
+      }
+#pragma unroll
+      for (int r = share(kLoads, k, kMul); r < share(kLoads, k + 1, kMul); ++r) dma.load(src, gn, freed, r);
+    });
+    if constexpr (FP4) sc = nsc;
   }
+  first_three(smem + cur * kStage);
+  step<C, FP4, 3>(f1, sc, acc, [](int) {});
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // the loads past the end, before LDS serves the epilogue
 
   if (un.split >= 0) {
     float* part = a.partials + ((size_t)un.split * a.parts + un.part) * C::kAcc * C::kThreads;
