@@ -125,7 +125,7 @@ ns_status mxfp4_gemm(const uint8_t* codes_p, const uint8_t* scales_p, const uint
       A{beta != 0.0f && !in_place ? addend : nullptr, mn * sizeof(float)}, W{ws, ws ? ws_bytes : 0};
   if (hits(O, {P, PS, Q, QS, A, W}) || hits(W, {P, PS, Q, QS, A})) return NS_ERR_ARG;
   NS_TRY(nvfp4::launch_panel(mx_product(codes_p, scales_p, codes_q, scales_q, M, N, K, alpha, beta, addend, out, (Dt)ot),
-                             plan, true, ws, 0, as_stream(stream)));
+                             plan, true, ws, as_stream(stream)));
   return NS_OK;
 }
 
@@ -194,7 +194,7 @@ ns_status mxfp4_linear(const void* x, ns_dtype xt, int64_t T, int64_t K, const u
   NS_TRY(nvfp4::launch_mx_quantize(x, (Dt)xt, T, K, kept_codes ? nvfp4::kMxRows | nvfp4::kMxCols : nvfp4::kMxRows,
                                    b + L.c0, b + L.s0, kept_codes, kept_scales, s));
   NS_TRY(nvfp4::launch_panel(mx_product(b + L.c0, b + L.s0, w_codes, w_scales, T, N, K, 1.0f, 0.0f, nullptr, y, (Dt)yt),
-                             mx_plan(T, N, K, true), true, b + L.part, 0, s));
+                             mx_plan(T, N, K, true), true, b + L.part, s));
   return NS_OK;
 }
 
@@ -229,11 +229,11 @@ ns_status mxfp4_linear_backward(const void* dy, ns_dtype dyt, int64_t T, int64_t
                                    b + L.s0, b + L.c1, b + L.s1, s));
   if (dx)
     NS_TRY(nvfp4::launch_panel(mx_product(b + L.c0, b + L.s0, wt_codes, wt_scales, T, K, N, 1.0f, 0.0f, nullptr, dx, (Dt)dxt),
-                               mx_plan(T, K, N, true), true, b + L.part, 0, s));
+                               mx_plan(T, K, N, true), true, b + L.part, s));
   if (dw)
     NS_TRY(nvfp4::launch_panel(mx_product(b + L.c1, b + L.s1, kept_codes, kept_scales, N, K, T, 1.0f, beta,
                                           static_cast<const float*>(dw), dw, (Dt)dwt),
-                               mx_plan(N, K, T, true), true, b + L.part, 0, s));
+                               mx_plan(N, K, T, true), true, b + L.part, s));
   return NS_OK;
 }
 
@@ -250,7 +250,8 @@ constexpr int64_t kMaxElems16 = (int64_t)1 << 31;
 // one while it writes the other), A and B, partials and scalars.
 struct Ns16Layout {
   int64_t mp, np;
-  size_t x, xt[2], a, b, part, fac, split, total;
+  size_t x, xt[2], a, b, part, fac, total;   // of one matrix
+  size_t split;                              // the batch's split tiles' partials, behind its matrices
   PanelPlan gram, poly, iter, last;
 };
 
@@ -274,8 +275,8 @@ Ns16Layout ns16_layout(int64_t m, int64_t n, int batch) {
   L.b = take((size_t)(L.mp * L.mp) * 2);
   L.part = take(nvfp4::kNs16Parts * sizeof(double));
   L.fac = take(2 * sizeof(float));
-  L.split = take(part);
   L.total = o;
+  L.split = align_up(part);
   return L;
 }
 
@@ -321,7 +322,7 @@ hipError_t ns16_batch(const nvfp4::Ns16Inputs& in, void* const* out, const float
     g.alpha = 1.0f / (nvfp4::kNs16Scale * nvfp4::kNs16Scale);
     g.dalpha = it == 0 ? fac + 1 : nullptr;
     g.out = A;
-    e = nvfp4::launch_panel(g, L.gram, false, ws + L.split, stride, s);
+    e = nvfp4::launch_panel(g, L.gram, false, ws + (size_t)batch * L.total, s);
     if (e != hipSuccess) return e;
     g.p = g.q = oa;
     g.panels = L.mp / 64;
@@ -333,7 +334,7 @@ hipError_t ns16_batch(const nvfp4::Ns16Inputs& in, void* const* out, const float
     g.cb = c.coeffs[3 * it + 1];
     g.cc = c.coeffs[3 * it + 2];
     g.out = B;
-    e = nvfp4::launch_panel(g, L.poly, false, ws + L.split, stride, s);
+    e = nvfp4::launch_panel(g, L.poly, false, ws + (size_t)batch * L.total, s);
     if (e != hipSuccess) return e;
     PanelProblem u;
     u.batch = batch;
@@ -348,7 +349,7 @@ hipError_t ns16_batch(const nvfp4::Ns16Inputs& in, void* const* out, const float
       u.ep = PanelEp::Iter;
       u.out = X;
       u.out_t = XN;
-      e = nvfp4::launch_panel(u, L.iter, false, ws + L.split, stride, s);
+      e = nvfp4::launch_panel(u, L.iter, false, ws + (size_t)batch * L.total, s);
     } else {
       // rows of the output are rows of X, or of its transpose when m > n
       u.p = tr ? oxt : ob;
@@ -361,7 +362,7 @@ hipError_t ns16_batch(const nvfp4::Ns16Inputs& in, void* const* out, const float
       u.ot = c.ot;
       u.out_each = out;
       u.alpha_each = alpha_each;
-      e = nvfp4::launch_panel(u, L.last, false, ws + L.split, stride, s);
+      e = nvfp4::launch_panel(u, L.last, false, ws + (size_t)batch * L.total, s);
     }
     if (e != hipSuccess) return e;
   }
@@ -441,7 +442,8 @@ size_t ns_f16_workspace_bytes(int count, const int64_t* m, const int64_t* n) {
   if (count <= 0 || !m || !n || ns16_shapes(count, m, n) != NS_OK) return 0;
   size_t most = 0;
   (void)for_batches(count, m, n, [&](const Ns16Batch& b) {
-    const size_t need = (size_t)b.count * ns16_layout(m[b.index[0]], n[b.index[0]], b.count).total;
+    const Ns16Layout L = ns16_layout(m[b.index[0]], n[b.index[0]], b.count);
+    const size_t need = (size_t)b.count * L.total + L.split;
     most = need > most ? need : most;
     return NS_OK;
   });

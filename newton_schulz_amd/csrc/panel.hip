@@ -13,12 +13,18 @@
 // lines into LDS (eight rows an instruction; a tile's panel is one contiguous
 // run of memory), chunk c of row r at position c ^ swizzle(r), so that 32
 // lanes reading one chunk of 32 rows hit distinct banks.  MXFP4 scales come
-// by the dword, one for a lane's four steps.  Stages alternate between two
-// buffers: while one is multiplied the next loads.
+// by the dword, one for a lane's four steps.
 //
-// Tiles left over after an equal number per CU are split along K into parts
-// whose FP32 partials a second kernel sums in part order.
+// Workgroups stay for as many tiles as there are per slot (a slot is one
+// resident workgroup).  The stages of a workgroup's tiles form one stream
+// through a ring of buffers, so that a tile's first panels load while the
+// tile before still multiplies and leaves; a tile leaves through 2.5 KB of
+// LDS of each wave's own, without a barrier.
+//
+// Tiles left over after an equal number per slot are split along K into
+// parts whose FP32 partials a second kernel sums in part order.
 #include <cstddef>
+#include <cstdlib>
 
 #include "mxfp4_device.hpp"
 #include "panel.hpp"
@@ -35,6 +41,8 @@ typedef _Float16 halfx2 __attribute__((ext_vector_type(2)));
 constexpr int kXcds = 8;          // workgroups go round-robin to 8 XCDs
 constexpr int kCusPerXcd = 32;
 
+constexpr int kScratch = 2560;    // bytes of LDS a wave's epilogue uses
+
 template <int B_, int WM_, int WN_, int NST_, int BLOCKS_>
 struct Tile {
   static constexpr int B = B_;                 // rows and columns
@@ -49,15 +57,17 @@ struct Tile {
   static constexpr int kAcc = FM * FN * 16;
 };
 using Tile256 = Tile<256, 2, 4, 2, 1>;
+using Tile192 = Tile<192, 2, 2, 2, 1>;
 using Tile128 = Tile<128, 2, 2, 2, 2>;
-using Tile64 = Tile<64, 2, 2, 3, 3>;
+using Tile64 = Tile<64, 2, 2, 3, 2>;
 
 struct Args {
   PanelOperand p, q;
   int M, N, panels;
-  int TM, TN, tiles, parts, slots, sym;
+  int TM, TN, tiles, batch, slots, sym;          // slots: per XCD
+  int parts;
+  uint32_t parts_inv;           // 2^16 / parts, rounded up: exact below 2^16 / parts units
   float* partials;
-  int64_t part_stride;          // bytes between the problems' partials
   // epilogue
   float alpha, beta, ca, cb, cc;
   const float* dalpha;
@@ -68,23 +78,31 @@ struct Args {
   int64_t bstride;
 };
 
-// Row-major outputs of a batch, one by one (n > 0).  The first argument of
-// the kernels, so that it sits at the start of the kernel-argument segment:
-// the entry of problem y is then two scalar loads from there.
+// The run of tiles of one XCD (see "schedule").
+struct alignas(16) Run {
+  int t0, whole, units, split0;   // first tile; whole units; units in all; split tiles of the runs before
+};
+
+// What the kernels look up by index: the runs, and the row-major outputs of a
+// batch with their factors on alpha (n > 0).  The first argument, so that it
+// sits at the start of the kernel-argument segment: an entry is then a scalar
+// load from there.
 struct Each {
+  Run run[kXcds];
   int n;
   float alpha[kMaxPanelBatch];
   void* out[kMaxPanelBatch];
 };
-static_assert(offsetof(Each, alpha) == 4 && offsetof(Each, out) == 8 + 4 * kMaxPanelBatch, "Each layout");
 
-__device__ __forceinline__ void pick_output(Args& a, int y) {
+template <class T>
+__device__ __forceinline__ T looked_up(size_t offset, int i) {
   typedef const __attribute__((address_space(4))) uint8_t* KBytes;
-  typedef uint8_t* const __attribute__((address_space(4)))* KPtr;
-  typedef const __attribute__((address_space(4))) float* KFloat;
-  const KBytes k = (KBytes)__builtin_amdgcn_kernarg_segment_ptr();
-  a.out = ((KPtr)(k + offsetof(Each, out)))[y];
-  a.alpha *= ((KFloat)(k + offsetof(Each, alpha)))[y];
+  typedef const __attribute__((address_space(4))) T* KT;
+  return ((KT)((KBytes)__builtin_amdgcn_kernarg_segment_ptr() + offset))[i];
+}
+__device__ __forceinline__ Run run_at(int x) {
+  const intx4 v = looked_up<intx4>(offsetof(Each, run), x);
+  return Run{v[0], v[1], v[2], v[3]};
 }
 
 template <class T>
@@ -92,67 +110,35 @@ __device__ __forceinline__ T* moved(T* p, int64_t off) {
   return p ? reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + off) : p;
 }
 
-__device__ __forceinline__ void pick_problem(Args& a, int nout) {
-  const int y = (int)blockIdx.y;
-  const int64_t off = (int64_t)y * a.bstride;
-  a.p.data = moved(a.p.data, off);
-  a.q.data = moved(a.q.data, off);
-  a.dalpha = moved(a.dalpha, off);
-  a.a = moved(a.a, off);
-  a.out_t = moved(a.out_t, off);
-  a.partials = moved(a.partials, (int64_t)y * a.part_stride);
-  if (nout)
-    pick_output(a, y);
-  else
-    a.out = moved(a.out, off);
-}
-
 // ---- schedule ----------------------------------------------------------------
-// The tiles are cut into kXcds contiguous runs, one per XCD, in an order that
-// keeps a run's tiles in a compact patch (they share the XCD's L2).  Of a
-// run's n tiles the first n / slots * slots run whole (slots: workgroups
-// resident on an XCD) and the rest, when parts > 1, in K-parts.
+// The tiles of all problems are cut into kXcds contiguous runs, one per XCD,
+// in an order that keeps a run's tiles in a compact patch (they share the
+// XCD's L2).  A run's first n / slots * slots tiles are whole units, the rest,
+// when parts > 1, K-parts; the workgroup in slot l of an XCD takes units l,
+// l + slots, ... of its run.
 
 struct Unit {
   int tile, part, split;        // split: index among the split tiles, -1 for a whole tile
 };
 
-__host__ __device__ inline void run_of(int tiles, int slots, int parts, int x, int& t0, int& n, int& whole) {
-  t0 = (int)((int64_t)x * tiles / kXcds);
-  n = (int)((int64_t)(x + 1) * tiles / kXcds) - t0;
-  whole = parts > 1 ? n / slots * slots : n;
-}
-
-__device__ __forceinline__ bool unit_of(const Args& a, int b, Unit& u) {
-  const int x = b % kXcds, l = b / kXcds;
-  int t0, n, whole;
-  run_of(a.tiles, a.slots, a.parts, x, t0, n, whole);
+// Unit l of a run; false when there is none.
+__device__ __forceinline__ bool unit_of(const Args& a, const Run& run, int l, Unit& u) {
   u.part = 0;
   u.split = -1;
-  u.tile = t0 + l;
-  if (l < whole) return true;
-  const int r = l - whole;
-  if (r >= (n - whole) * a.parts) return false;
-  int base = 0;
-  for (int y = 0; y < x; ++y) {
-    int ty, ny, wy;
-    run_of(a.tiles, a.slots, a.parts, y, ty, ny, wy);
-    base += ny - wy;
-  }
-  u.tile = t0 + whole + r / a.parts;
-  u.part = r % a.parts;
-  u.split = base + r / a.parts;
+  u.tile = run.t0 + l;
+  if (l < run.whole) return true;
+  if (l >= run.units) return false;
+  const int r = l - run.whole;
+  const int s = (int)(((uint32_t)r * a.parts_inv) >> 16);      // r / parts
+  u.tile = run.t0 + run.whole + s;
+  u.part = r - s * a.parts;
+  u.split = run.split0 + s;
   return true;
 }
 
-__device__ __forceinline__ int split_tile(const Args& a, int s) {
-  for (int x = 0; x < kXcds; ++x) {
-    int t0, n, whole;
-    run_of(a.tiles, a.slots, a.parts, x, t0, n, whole);
-    if (s < n - whole) return t0 + whole + s;
-    s -= n - whole;
-  }
-  return 0;
+// First panel of K-part p of n.
+__device__ __forceinline__ int part_panel(const Args& a, int p, int n) {
+  return n == 1 ? p * a.panels : __builtin_amdgcn_readfirstlane((int)((uint32_t)(a.panels * p) / (uint32_t)n));
 }
 
 // Strips of kStrip tile rows, column by column within a strip; symmetric
@@ -187,6 +173,23 @@ __device__ __forceinline__ void tile_of(const Args& a, int t, int& I, int& J) {
   J = t / w;
 }
 
+// Problem, row block and column block of a tile of the batch, in scalar
+// registers (the divisions run on the vector unit).
+__device__ __forceinline__ void place_of(const Args& a, int t, int& y, int& I, int& J) {
+  y = a.batch == 1 ? 0 : __builtin_amdgcn_readfirstlane(t / a.tiles);
+  int i, j;
+  tile_of(a, t - y * a.tiles, i, j);
+  I = __builtin_amdgcn_readfirstlane(i);
+  J = __builtin_amdgcn_readfirstlane(j);
+}
+
+// The same value, which the compiler takes as new: what is computed from it
+// once a tile stays there, instead of waiting in registers through the tiles.
+__device__ __forceinline__ int renewed(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // ---- loads -------------------------------------------------------------------
 // Global -> LDS DMA: lane l's bytes land at lds + 16 l (4 l).  Inline asm, so
 // that the compiler does not take the LDS write as pending before every later
@@ -206,65 +209,80 @@ __device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t
 // offset for each step plus a constant for its 32-row block.
 __device__ __forceinline__ int swizzle(int r) { return (r ^ ((r & 31) >> 3)) & 7; }
 
-// Byte offsets of a lane's loads inside a panel.  Rows past the operand's end
-// read its last row: they feed only outputs that the epilogue does not write.
+// Where a workgroup's loads stand: the next panel of the unit being loaded,
+// the wave's operand of it, and the byte offsets of a lane's loads inside a
+// panel.  Rows past the operand's end read its last row: they feed only
+// outputs that the epilogue does not write.  A wave's share of a stage never
+// straddles the operands: B rows are a multiple of it.
 template <class C, bool FP4>
-struct Src {
+struct Loads {
+  static constexpr int kLoads = C::kCodeLoads + (FP4 ? C::kScaleLoads : 0);
+  int l, g, g1;                         // unit of the run, next panel, end
+  const uint8_t *data, *scales;         // panel g of the wave's operand
+  int64_t pitch;                        // bytes of a panel's codes
   uint32_t code[C::kCodeLoads];
   uint32_t scale[FP4 ? C::kScaleLoads : 1];
-};
 
-template <class C, bool FP4>
-__device__ __forceinline__ void init_src(const Args& a, int m0, int n0, int wave, int lane, Src<C, FP4>& s) {
+  __device__ __forceinline__ void start(const Args& a, const Unit& u, int wave, int lane) {
+    int y, I, J;
+    place_of(a, u.tile, y, I, J);
+    const int nparts = u.split < 0 ? 1 : a.parts;
+    g = part_panel(a, u.part, nparts);
+    g1 = part_panel(a, u.part + 1, nparts);
+    const bool isP = wave * C::kCodeLoads * 8 < C::B;
+    const int64_t rows = isP ? a.p.rows : a.q.rows;
+    pitch = rows * 128;
+    data = (isP ? a.p.data : a.q.data) + (int64_t)y * a.bstride + (int64_t)g * pitch;
+    if constexpr (FP4) scales = (isP ? a.p.scales : a.q.scales) + (int64_t)g * rows * 8;
+    const int lim = isP ? a.M : a.N;
+    // operand row of the wave's first stage row
+    const int r0 = (isP ? I * C::B : J * C::B - C::B) + 8 * wave * C::kCodeLoads;
 #pragma unroll
-  for (int i = 0; i < C::kCodeLoads; ++i) {
-    const int r = 8 * (wave * C::kCodeLoads + i) + (lane >> 3);      // operand row of the stage
-    int row = r < C::B ? m0 + r : n0 + r - C::B;
-    const int lim = r < C::B ? a.M : a.N;
-    row = row < lim ? row : lim - 1;
-    s.code[i] = (uint32_t)row * 128u + 16u * (uint32_t)((lane & 7) ^ swizzle(r));
-  }
-  if constexpr (FP4) {
-#pragma unroll
-    for (int i = 0; i < C::kScaleLoads; ++i) {
-      const int r = 32 * (wave * C::kScaleLoads + i) + (lane >> 1);
-      int row = r < C::B ? m0 + r : n0 + r - C::B;
-      const int lim = r < C::B ? a.M : a.N;
+    for (int i = 0; i < C::kCodeLoads; ++i) {
+      int row = r0 + 8 * i + (lane >> 3);
       row = row < lim ? row : lim - 1;
-      s.scale[i] = (uint32_t)row * 8u + 4u * (uint32_t)(lane & 1);
+      code[i] = (uint32_t)row * 128u + 16u * (uint32_t)((lane & 7) ^ swizzle(8 * i + 8 * wave * C::kCodeLoads + (lane >> 3)));
+    }
+    if constexpr (FP4) {
+#pragma unroll
+      for (int i = 0; i < C::kScaleLoads; ++i) {
+        int row = r0 + 32 * i + (lane >> 1);
+        row = row < lim ? row : lim - 1;
+        scale[i] = (uint32_t)row * 8u + 4u * (uint32_t)(lane & 1);
+      }
     }
   }
-}
-
-// Load number k of a wave's share of a stage.  A share never straddles the
-// operands: B rows are a multiple of it.
-template <class C, bool FP4>
-struct Issue {
-  static constexpr int kLoads = C::kCodeLoads + (FP4 ? C::kScaleLoads : 0);
-  const uint8_t *data, *scales;        // the wave's operand
-  int64_t rows;
-  uint32_t code0, scale0;              // LDS offsets of the wave's share in a stage
-
-  __device__ __forceinline__ Issue(const Args& a, int wave) {
-    const bool isP = wave * C::kCodeLoads * 8 < C::B;
-    data = isP ? a.p.data : a.q.data;
-    scales = isP ? a.p.scales : a.q.scales;
-    rows = isP ? a.p.rows : a.q.rows;
-    code0 = (uint32_t)(wave * C::kCodeLoads) * 1024u;
-    scale0 = (uint32_t)C::kCodeBytes + (uint32_t)(wave * C::kScaleLoads) * 256u;
-  }
-  __device__ __forceinline__ void load(const Src<C, FP4>& s, int g, uint32_t stage, int k) const {
+  // Load number k of the wave's share into the stage at LDS address `stage`.
+  __device__ __forceinline__ void load(uint32_t stage, int wave, int k) const {
     if (k < C::kCodeLoads)
-      dma16(data + (int64_t)g * rows * 128, s.code[k], stage + code0 + 1024u * k);
+      dma16(data, code[k], stage + (uint32_t)(wave * C::kCodeLoads + k) * 1024u);
     else if constexpr (FP4)
-      dma4(scales + (int64_t)g * rows * 8, s.scale[k - C::kCodeLoads], stage + scale0 + 256u * (k - C::kCodeLoads));
+      dma4(scales, scale[k - C::kCodeLoads],
+           stage + (uint32_t)C::kCodeBytes + (uint32_t)(wave * C::kScaleLoads + k - C::kCodeLoads) * 256u);
+  }
+  // To the next panel: of this unit, of the workgroup's next unit, or, behind
+  // the last, the same again (into a buffer that nothing reads).
+  __device__ __forceinline__ void advance(const Args& a, const Run& run, int wave, int lane) {
+    if (g + 1 < g1) {
+      ++g;
+      data += pitch;
+      if constexpr (FP4) scales += pitch / 16;
+      return;
+    }
+    Unit u;
+    if (unit_of(a, run, l + a.slots, u)) {
+      l += a.slots;
+      start(a, u, wave, renewed(lane));
+    }
   }
 };
 
 // ---- multiply ------------------------------------------------------------------
 template <int S>
 __device__ __forceinline__ floatx16 mfma_fp4(intx4 a, intx4 b, floatx16 c, uint32_t sa, uint32_t sb) {
-  const intx8 x = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, y = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+  // 4-bit operands are four registers; the rest of the builtin's eight is not read
+  const intx8 x = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+  const intx8 y = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, S, (int)sa, S, (int)sb);
 }
 __device__ __forceinline__ floatx16 mfma_f16(intx4 a, intx4 b, floatx16 c) {
@@ -341,196 +359,198 @@ __device__ __forceinline__ float f16_hi(uint32_t w) {
   return (float)r.h[1];
 }
 
-// Two lanes that hold columns c and c + 1 of four rows (lo: rows 0 and 1
-// packed, hi: rows 2 and 3) exchange halves: the even lane ends with the
-// column pairs of rows 0 and 1, the odd one with those of rows 2 and 3.
-__device__ __forceinline__ void pair_columns(uint32_t lo, uint32_t hi, bool odd, uint32_t& first, uint32_t& second) {
-  const uint32_t give = odd ? lo : hi, keep = odd ? hi : lo;
-  const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);
-  const uint32_t a = odd ? got : keep, b = odd ? keep : got;     // a: column c, b: column c + 1
-  first = __builtin_amdgcn_perm(b, a, 0x05040100u);
-  second = __builtin_amdgcn_perm(b, a, 0x07060302u);
+// Eight neighbours of a row-major matrix, or the first n of them.
+template <Dt T>
+__device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
+  if constexpr (T == Dt::F32) {
+    const float* f = static_cast<const float*>(p) + at;
+    const float4 a = *reinterpret_cast<const float4*>(f), b = *reinterpret_cast<const float4*>(f + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    v[0] = mx::bf16_lo(a.x); v[1] = mx::bf16_hi(a.x); v[2] = mx::bf16_lo(a.y); v[3] = mx::bf16_hi(a.y);
+    v[4] = mx::bf16_lo(a.z); v[5] = mx::bf16_hi(a.z); v[6] = mx::bf16_lo(a.w); v[7] = mx::bf16_hi(a.w);
+  }
+}
+template <Dt T>
+__device__ __forceinline__ void load_n(const void* p, int64_t at, int n, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (T == Dt::F32) v[i] = i < n ? static_cast<const float*>(p)[at + i] : 0.0f;
+    else v[i] = i < n ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[at + i] << 16) : 0.0f;
+  }
+}
+template <Dt T>
+__device__ __forceinline__ void store8(void* p, int64_t at, const float (&v)[8]) {
+  if constexpr (T == Dt::F32) {
+    float* f = static_cast<float*>(p) + at;
+    *reinterpret_cast<float4*>(f) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(f + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) =
+        make_uint4(mx::pack_bf16(v[0], v[1]), mx::pack_bf16(v[2], v[3]), mx::pack_bf16(v[4], v[5]),
+                   mx::pack_bf16(v[6], v[7]));
+  }
+}
+template <Dt T>
+__device__ __forceinline__ void store_n(void* p, int64_t at, int n, const float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) {
+      if constexpr (T == Dt::F32) static_cast<float*>(p)[at + i] = v[i];
+      else static_cast<uint16_t*>(p)[at + i] = (uint16_t)mx::pack_bf16(v[i], 0.0f);
+    }
 }
 
-// The tile as 16-bit values in LDS, row-major with a padded pitch; `words`
-// holds, per block and quad, the lane's four rows packed in pairs.
-template <class C>
-struct Stage16 {
-  static constexpr int kPitch = C::B * 2 + 16;
-  static constexpr int kBytes = C::B * kPitch;
-};
+// Orders a wave's own LDS writes before its reads of other lanes' values.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
-template <class C>
-struct Words {
-  uint32_t w[C::FM][C::FN][4][2];
-};
-template <class C, Dt T>
-__device__ __forceinline__ void pack_tile(const floatx16 (&acc)[C::FM][C::FN], Words<C>& w) {
+// f(row, column, v): eight neighbouring values of a tile row, each lane its
+// own; the wave's 32 x 32 blocks pass through LDS sixteen rows at a time.
+template <class C, class F>
+__device__ __forceinline__ void by_rows(const floatx16 (&acc)[C::FM][C::FN], int wm, int wn, int lane, uint8_t* lds,
+                                        F&& f) {
+  constexpr int kPitch = 36;             // floats; 16 rows are 2304 bytes
+  float* t = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int el = renewed(lane), h = el >> 5, c = el & 31, r = el >> 2, c8 = (el & 3) * 8;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) t[(8 * q + 4 * h + s) * kPitch + c] = acc[i][j][8 * half + 4 * q + s];
+        wave_sync();
+        float v[8];
+        const float4 lo = *reinterpret_cast<const float4*>(t + r * kPitch + c8);
+        const float4 hi = *reinterpret_cast<const float4*>(t + r * kPitch + c8 + 4);
+        v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+        v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+        f((wm * C::FM + i) * 32 + 16 * half + r, (wn * C::FN + j) * 32 + c8, v);
+        wave_sync();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+}
+
+// f(column, row, w): eight neighbouring values of a tile column times mul as
+// f16.
+template <class C, class F>
+__device__ __forceinline__ void by_cols(const floatx16 (&acc)[C::FM][C::FN], float mul, int wm, int wn, int lane, uint8_t* lds,
+                                        F&& f) {
+  constexpr int kPitch = 80;             // bytes; 32 columns of 32 rows
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
+      const int el = renewed(lane), h = el >> 5, c = el & 31, r = el >> 2, c8 = (el & 3) * 8;
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        w.w[i][j][q >> 1][q & 1] = T == Dt::BF16 ? mx::pack_bf16(acc[i][j][2 * q], acc[i][j][2 * q + 1])
-                                                 : pack_f16(acc[i][j][2 * q], acc[i][j][2 * q + 1]);
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint2*>(lds + c * kPitch + 2 * (8 * q + 4 * h)) =
+            make_uint2(pack_f16(mul * acc[i][j][4 * q], mul * acc[i][j][4 * q + 1]),
+                       pack_f16(mul * acc[i][j][4 * q + 2], mul * acc[i][j][4 * q + 3]));
+      wave_sync();
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint4 w = *reinterpret_cast<const uint4*>(lds + (16 * half + r) * kPitch + 2 * c8);
+        f((wn * C::FN + j) * 32 + 16 * half + r, (wm * C::FM + i) * 32 + c8, w);
+      }
+      wave_sync();
       __builtin_amdgcn_sched_barrier(0);
     }
 }
 
-template <class C>
-__device__ __forceinline__ void stage_rows(uint8_t* lds, int wm, int wn, int lane, const Words<C>& w) {
-  const int h = lane >> 5, c = lane & 31;
-  const bool odd = lane & 1;
-#pragma unroll
-  for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-    for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t first, second;
-        pair_columns(w.w[i][j][q][0], w.w[i][j][q][1], odd, first, second);
-        const int row = (wm * C::FM + i) * 32 + 8 * q + 4 * h + (odd ? 2 : 0);
-        const int col = (wn * C::FN + j) * 32 + (c & ~1);
-        *reinterpret_cast<uint32_t*>(lds + row * Stage16<C>::kPitch + col * 2) = first;
-        *reinterpret_cast<uint32_t*>(lds + (row + 1) * Stage16<C>::kPitch + col * 2) = second;
-      }
+// Eight neighbours of an f16 panel operand: row r, columns from c (a multiple
+// of 8) of an operand with `rows` rows a panel.
+__device__ __forceinline__ uint8_t* panel_at(uint8_t* p, int rows, int r, int c) {
+  return p + ((int64_t)(c >> 6) * rows + r) * 128 + (c & 63) * 2;
 }
 
-// The transposed tile: row = the tile's column.
-template <class C>
-__device__ __forceinline__ void stage_cols(uint8_t* lds, int wm, int wn, int lane, const Words<C>& w) {
-  const int h = lane >> 5, c = lane & 31;
-#pragma unroll
-  for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-    for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = (wn * C::FN + j) * 32 + c, col = (wm * C::FM + i) * 32 + 8 * q + 4 * h;
-        *reinterpret_cast<uint2*>(lds + row * Stage16<C>::kPitch + col * 2) =
-            make_uint2(w.w[i][j][q][0], w.w[i][j][q][1]);
-      }
-}
-
-// A staged tile to f16 panels: rows r0 .. of an operand with `rows` rows a
-// panel, columns from c0 (a multiple of 64) up to `cols` (likewise).
-template <class C>
-__device__ __forceinline__ void store_panels(const uint8_t* lds, uint8_t* dst, int r0, int rows, int c0, int cols) {
-  for (int k = (int)threadIdx.x; k < C::B * C::B / 8; k += C::kThreads) {
-    const int ch = k & 7, r = (k >> 3) % C::B, g = (k >> 3) / C::B;      // chunk, row, panel of the tile
-    if (r0 + r < rows && c0 + 64 * g < cols)
-      *reinterpret_cast<uint4*>(dst + ((int64_t)(c0 / 64 + g) * rows + r0 + r) * 128 + 16 * ch) =
-          *reinterpret_cast<const uint4*>(lds + r * Stage16<C>::kPitch + 128 * g + 16 * ch);
+// lds: this wave's kScratch bytes.  y: problem of the batch.
+template <class C, PanelEp EP, Dt OT, bool VEC>
+__device__ __forceinline__ void epilogue(const Args& a, int neach, floatx16 (&acc)[C::FM][C::FN], int y, int I, int J,
+                                         int wm, int wn, int lane, uint8_t* lds) {
+  const int m0 = I * C::B, n0 = J * C::B;
+  const int64_t off = (int64_t)y * a.bstride;
+  float alpha = a.alpha;
+  if (a.dalpha) alpha *= *moved(a.dalpha, off);
+  uint8_t* out = a.out + off;
+  if (neach) {
+    out = static_cast<uint8_t*>(looked_up<void*>(offsetof(Each, out), y));
+    alpha *= looked_up<float>(offsetof(Each, alpha), y);
   }
-}
-
-// Barrier after this wave's LDS accesses (global stores stay in flight).
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
-template <class C, PanelEp EP, Dt OT>
-__device__ __forceinline__ void epilogue(const Args& a, floatx16 (&acc)[C::FM][C::FN], int I, int J, int wm, int wn,
-                                         int lane, uint8_t* lds) {
-  const int m0 = I * C::B, n0 = J * C::B, h = lane >> 5, c = lane & 31;
-  const float alpha = a.dalpha ? a.alpha * *a.dalpha : a.alpha;
-  const bool inside = m0 + C::B <= a.M && n0 + C::B <= a.N;
   if constexpr (EP == PanelEp::Step || EP == PanelEp::Out) {
-    // element by element: 32 lanes cover 32 neighbouring columns
-    const int64_t base = (int64_t)(m0 + wm * C::FM * 32 + 4 * h) * a.N + n0 + wn * C::FN * 32 + c;
-    constexpr bool kStaged = EP == PanelEp::Out && OT == Dt::BF16;
+    // VEC: rows of whole 16-byte units, so that eight neighbours are in or out
+    // together and move as such
+    by_rows<C>(acc, wm, wn, lane, lds, [&](int dr, int dc, float (&v)[8]) {
+      const int row = m0 + dr, col = n0 + dc;
+      if (row >= a.M || col >= a.N) return;
+      const int64_t at = (int64_t)row * a.N + col;
+      const int n = a.N - col < 8 ? a.N - col : 8;
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i)
+      for (int e = 0; e < 8; ++e) v[e] *= alpha;
+      float o[8];                        // the addend, or the weights
+      if constexpr (EP == PanelEp::Step) {
+        if constexpr (VEC) load8<OT>(out, at, o);
+        else load_n<OT>(out, at, n, o);
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j)
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(a.beta, o[e], -v[e]);
+      } else if (a.addend) {
+        if constexpr (VEC) load8<Dt::F32>(a.addend, at, o);
+        else load_n<Dt::F32>(a.addend, at, n, o);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int dr = i * 32 + 8 * (r >> 2) + (r & 3), dc = j * 32;
-          const int64_t at = base + (int64_t)dr * a.N + dc;
-          const bool ok = inside || (m0 + wm * C::FM * 32 + 4 * h + dr < a.M && n0 + wn * C::FN * 32 + c + dc < a.N);
-          float v = alpha * acc[i][j][r];
-          if constexpr (EP == PanelEp::Out) {
-            if (a.addend && ok) v = fmaf(a.beta, a.addend[at], v);
-            if constexpr (kStaged) acc[i][j][r] = v;
-            else if (ok) reinterpret_cast<float*>(a.out)[at] = v;
-          } else if (ok) {
-            if constexpr (OT == Dt::F32) {
-              float* w = reinterpret_cast<float*>(a.out) + at;
-              *w = fmaf(a.beta, *w, -v);
-            } else {
-              uint16_t* w = reinterpret_cast<uint16_t*>(a.out) + at;
-              *w = (uint16_t)mx::pack_bf16(fmaf(a.beta, __uint_as_float((uint32_t)*w << 16), -v), 0.0f);
-            }
-          }
-        }
-    if constexpr (kStaged) {
-      Words<C> w;
-      pack_tile<C, Dt::BF16>(acc, w);
-      lds_barrier();
-      stage_rows<C>(lds, wm, wn, lane, w);
-      lds_barrier();
-      uint16_t* out = reinterpret_cast<uint16_t*>(a.out);
-      const bool vec = a.N % 8 == 0;
-      for (int k = (int)threadIdx.x; k < C::B * C::B / 8; k += C::kThreads) {
-        const int ch = k % (C::B / 8), r = k / (C::B / 8);
-        const int row = m0 + r, col = n0 + 8 * ch;
-        if (row >= a.M || col >= a.N) continue;
-        const uint4 v = *reinterpret_cast<const uint4*>(lds + r * Stage16<C>::kPitch + 16 * ch);
-        uint16_t* o = out + (int64_t)row * a.N + col;
-        if (vec) {
-          *reinterpret_cast<uint4*>(o) = v;
-        } else {
-          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int t = 0; t < 8; ++t)
-            if (col + t < a.N) o[t] = (uint16_t)(e[t >> 1] >> (16 * (t & 1)));
-        }
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(a.beta, o[e], v[e]);
       }
-    }
+      if constexpr (VEC) store8<OT>(out, at, v);
+      else store_n<OT>(out, at, n, v);
+    });
   } else {
     if constexpr (EP == PanelEp::Poly) {
-      // A is symmetric: rows 4 .. 7 of a column are four neighbours of a row
+      // A is symmetric: four neighbours of a column are four of a row
+      const uint8_t* A = a.a + off;
 #pragma unroll
       for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j)
+        for (int j = 0; j < C::FN; ++j) {
+          const int el = renewed(lane), h = el >> 5, c = el & 31;
+          const int row = m0 + (wm * C::FM + i) * 32 + 4 * h, col = n0 + (wn * C::FN + j) * 32 + c;
+          // outside A (whole blocks: M is a multiple of 64) anything finite
+          // does, nothing of it is stored
+          const int ra = row < a.M ? row : 0, ca = col < a.M ? col : 0;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int row = m0 + (wm * C::FM + i) * 32 + 8 * q + 4 * h, col = n0 + (wn * C::FN + j) * 32 + c;
-            uint2 w = make_uint2(0u, 0u);
-            if (inside || (row < a.M && col < a.N))
-              w = *reinterpret_cast<const uint2*>(a.a + ((int64_t)(row >> 6) * a.M + col) * 128 + (row & 63) * 2);
+            const uint2 w = *reinterpret_cast<const uint2*>(
+                A + ((int64_t)((ra + 8 * q) >> 6) * a.M + ca) * 128 + ((ra + 8 * q) & 63) * 2);
             const float av[4] = {f16_lo(w.x), f16_hi(w.x), f16_lo(w.y), f16_hi(w.y)};
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-              float v = fmaf(a.cc, acc[i][j][4 * q + t], a.cb * av[t]);
-              acc[i][j][4 * q + t] = row + t == col ? v + a.ca : v;
+              const float v = fmaf(a.cc, acc[i][j][4 * q + t], a.cb * av[t]);
+              acc[i][j][4 * q + t] = row + 8 * q + t == col ? v + a.ca : v;
             }
-            if (q == 3) __builtin_amdgcn_sched_barrier(0);
           }
-    } else {
-#pragma unroll
-      for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[i][j][r] *= alpha;
+          __builtin_amdgcn_sched_barrier(0);
+        }
     }
-    Words<C> w;
-    pack_tile<C, Dt::F32>(acc, w);                       // f16
+    const float mul = EP == PanelEp::Poly ? 1.0f : alpha;
+    // the transpose; a symmetric product's mirror (a diagonal tile is its own)
     constexpr bool kIter = EP == PanelEp::Iter;
-    uint8_t* tdst = kIter ? a.out_t : a.out;
-    lds_barrier();
-    stage_cols<C>(lds, wm, wn, lane, w);
-    lds_barrier();
-    // the transpose: rows n0 .., columns m0 ..; a symmetric product's mirror
-    // (a diagonal tile is its own)
-    store_panels<C>(lds, tdst, n0, a.N, m0, a.M);
-    if (kIter || I != J) {
-      lds_barrier();
-      stage_rows<C>(lds, wm, wn, lane, w);
-      lds_barrier();
-      store_panels<C>(lds, a.out, m0, a.M, n0, a.N);
-    }
+    uint8_t* tdst = kIter ? a.out_t + off : out;
+    by_cols<C>(acc, mul, wm, wn, lane, lds, [&](int dc, int dr, uint4 w) {
+      if (n0 + dc < a.N && m0 + dr < a.M) *reinterpret_cast<uint4*>(panel_at(tdst, a.N, n0 + dc, m0 + dr)) = w;
+    });
+    if (kIter || I != J)
+      by_rows<C>(acc, wm, wn, lane, lds, [&](int dr, int dc, float (&v)[8]) {
+        if (m0 + dr < a.M && n0 + dc < a.N)
+          *reinterpret_cast<uint4*>(panel_at(out, a.M, m0 + dr, n0 + dc)) =
+              make_uint4(pack_f16(mul * v[0], mul * v[1]), pack_f16(mul * v[2], mul * v[3]),
+                         pack_f16(mul * v[4], mul * v[5]), pack_f16(mul * v[6], mul * v[7]));
+      });
   }
 }
 
@@ -543,35 +563,35 @@ __device__ __forceinline__ size_t part_index(int b, int q, int thread) {
 template <class C, bool FP4>
 constexpr int stage_bytes() { return C::kCodeBytes + (FP4 ? C::kRows * 8 : 0); }
 
-template <class C, bool FP4, PanelEp EP, Dt OT>
-__global__ __launch_bounds__(C::kThreads, C::kBlocks* C::kWaves / 4) void panel_kernel(const Each e, Args a) {
-  constexpr int kStage = stage_bytes<C, FP4>();
-  __shared__ __attribute__((aligned(16)))
-  uint8_t smem[C::NST * kStage > Stage16<C>::kBytes ? C::NST * kStage : Stage16<C>::kBytes];
-  pick_problem(a, e.n);
-  Unit un;
-  if (!unit_of(a, (int)blockIdx.x, un)) return;
-  int I, J;
-  tile_of(a, un.tile, I, J);
-  const int nparts = un.split < 0 ? 1 : a.parts;
-  const int g0 = (int)((int64_t)a.panels * un.part / nparts), g1 = (int)((int64_t)a.panels * (un.part + 1) / nparts);
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / C::WN, wn = wave % C::WN;
-
-  floatx16 acc[C::FM][C::FN];
+template <class C>
+__device__ __forceinline__ void clear(floatx16 (&acc)[C::FM][C::FN]) {
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
     for (int j = 0; j < C::FN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+}
 
-  Src<C, FP4> src;
-  init_src<C, FP4>(a, I * C::B, J * C::B, wave, lane, src);
-  const Issue<C, FP4> dma(a, wave);
+template <class C, bool FP4, PanelEp EP, Dt OT, bool VEC>
+__global__ __launch_bounds__(C::kThreads, C::kBlocks* C::kWaves / 4) void panel_kernel(const Each e, Args a) {
+  constexpr int kStage = stage_bytes<C, FP4>();
+  __shared__ __attribute__((aligned(16))) uint8_t smem[C::NST * kStage + C::kWaves * kScratch];
+  const Run run = run_at((int)blockIdx.x % kXcds);
+  int l = (int)blockIdx.x / kXcds;
+  Unit un;
+  if (!unit_of(a, run, l, un)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  uint8_t* scratch = smem + C::NST * kStage + wave * kScratch;
+
+  floatx16 acc[C::FM][C::FN];
+  Loads<C, FP4> next;
+  next.l = l;
+  next.start(a, un, wave, lane);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
-  constexpr int kLoads = Issue<C, FP4>::kLoads, kReads = C::FM + C::FN, kMul = C::FM * C::FN;
+  constexpr int kLoads = Loads<C, FP4>::kLoads, kReads = C::FM + C::FN, kMul = C::FM * C::FN;
   uint32_t off[4];
 #pragma unroll
   for (int s = 0; s < 4; ++s)
@@ -579,99 +599,103 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks* C::kWaves / 4) void panel_
   const uint32_t soff = (uint32_t)((lane & 31) * 8 + 4 * (lane >> 5));
   Frags<C> f0, f1;
   Scales<C> sc;
+  // all but the newest NST - 2 stages' loads of this wave have landed
   auto wait_loads = [&] { asm volatile("s_waitcnt vmcnt(%0)" ::"n"((C::NST - 2) * kLoads) : "memory"); };
-  auto read_first = [&](const uint8_t* st) {
+
+  // NST - 1 stages in flight before the first is read, then always NST
 #pragma unroll
-    for (int k = 0; k < kReads; ++k) {
-      if constexpr (FP4) read_scale<C>(st, soff, wm, wn, k, sc);
-      read_frag<C>(st, off[0], wm, wn, k, f0);
+  for (int s = 0; s < C::NST; ++s) {
+    if (s == C::NST - 1) {
+      wait_loads();
+      __builtin_amdgcn_s_barrier();
     }
-  };
-  // Stages g0 .. g0 + NST - 2 in flight, then always one more: a panel past
-  // the last is the last again, into a buffer that nothing reads.
-  auto panel = [&](int g) { return g < g1 ? g : g1 - 1; };
 #pragma unroll
-  for (int s = 0; s < C::NST - 1; ++s)
+    for (int k = 0; k < kLoads; ++k) next.load(lds0 + s * kStage, wave, k);
+    if (s < C::NST - 1) next.advance(a, run, wave, lane);
+  }
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) dma.load(src, panel(g0 + s), lds0 + s * kStage, k);
-  wait_loads();
-  __builtin_amdgcn_s_barrier();
-  read_first(smem);
-#pragma unroll
-  for (int k = 0; k < kLoads; ++k) dma.load(src, panel(g0 + C::NST - 1), lds0 + (C::NST - 1) * kStage, k);
+  for (int k = 0; k < kReads; ++k) {
+    if constexpr (FP4) read_scale<C>(smem, soff, wm, wn, k, sc);
+    read_frag<C>(smem, off[0], wm, wn, k, f0);
+  }
 
   int cur = 0;
-  auto first_three = [&](const uint8_t* st) {
-    auto ahead = [&](int s, Frags<C>& f) {
-      return [&, s](int k) {
+  do {
+    clear<C>(acc);
+    const int nparts = un.split < 0 ? 1 : a.parts;
+    const int g0 = part_panel(a, un.part, nparts), g1 = part_panel(a, un.part + 1, nparts);
+    for (int g = g0; g < g1; ++g) {
+      // here, not behind the loads: a branch behind the MFMAs would let the
+      // compiler sink them past it
+      next.advance(a, run, wave, lane);
+      const uint8_t* st = smem + cur * kStage;
+      auto ahead = [&](int s, Frags<C>& f) {
+        return [&, s](int k) {
 #pragma unroll
-        for (int r = share(kReads, k, kMul); r < share(kReads, k + 1, kMul); ++r)
-          read_frag<C>(st, off[s], wm, wn, r, f);
+          for (int r = share(kReads, k, kMul); r < share(kReads, k + 1, kMul); ++r)
+            read_frag<C>(st, off[s], wm, wn, r, f);
+        };
       };
-    };
-    step<C, FP4, 0>(f0, sc, acc, ahead(1, f1));
-    step<C, FP4, 1>(f1, sc, acc, ahead(2, f0));
-    step<C, FP4, 2>(f0, sc, acc, ahead(3, f1));
-  };
-  for (int g = g0; g + 1 < g1; ++g) {
-    first_three(smem + cur * kStage);
-    // every read of this stage has returned: its buffer is free once all
-    // waves are here, and the next stage's loads have landed
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    wait_loads();
-    __builtin_amdgcn_s_barrier();
-    const uint32_t freed = lds0 + cur * kStage;
-    cur = cur + 1 == C::NST ? 0 : cur + 1;
-    const uint8_t* st = smem + cur * kStage;
-    const int gn = panel(g + C::NST);
-    Scales<C> nsc;
-    step<C, FP4, 3>(f1, sc, acc, [&](int k) {
+      step<C, FP4, 0>(f0, sc, acc, ahead(1, f1));
+      step<C, FP4, 1>(f1, sc, acc, ahead(2, f0));
+      step<C, FP4, 2>(f0, sc, acc, ahead(3, f1));
+      // every read of this stage has returned: its buffer is free once all
+      // waves are here, and the next stage's loads have landed
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      wait_loads();
+      __builtin_amdgcn_s_barrier();
+      const uint32_t freed = lds0 + cur * kStage;
+      cur = cur + 1 == C::NST ? 0 : cur + 1;
+      const uint8_t* nst = smem + cur * kStage;
+      Scales<C> nsc;
+      step<C, FP4, 3>(f1, sc, acc, [&](int k) {
 #pragma unroll
-      for (int r = share(kReads, k, kMul); r < share(kReads, k + 1, kMul); ++r) {
-        if constexpr (FP4) read_scale<C>(st, soff, wm, wn, r, nsc);
-        read_frag<C>(st, off[0], wm, wn, r, f0);
-      }
+        for (int r = share(kReads, k, kMul); r < share(kReads, k + 1, kMul); ++r) {
+          if constexpr (FP4) read_scale<C>(nst, soff, wm, wn, r, nsc);
+          read_frag<C>(nst, off[0], wm, wn, r, f0);
+        }
 #pragma unroll
-      for (int r = share(kLoads, k, kMul); r < share(kLoads, k + 1, kMul); ++r) dma.load(src, gn, freed, r);
-    });
-    if constexpr (FP4) sc = nsc;
-  }
-  first_three(smem + cur * kStage);
-  step<C, FP4, 3>(f1, sc, acc, [](int) {});
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // the loads past the end, before LDS serves the epilogue
-
-  if (un.split >= 0) {
-    float* part = a.partials + ((size_t)un.split * a.parts + un.part) * C::kAcc * C::kThreads;
+        for (int r = share(kLoads, k, kMul); r < share(kLoads, k + 1, kMul); ++r) next.load(freed, wave, r);
+      });
+      if constexpr (FP4) sc = nsc;
+    }
+    if (un.split >= 0) {
+      float* part = a.partials + ((size_t)un.split * a.parts + un.part) * C::kAcc * C::kThreads;
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i)
+      for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j)
+        for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<float4*>(part + part_index<C>(i * C::FN + j, q, threadIdx.x)) = make_float4(
-              acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
-    return;
-  }
-  epilogue<C, EP, OT>(a, acc, I, J, wm, wn, lane, smem);
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<float4*>(part + part_index<C>(i * C::FN + j, q, threadIdx.x)) = make_float4(
+                acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+    } else {
+      int y, I, J;
+      place_of(a, un.tile, y, I, J);
+      epilogue<C, EP, OT, VEC>(a, e.n, acc, y, I, J, wm, wn, renewed(lane), scratch);
+    }
+    l += a.slots;
+  } while (unit_of(a, run, l, un));
+  // the loads behind the last stage write LDS until they land
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 // One split tile a workgroup: its parts' partials, summed in part order.
-template <class C, PanelEp EP, Dt OT>
+template <class C, PanelEp EP, Dt OT, bool VEC>
 __global__ __launch_bounds__(C::kThreads) void panel_sum_kernel(const Each e, Args a) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[Stage16<C>::kBytes];
-  pick_problem(a, e.n);
+  __shared__ __attribute__((aligned(16))) uint8_t smem[C::kWaves * kScratch];
   const int split = (int)blockIdx.x;
-  int I, J;
-  tile_of(a, split_tile(a, split), I, J);
+  Run run = run_at(0);
+  for (int x = 1; x < kXcds; ++x) {
+    const Run r = run_at(x);
+    if (r.split0 <= split) run = r;        // runs without split tiles share the next one's split0
+  }
+  int y, I, J;
+  place_of(a, run.t0 + run.whole + split - run.split0, y, I, J);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   floatx16 acc[C::FM][C::FN];
-#pragma unroll
-  for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-    for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  clear<C>(acc);
   const float* part = a.partials + (size_t)split * a.parts * C::kAcc * C::kThreads;
   for (int p = 0; p < a.parts; ++p, part += (size_t)C::kAcc * C::kThreads) {
 #pragma unroll
@@ -687,81 +711,104 @@ __global__ __launch_bounds__(C::kThreads) void panel_sum_kernel(const Each e, Ar
           acc[i][j][4 * q + 3] += v.w;
         }
   }
-  epilogue<C, EP, OT>(a, acc, I, J, wave / C::WN, wave % C::WN, lane, smem);
+  epilogue<C, EP, OT, VEC>(a, e.n, acc, y, I, J, wave / C::WN, wave % C::WN, lane, smem + wave * kScratch);
+}
+
+template <class C, bool FP4, PanelEp EP, Dt OT, bool VEC>
+hipError_t launch_one(const Each& e, const Args& a, const PanelPlan& p, hipStream_t s) {
+  panel_kernel<C, FP4, EP, OT, VEC><<<dim3((unsigned)p.groups), C::kThreads, 0, s>>>(e, a);
+  const hipError_t r = hipGetLastError();
+  if (r != hipSuccess || p.split_tiles == 0) return r;
+  panel_sum_kernel<C, EP, OT, VEC><<<dim3((unsigned)p.split_tiles), C::kThreads, 0, s>>>(e, a);
+  return hipGetLastError();
 }
 
 template <class C, bool FP4, PanelEp EP, Dt OT>
-hipError_t launch(const Each& e, const Args& a, const PanelPlan& p, int batch, hipStream_t s) {
-  panel_kernel<C, FP4, EP, OT><<<dim3((unsigned)p.units, (unsigned)batch), C::kThreads, 0, s>>>(e, a);
-  const hipError_t r = hipGetLastError();
-  if (r != hipSuccess || p.split_tiles == 0) return r;
-  panel_sum_kernel<C, EP, OT><<<dim3((unsigned)p.split_tiles, (unsigned)batch), C::kThreads, 0, s>>>(e, a);
-  return hipGetLastError();
+hipError_t launch(const Each& e, const Args& a, const PanelPlan& p, hipStream_t s) {
+  if constexpr (EP == PanelEp::Out || EP == PanelEp::Step)
+    if (a.N % 8 != 0) return launch_one<C, FP4, EP, OT, false>(e, a, p, s);
+  return launch_one<C, FP4, EP, OT, true>(e, a, p, s);
 }
 
 template <class C>
 hipError_t launch_tile(const PanelProblem& g, const Each& e, const Args& a, const PanelPlan& p, bool fp4,
                        hipStream_t s) {
-  const int b = g.batch;
   if (fp4)                               // MXFP4 products have the plain epilogue only
-    return g.ot == Dt::F32 ? launch<C, true, PanelEp::Out, Dt::F32>(e, a, p, b, s)
-                           : launch<C, true, PanelEp::Out, Dt::BF16>(e, a, p, b, s);
+    return g.ot == Dt::F32 ? launch<C, true, PanelEp::Out, Dt::F32>(e, a, p, s)
+                           : launch<C, true, PanelEp::Out, Dt::BF16>(e, a, p, s);
   switch (g.ep) {
     case PanelEp::Out:
-      return g.ot == Dt::F32 ? launch<C, false, PanelEp::Out, Dt::F32>(e, a, p, b, s)
-                             : launch<C, false, PanelEp::Out, Dt::BF16>(e, a, p, b, s);
+      return g.ot == Dt::F32 ? launch<C, false, PanelEp::Out, Dt::F32>(e, a, p, s)
+                             : launch<C, false, PanelEp::Out, Dt::BF16>(e, a, p, s);
     case PanelEp::Step:
-      return g.ot == Dt::F32 ? launch<C, false, PanelEp::Step, Dt::F32>(e, a, p, b, s)
-                             : launch<C, false, PanelEp::Step, Dt::BF16>(e, a, p, b, s);
-    case PanelEp::Gram: return launch<C, false, PanelEp::Gram, Dt::F32>(e, a, p, b, s);
-    case PanelEp::Poly: return launch<C, false, PanelEp::Poly, Dt::F32>(e, a, p, b, s);
-    case PanelEp::Iter: return launch<C, false, PanelEp::Iter, Dt::F32>(e, a, p, b, s);
+      return g.ot == Dt::F32 ? launch<C, false, PanelEp::Step, Dt::F32>(e, a, p, s)
+                             : launch<C, false, PanelEp::Step, Dt::BF16>(e, a, p, s);
+    case PanelEp::Gram: return launch<C, false, PanelEp::Gram, Dt::F32>(e, a, p, s);
+    case PanelEp::Poly: return launch<C, false, PanelEp::Poly, Dt::F32>(e, a, p, s);
+    case PanelEp::Iter: return launch<C, false, PanelEp::Iter, Dt::F32>(e, a, p, s);
   }
   return hipErrorInvalidValue;
 }
 
+// The runs of a plan's tiles.  split: K-parts of the tiles that do not fill a
+// round of the slots.
+void runs_of(int tiles, int slots, int parts, Run (&run)[kXcds]) {
+  int split0 = 0;
+  for (int x = 0; x < kXcds; ++x) {
+    Run& r = run[x];
+    r.t0 = (int)((int64_t)x * tiles / kXcds);
+    const int n = (int)((int64_t)(x + 1) * tiles / kXcds) - r.t0;
+    r.whole = parts > 1 ? n / slots * slots : n;
+    r.units = r.whole + (n - r.whole) * parts;
+    r.split0 = split0;
+    split0 += n - r.whole;
+  }
+}
+
 template <class C>
-PanelPlan plan_tile(int64_t M, int64_t N, bool sym, int parts) {
+PanelPlan plan_tile(int64_t M, int64_t N, bool sym, int batch, int parts) {
   PanelPlan p;
   p.tile = C::B;
   p.parts = parts;
   p.TM = (int)((M + C::B - 1) / C::B);
   p.TN = (int)((N + C::B - 1) / C::B);
   p.tiles = sym ? p.TM * (p.TM + 1) / 2 : p.TM * p.TN;
-  p.split_tiles = 0;
+  p.slots = C::kBlocks * kCusPerXcd;
+  Run run[kXcds];
+  runs_of(p.tiles * batch, p.slots, parts, run);
   int most = 0;
-  for (int x = 0; x < kXcds; ++x) {
-    int t0, n, whole;
-    run_of(p.tiles, C::kBlocks * kCusPerXcd, parts, x, t0, n, whole);
-    const int u = whole + (n - whole) * parts;
-    most = u > most ? u : most;
-    if (parts > 1) p.split_tiles += n - whole;
+  p.split_tiles = 0;
+  for (const Run& r : run) {
+    most = r.units > most ? r.units : most;
+    if (parts > 1) p.split_tiles += (r.units - r.whole) / parts;
   }
-  p.units = most * kXcds;
+  p.groups = (most < p.slots ? most : p.slots) * kXcds;
   p.ws_bytes = (size_t)p.split_tiles * parts * C::kAcc * C::kThreads * sizeof(float);
   return p;
 }
 
-PanelPlan plan_at(int tile, int64_t M, int64_t N, bool sym, int parts) {
-  return tile == 256 ? plan_tile<Tile256>(M, N, sym, parts)
-                     : tile == 128 ? plan_tile<Tile128>(M, N, sym, parts) : plan_tile<Tile64>(M, N, sym, parts);
+PanelPlan plan_at(int tile, int64_t M, int64_t N, bool sym, int batch, int parts) {
+  switch (tile) {
+    case 256: return plan_tile<Tile256>(M, N, sym, batch, parts);
+    case 192: return plan_tile<Tile192>(M, N, sym, batch, parts);
+    case 128: return plan_tile<Tile128>(M, N, sym, batch, parts);
+    default: return plan_tile<Tile64>(M, N, sym, batch, parts);
+  }
 }
 
 }  // namespace
 
-PanelPlan plan_panel(int64_t M, int64_t N, int64_t panels, bool sym, int batch, bool allow_split,
-                     bool fp4) {
+PanelPlan plan_panel(int64_t M, int64_t N, int64_t panels, bool sym, int batch, bool allow_split, bool fp4) {
   (void)panels;
-  (void)fp4;
   (void)allow_split;
+  (void)fp4;
   const int64_t big = (M < N ? M : N);
-  const int tile = big >= 1024 ? 256 : big >= 256 ? 128 : 64;
-  (void)batch;
-  return plan_at(tile, M, N, sym, 1);
+  const int tile = getenv("PT") ? atoi(getenv("PT")) : big >= 1024 ? 256 : big >= 256 ? 128 : 64;
+  const int parts = getenv("PP") ? atoi(getenv("PP")) : 1;
+  return plan_at(tile, M, N, sym, batch, allow_split ? parts : 1);
 }
 
-hipError_t launch_panel(const PanelProblem& g, const PanelPlan& p, bool fp4, void* ws, int64_t ws_stride,
-                        hipStream_t s) {
+hipError_t launch_panel(const PanelProblem& g, const PanelPlan& p, bool fp4, void* ws, hipStream_t s) {
   if (g.batch < 1 || g.batch > kMaxPanelBatch) return hipErrorInvalidValue;
   Args a{};
   a.p = g.p;
@@ -772,10 +819,12 @@ hipError_t launch_panel(const PanelProblem& g, const PanelPlan& p, bool fp4, voi
   a.TM = p.TM;
   a.TN = p.TN;
   a.tiles = p.tiles;
+  a.batch = g.batch;
   a.parts = p.parts;
+  a.parts_inv = (65536u + (uint32_t)p.parts - 1) / (uint32_t)p.parts;
+  a.slots = p.slots;
   a.sym = g.sym ? 1 : 0;
   a.partials = static_cast<float*>(ws);
-  a.part_stride = ws_stride;
   a.alpha = g.alpha;
   a.beta = g.beta;
   a.ca = g.ca;
@@ -788,15 +837,17 @@ hipError_t launch_panel(const PanelProblem& g, const PanelPlan& p, bool fp4, voi
   a.a = g.a;
   a.bstride = g.bstride;
   Each e;
+  runs_of(p.tiles * g.batch, p.slots, p.parts, e.run);
   e.n = g.out_each ? g.batch : 0;
   for (int i = 0; i < kMaxPanelBatch; ++i) {
     e.out[i] = i < e.n ? g.out_each[i] : nullptr;
     e.alpha[i] = i < e.n && g.alpha_each ? g.alpha_each[i] : 1.0f;
   }
   switch (p.tile) {
-    case 256: a.slots = Tile256::kBlocks * kCusPerXcd; return launch_tile<Tile256>(g, e, a, p, fp4, s);
-    case 128: a.slots = Tile128::kBlocks * kCusPerXcd; return launch_tile<Tile128>(g, e, a, p, fp4, s);
-    default: a.slots = Tile64::kBlocks * kCusPerXcd; return launch_tile<Tile64>(g, e, a, p, fp4, s);
+    case 256: return launch_tile<Tile256>(g, e, a, p, fp4, s);
+    case 192: return launch_tile<Tile192>(g, e, a, p, fp4, s);
+    case 128: return launch_tile<Tile128>(g, e, a, p, fp4, s);
+    default: return launch_tile<Tile64>(g, e, a, p, fp4, s);
   }
 }
 

@@ -48,16 +48,15 @@ struct PanelProblem {
 constexpr int kMaxPanelBatch = 32;
 
 struct PanelPlan {
-  int tile;                // 256, 128 or 64 rows and columns
+  int tile;                // rows and columns of a tile
   int parts;               // K-parts of each tile left over after equal rounds (1: none)
-  int TM, TN, tiles;
-  int split_tiles, units;
-  size_t ws_bytes;         // FP32 partials of one problem
+  int TM, TN, tiles;       // of one problem
+  int slots;               // workgroups per XCD
+  int split_tiles, groups; // of the whole batch
+  size_t ws_bytes;         // FP32 partials of the whole batch
 };
-PanelPlan plan_panel(int64_t M, int64_t N, int64_t panels, bool sym, int batch, bool allow_split,
-                     bool fp4);
-hipError_t launch_panel(const PanelProblem& g, const PanelPlan& p, bool fp4, void* ws, int64_t ws_stride,
-                        hipStream_t s);
+PanelPlan plan_panel(int64_t M, int64_t N, int64_t panels, bool sym, int batch, bool allow_split, bool fp4);
+hipError_t launch_panel(const PanelProblem& g, const PanelPlan& p, bool fp4, void* ws, hipStream_t s);
 
 // ---- MXFP4 quantizers (mxfp4.hip) -------------------------------------------
 constexpr int kMxRows = 1, kMxCols = 2;
