@@ -44,7 +44,7 @@ PanelProblem mx_product(const uint8_t* pc, const uint8_t* ps, const uint8_t* qc,
 }
 
 inline PanelPlan mx_plan(int64_t M, int64_t N, int64_t K, bool split) {
-  return nvfp4::plan_panel(M, N, mx_panels(K), false, 1, split, true);
+  return nvfp4::plan_panel(M, N, mx_panels(K), false, 1, split, false);
 }
 
 }  // namespace
@@ -261,7 +261,7 @@ Ns16Layout ns16_layout(int64_t m, int64_t n, int batch) {
   L.mp = (xm + 63) / 64 * 64;
   L.np = (xn + 63) / 64 * 64;
   L.gram = nvfp4::plan_panel(L.mp, L.mp, L.np / 64, true, batch, true, false);
-  L.poly = nvfp4::plan_panel(L.mp, L.mp, L.mp / 64, true, batch, true, false);
+  L.poly = nvfp4::plan_panel(L.mp, L.mp, L.mp / 64, true, batch, true, true);
   L.iter = nvfp4::plan_panel(L.mp, L.np, L.mp / 64, false, batch, true, false);
   L.last = nvfp4::plan_panel(m, n, L.mp / 64, false, batch, true, false);
   size_t part = 0;

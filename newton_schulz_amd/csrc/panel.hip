@@ -24,7 +24,6 @@
 // Tiles left over after an equal number per slot are split along K into
 // parts whose FP32 partials a second kernel sums in part order.
 #include <cstddef>
-#include <cstdlib>
 
 #include "mxfp4_device.hpp"
 #include "panel.hpp"
@@ -57,7 +56,6 @@ struct Tile {
   static constexpr int kAcc = FM * FN * 16;
 };
 using Tile256 = Tile<256, 2, 4, 2, 1>;
-using Tile192 = Tile<192, 2, 2, 2, 1>;
 using Tile128 = Tile<128, 2, 2, 2, 2>;
 using Tile64 = Tile<64, 2, 2, 3, 2>;
 
@@ -512,30 +510,49 @@ __device__ __forceinline__ void epilogue(const Args& a, int neach, floatx16 (&ac
     });
   } else {
     if constexpr (EP == PanelEp::Poly) {
-      // A is symmetric: four neighbours of a column are four of a row
+      // A is symmetric: four neighbours of a column are four of a row; a
+      // batch's loads go out before the first is used
       const uint8_t* A = a.a + off;
+      constexpr int kBatch = C::FM * C::FN > 4 ? 2 : C::FM;      // block rows at a time
+      const int h = lane >> 5, c = lane & 31;
 #pragma unroll
-      for (int i = 0; i < C::FM; ++i)
+      for (int i0 = 0; i0 < C::FM; i0 += kBatch) {
+        uint2 w[kBatch][C::FN][4];
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) {
-          const int el = renewed(lane), h = el >> 5, c = el & 31;
-          const int row = m0 + (wm * C::FM + i) * 32 + 4 * h, col = n0 + (wn * C::FN + j) * 32 + c;
-          // outside A (whole blocks: M is a multiple of 64) anything finite
-          // does, nothing of it is stored
-          const int ra = row < a.M ? row : 0, ca = col < a.M ? col : 0;
+        for (int i = i0; i < i0 + kBatch && i < C::FM; ++i)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint2 w = *reinterpret_cast<const uint2*>(
-                A + ((int64_t)((ra + 8 * q) >> 6) * a.M + ca) * 128 + ((ra + 8 * q) & 63) * 2);
-            const float av[4] = {f16_lo(w.x), f16_hi(w.x), f16_lo(w.y), f16_hi(w.y)};
+          for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const float v = fmaf(a.cc, acc[i][j][4 * q + t], a.cb * av[t]);
-              acc[i][j][4 * q + t] = row + 8 * q + t == col ? v + a.ca : v;
+            for (int q = 0; q < 4; ++q) {
+              // outside A (whole blocks: M is a multiple of 64) anything
+              // finite does, nothing of it is stored
+              int row = m0 + (wm * C::FM + i) * 32, col = n0 + (wn * C::FN + j) * 32;
+              row = (row < a.M ? row : 0) + 8 * q;
+              col = col < a.M ? col : 0;
+              w[i - i0][j][q] = *reinterpret_cast<const uint2*>(
+                  A + (int64_t)(row >> 6) * a.M * 128 + (int64_t)col * 128 + (row & 63) * 2 + (uint32_t)(c * 128 + 8 * h));
             }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = i0; i < i0 + kBatch && i < C::FM; ++i)
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j) {
+            // row - column of the lane's first value
+            const int d = m0 - n0 + (wm * C::FM + i) * 32 - (wn * C::FN + j) * 32 + 4 * h - c;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint2 u = w[i - i0][j][q];
+              const float av[4] = {f16_lo(u.x), f16_hi(u.x), f16_lo(u.y), f16_hi(u.y)};
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const float v = fmaf(a.cc, acc[i][j][4 * q + t], a.cb * av[t]);
+                acc[i][j][4 * q + t] = d + 8 * q + t == 0 ? v + a.ca : v;
+              }
+            }
+            // here, not where the stores need it (with A's values kept till then)
+            asm volatile("" : "+v"(acc[i][j]));
           }
-          __builtin_amdgcn_sched_barrier(0);
-        }
+      }
     }
     const float mul = EP == PanelEp::Poly ? 1.0f : alpha;
     // the transpose; a symmetric product's mirror (a diagonal tile is its own)
@@ -680,11 +697,19 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks* C::kWaves / 4) void panel_
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-// One split tile a workgroup: its parts' partials, summed in part order.
+// A tile whose waves hold one 32 x 32 block each.
+template <class C>
+struct OneBlock : C {
+  static constexpr int FM = 1, FN = 1;
+};
+
+// The split tiles: block number b of every wave's sub-tile a workgroup, its
+// parts' partials summed in part order.
 template <class C, PanelEp EP, Dt OT, bool VEC>
 __global__ __launch_bounds__(C::kThreads) void panel_sum_kernel(const Each e, Args a) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[C::kWaves * kScratch];
-  const int split = (int)blockIdx.x;
+  constexpr int kBlocks = C::FM * C::FN;
+  const int split = (int)blockIdx.x / kBlocks, b = (int)blockIdx.x % kBlocks;
   Run run = run_at(0);
   for (int x = 1; x < kXcds; ++x) {
     const Run r = run_at(x);
@@ -694,24 +719,23 @@ __global__ __launch_bounds__(C::kThreads) void panel_sum_kernel(const Each e, Ar
   place_of(a, run.t0 + run.whole + split - run.split0, y, I, J);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  floatx16 acc[C::FM][C::FN];
-  clear<C>(acc);
+  floatx16 acc[1][1];
   const float* part = a.partials + (size_t)split * a.parts * C::kAcc * C::kThreads;
-  for (int p = 0; p < a.parts; ++p, part += (size_t)C::kAcc * C::kThreads) {
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i)
+  for (int r = 0; r < 16; ++r) acc[0][0][r] = 0.0f;
+#pragma unroll 4
+  for (int p = 0; p < a.parts; ++p)
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 v = *reinterpret_cast<const float4*>(part + part_index<C>(i * C::FN + j, q, threadIdx.x));
-          acc[i][j][4 * q] += v.x;
-          acc[i][j][4 * q + 1] += v.y;
-          acc[i][j][4 * q + 2] += v.z;
-          acc[i][j][4 * q + 3] += v.w;
-        }
-  }
-  epilogue<C, EP, OT, VEC>(a, e.n, acc, y, I, J, wave / C::WN, wave % C::WN, lane, smem + wave * kScratch);
+    for (int q = 0; q < 4; ++q) {
+      const float4 v = *reinterpret_cast<const float4*>(part + (size_t)p * C::kAcc * C::kThreads +
+                                                        part_index<C>(b, q, threadIdx.x));
+      acc[0][0][4 * q] += v.x;
+      acc[0][0][4 * q + 1] += v.y;
+      acc[0][0][4 * q + 2] += v.z;
+      acc[0][0][4 * q + 3] += v.w;
+    }
+  epilogue<OneBlock<C>, EP, OT, VEC>(a, e.n, acc, y, I, J, wave / C::WN * C::FM + b / C::FN, wave % C::WN * C::FN + b % C::FN,
+                                     lane, smem + wave * kScratch);
 }
 
 template <class C, bool FP4, PanelEp EP, Dt OT, bool VEC>
@@ -719,7 +743,7 @@ hipError_t launch_one(const Each& e, const Args& a, const PanelPlan& p, hipStrea
   panel_kernel<C, FP4, EP, OT, VEC><<<dim3((unsigned)p.groups), C::kThreads, 0, s>>>(e, a);
   const hipError_t r = hipGetLastError();
   if (r != hipSuccess || p.split_tiles == 0) return r;
-  panel_sum_kernel<C, EP, OT, VEC><<<dim3((unsigned)p.split_tiles), C::kThreads, 0, s>>>(e, a);
+  panel_sum_kernel<C, EP, OT, VEC><<<dim3((unsigned)(p.split_tiles * C::FM * C::FN)), C::kThreads, 0, s>>>(e, a);
   return hipGetLastError();
 }
 
@@ -744,7 +768,9 @@ hipError_t launch_tile(const PanelProblem& g, const Each& e, const Args& a, cons
       return g.ot == Dt::F32 ? launch<C, false, PanelEp::Step, Dt::F32>(e, a, p, s)
                              : launch<C, false, PanelEp::Step, Dt::BF16>(e, a, p, s);
     case PanelEp::Gram: return launch<C, false, PanelEp::Gram, Dt::F32>(e, a, p, s);
-    case PanelEp::Poly: return launch<C, false, PanelEp::Poly, Dt::F32>(e, a, p, s);
+    case PanelEp::Poly:
+      if constexpr (C::B < 256) return launch<C, false, PanelEp::Poly, Dt::F32>(e, a, p, s);
+      break;
     case PanelEp::Iter: return launch<C, false, PanelEp::Iter, Dt::F32>(e, a, p, s);
   }
   return hipErrorInvalidValue;
@@ -790,22 +816,63 @@ PanelPlan plan_tile(int64_t M, int64_t N, bool sym, int batch, int parts) {
 PanelPlan plan_at(int tile, int64_t M, int64_t N, bool sym, int batch, int parts) {
   switch (tile) {
     case 256: return plan_tile<Tile256>(M, N, sym, batch, parts);
-    case 192: return plan_tile<Tile192>(M, N, sym, batch, parts);
     case 128: return plan_tile<Tile128>(M, N, sym, batch, parts);
     default: return plan_tile<Tile64>(M, N, sym, batch, parts);
   }
 }
 
+// Microseconds that a plan takes, from measured products of random operands
+// (256 CUs; MXFP4 and f16 cost the same per panel).  A round is one tile per
+// slot; its time per panel grows with the tiles in it, since a full chip's
+// matrix units run at a lower clock:
+//   tile  slots  tiles: us per panel       once a round  once
+//    256    256    64: 1.20   256: 1.75          3         6
+//    128    512   256: 0.62   512: 1.10          2         4
+//     64    512   256: 0.36   512: 0.47          1         3
+// Measured against this: 4096^2 x 4096 38 us on 256 (43 on 128, 73 on 64),
+// 2048^2 x 4096 16 us on 128 (27 on 256, 20 on 64), 1024^2 x 4096 9 us on 64
+// (26 and 14).  A split adds its partials' traffic and the second kernel:
+// 1024^2 x 16384 takes 43 us on 128 whole, 23 in 4 parts.
+double plan_cost(const PanelPlan& p, int64_t panels, int batch) {
+  const double slots = p.slots * kXcds;
+  const int few = p.tile == 256 ? 64 : 256;
+  const double low = p.tile == 256 ? 1.20 : p.tile == 128 ? 0.62 : 0.36;
+  const double high = p.tile == 256 ? 1.75 : p.tile == 128 ? 1.10 : 0.47;
+  const double round = p.tile == 256 ? 3 : p.tile == 128 ? 2 : 1;
+  auto per_panel = [&](double tiles) {
+    if (tiles <= few) return low;
+    return tiles >= slots ? high : low + (high - low) * (tiles - few) / (slots - few);
+  };
+  const int64_t all = (int64_t)p.tiles * batch;
+  const int64_t whole = p.parts > 1 ? all - p.split_tiles : all;
+  auto rounds = [&](int64_t units, double g) {
+    const int64_t full = units / (int64_t)slots, rest = units % (int64_t)slots;
+    return full * (round + g * high) + (rest ? round + g * per_panel((double)rest) : 0.0);
+  };
+  double us = round * 2 + rounds(whole, (double)panels);
+  if (p.split_tiles)
+    us += rounds((int64_t)p.split_tiles * p.parts, (double)panels / p.parts) + 2.0 + 2.0 * (double)p.ws_bytes / 5e6;
+  return us;
+}
+
 }  // namespace
 
-PanelPlan plan_panel(int64_t M, int64_t N, int64_t panels, bool sym, int batch, bool allow_split, bool fp4) {
-  (void)panels;
-  (void)allow_split;
-  (void)fp4;
-  const int64_t big = (M < N ? M : N);
-  const int tile = getenv("PT") ? atoi(getenv("PT")) : big >= 1024 ? 256 : big >= 256 ? 128 : 64;
-  const int parts = getenv("PP") ? atoi(getenv("PP")) : 1;
-  return plan_at(tile, M, N, sym, batch, allow_split ? parts : 1);
+PanelPlan plan_panel(int64_t M, int64_t N, int64_t panels, bool sym, int batch, bool allow_split, bool poly) {
+  PanelPlan best{};
+  double least = 0.0;
+  for (int tile : {256, 128, 64}) {
+    if (tile == 256 && poly) continue;
+    for (int parts : {1, 2, 4, 8}) {
+      if (parts > 1 && (!allow_split || parts > panels)) break;
+      const PanelPlan p = plan_at(tile, M, N, sym, batch, parts);
+      const double us = plan_cost(p, panels, batch);
+      if (least == 0.0 || us < least) {
+        least = us;
+        best = p;
+      }
+    }
+  }
+  return best;
 }
 
 hipError_t launch_panel(const PanelProblem& g, const PanelPlan& p, bool fp4, void* ws, hipStream_t s) {
@@ -845,7 +912,6 @@ hipError_t launch_panel(const PanelProblem& g, const PanelPlan& p, bool fp4, voi
   }
   switch (p.tile) {
     case 256: return launch_tile<Tile256>(g, e, a, p, fp4, s);
-    case 192: return launch_tile<Tile192>(g, e, a, p, fp4, s);
     case 128: return launch_tile<Tile128>(g, e, a, p, fp4, s);
     default: return launch_tile<Tile64>(g, e, a, p, fp4, s);
   }

@@ -55,7 +55,9 @@ struct PanelPlan {
   int split_tiles, groups; // of the whole batch
   size_t ws_bytes;         // FP32 partials of the whole batch
 };
-PanelPlan plan_panel(int64_t M, int64_t N, int64_t panels, bool sym, int batch, bool allow_split, bool fp4);
+// poly: for the Poly epilogue, which has no 256 x 256 tiles: A's values next to
+// the 128 accumulators of a lane spill there (4 x 2048^2: 73 us, 50 us on 128).
+PanelPlan plan_panel(int64_t M, int64_t N, int64_t panels, bool sym, int batch, bool allow_split, bool poly);
 hipError_t launch_panel(const PanelProblem& g, const PanelPlan& p, bool fp4, void* ws, hipStream_t s);
 
 // ---- MXFP4 quantizers (mxfp4.hip) -------------------------------------------
