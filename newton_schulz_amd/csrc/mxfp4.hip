@@ -27,10 +27,6 @@ template <> struct Io<float> {
   }
   static __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
   // two neighbouring columns
-  static __device__ __forceinline__ void load2(const float* p, float& a, float& b) {
-    const float2 w = *reinterpret_cast<const float2*>(p);
-    a = w.x; b = w.y;
-  }
   static __device__ __forceinline__ void store2(float* p, float a, float b) {
     *reinterpret_cast<float2*>(p) = make_float2(a, b);
   }
@@ -48,10 +44,6 @@ template <> struct Io<uint16_t> {   // BF16 bits
                                               pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
   }
   static __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)pack_bf16(v, 0.0f); }
-  static __device__ __forceinline__ void load2(const uint16_t* p, float& a, float& b) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-    a = bf16_lo(w); b = bf16_hi(w);
-  }
   static __device__ __forceinline__ void store2(uint16_t* p, float a, float b) {
     *reinterpret_cast<uint32_t*>(p) = pack_bf16(a, b);
   }
@@ -144,88 +136,214 @@ __global__ __launch_bounds__(256) void dequant_rows_kernel(const uint8_t* __rest
 
 // ---- blocks down the columns (and both at once) -----------------------------
 // A workgroup takes 256 rows (one panel of x^T) x 128 columns: wave w the
-// 32-row block w, a lane two neighbouring columns of it, so a column block's
-// 32 values sit in one lane's registers and a row of the tile is one
-// coalesced access.  Codes and scales of the 128 columns go through LDS, so
-// that each column's 128-byte line leaves whole.
+// 32-row block w, a lane two neighbouring columns of it, so that a row of the
+// tile is one coalesced access and a column block's 32 values sit in one
+// lane.  Codes and scales of the 128 columns go through LDS, so that each
+// column's 128-byte line leaves whole.
 //
-// BOTH: the row blocks of the same tile (32 columns = 16 lanes) from the same
-// registers: the maximum by DPP over the 16 lanes, one byte of codes a lane
-// and row, gathered in LDS into 64-byte halves of the rows' lines.
+// BOTH: the wave's 32 x 128 values also pass through LDS of its own, sixteen
+// rows at a time, from where a lane takes 32 neighbours of a row -- one row
+// block -- and encodes them like a column's.  (Reducing the rows' maxima
+// across lanes instead costs four times the vector instructions: 62 us for
+// 8192 x 4096 BF16, against 19 us so, the time of the bytes.)
+//
+// BF16 stays packed: maxima by 16-bit integer pairs, codes straight from
+// pairs.
 
 constexpr int kTileCols = 128;
 
-// Maximum over the 16 lanes of a DPP row, left in every lane (rotations by
-// 8, 4, 2, 1).
-__device__ __forceinline__ uint32_t row16_max(uint32_t a) {
-  a = umax(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x128, 0xF, 0xF, true));
-  a = umax(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x124, 0xF, 0xF, true));
-  a = umax(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x122, 0xF, 0xF, true));
-  return umax(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x121, 0xF, 0xF, true));
+// Two neighbouring columns of a row, and a block's 32 values.
+template <class T> struct Pair;
+template <> struct Pair<float> {
+  float a, b;
+  static __device__ __forceinline__ Pair zero() { return {0.0f, 0.0f}; }
+};
+template <> struct Pair<uint16_t> {
+  uint32_t w;
+  static __device__ __forceinline__ Pair zero() { return {0u}; }
+};
+
+template <bool VEC>
+__device__ __forceinline__ Pair<float> load_pair(const float* p, int n) {
+  if constexpr (VEC) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    return {v.x, v.y};
+  } else {
+    return {p[0], n > 1 ? p[1] : 0.0f};
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ Pair<uint16_t> load_pair(const uint16_t* p, int n) {
+  if constexpr (VEC) return {*reinterpret_cast<const uint32_t*>(p)};
+  else return {(uint32_t)p[0] | (n > 1 ? (uint32_t)p[1] << 16 : 0u)};
 }
 
-template <class T, bool VEC, bool BOTH>
-__global__ __launch_bounds__(512) void quant_cols_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
-                                                         uint32_t tiles,
-                                                         uint8_t* __restrict__ codes_c,
-                                                         uint8_t* __restrict__ scales_c,
-                                                         uint8_t* __restrict__ codes_r,
-                                                         uint8_t* __restrict__ scales_r) {
-  __shared__ __attribute__((aligned(16))) uint8_t lc[kTileCols * 128];
-  __shared__ __attribute__((aligned(16))) uint8_t ls[kTileCols * 8];
-  __shared__ __attribute__((aligned(16))) uint8_t lr[BOTH ? 256 * 64 : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t lrs[BOTH ? 256 * 4 : 16];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int64_t c0 = (int64_t)(blockIdx.x % tiles) * kTileCols, gr = blockIdx.x / tiles;
-  const int64_t r0 = gr * kPanel + 32 * wave;
-  const int64_t c = c0 + 2 * lane;
-  float v0[32], v1[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    v0[i] = v1[i] = 0.0f;
-    if (r0 + i < rows) {
-      const T* p = x + (r0 + i) * cols + c;
-      if (VEC) {
-        if (c < cols) Io<T>::load2(p, v0[i], v1[i]);
-      } else {
-        if (c < cols) v0[i] = Io<T>::load1(p);
-        if (c + 1 < cols) v1[i] = Io<T>::load1(p + 1);
-      }
-    }
-  }
+typedef unsigned short ushortx2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  union { uint32_t u; ushortx2 v; } x{a}, y{b};
+  x.v = __builtin_elementwise_max(x.v, y.v);
+  return x.u;
+}
+// Two codes in byte SEL of `old`, from a pair of BF16 values.
+template <int SEL>
+__device__ __forceinline__ uint32_t encode2_bf16(uint32_t old, uint32_t pair, float scale) {
+  union { uint32_t u; bf16x2 v; } x{pair};
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, x.v, scale, SEL);
+}
+__device__ __forceinline__ uint32_t encode8_bf16(const uint32_t (&p)[4], uint32_t byte) {
+  const float s = scale_value(byte);
+  uint32_t w = 0;
+  w = encode2_bf16<0>(w, p[0], s);
+  w = encode2_bf16<1>(w, p[1], s);
+  w = encode2_bf16<2>(w, p[2], s);
+  w = encode2_bf16<3>(w, p[3], s);
+  return byte == 255u ? 0u : w;
+}
+
+// Both columns of a lane: codes (16 bytes) and scale byte of each.
+__device__ __forceinline__ void encode_cols(const Pair<float> (&v)[32], uint4& c0, uint4& c1, uint32_t& b0, uint32_t& b1) {
   uint32_t a0 = 0, a1 = 0;
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    a0 = umax(a0, mag_bits(v0[i]));
-    a1 = umax(a1, mag_bits(v1[i]));
+    a0 = umax(a0, mag_bits(v[i].a));
+    a1 = umax(a1, mag_bits(v[i].b));
   }
-  const uint32_t b0 = scale_byte(a0), b1 = scale_byte(a1);
+  b0 = scale_byte(a0);
+  b1 = scale_byte(a1);
   uint32_t w0[4], w1[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     float e0[8], e1[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      e0[i] = v0[8 * q + i];
-      e1[i] = v1[8 * q + i];
+      e0[i] = v[8 * q + i].a;
+      e1[i] = v[8 * q + i].b;
     }
     w0[q] = encode8(e0, b0);
     w1[q] = encode8(e1, b1);
   }
+  c0 = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+  c1 = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+}
+__device__ __forceinline__ void encode_cols(const Pair<uint16_t> (&v)[32], uint4& c0, uint4& c1, uint32_t& b0,
+                                            uint32_t& b1) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) a = max_u16x2(a, v[i].w & 0x7FFF7FFFu);
+  b0 = scale_byte(a << 16);
+  b1 = scale_byte(a & 0xFFFF0000u);
+  uint32_t w0[4], w1[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t e0[4], e1[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {        // rows 2 i and 2 i + 1 of either column
+      const uint32_t lo = v[8 * q + 2 * i].w, hi = v[8 * q + 2 * i + 1].w;
+      e0[i] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+      e1[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+    }
+    w0[q] = encode8_bf16(e0, b0);
+    w1[q] = encode8_bf16(e1, b1);
+  }
+  c0 = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+  c1 = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+}
+
+// A row block of 32 neighbours in LDS.
+__device__ __forceinline__ void encode_row(const float* p, uint4& c, uint32_t& byte) {
+  float v[32];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float4 f = *reinterpret_cast<const float4*>(p + 4 * q);
+    v[4 * q] = f.x; v[4 * q + 1] = f.y; v[4 * q + 2] = f.z; v[4 * q + 3] = f.w;
+  }
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) a = umax(a, mag_bits(v[i]));
+  byte = scale_byte(a);
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = v[8 * q + i];
+    w[q] = encode8(e, byte);
+  }
+  c = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void encode_row(const uint16_t* p, uint4& c, uint32_t& byte) {
+  uint32_t v[4][4];
+  uint32_t a = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint4 f = *reinterpret_cast<const uint4*>(p + 8 * q);
+    v[q][0] = f.x; v[q][1] = f.y; v[q][2] = f.z; v[q][3] = f.w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a = max_u16x2(a, v[q][i] & 0x7FFF7FFFu);
+  }
+  byte = scale_byte(umax(a << 16, a & 0xFFFF0000u));
+  c = make_uint4(encode8_bf16(v[0], byte), encode8_bf16(v[1], byte), encode8_bf16(v[2], byte), encode8_bf16(v[3], byte));
+}
+
+// Orders a wave's own LDS writes before its reads of other lanes' values.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <class T, bool VEC, bool BOTH>
+__global__ __launch_bounds__(512) void quant_cols_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
+                                                         uint32_t tiles, uint8_t* __restrict__ codes_c,
+                                                         uint8_t* __restrict__ scales_c,
+                                                         uint8_t* __restrict__ codes_r,
+                                                         uint8_t* __restrict__ scales_r) {
+  constexpr int kPitch = kTileCols * (int)sizeof(T) + 16;      // spreads a lane quad's rows over the banks
+  __shared__ __attribute__((aligned(16))) uint8_t lc[kTileCols * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t ls[kTileCols * 8];
+  __shared__ __attribute__((aligned(16))) uint8_t lr[BOTH ? 8 * 16 * kPitch : 16];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int64_t c0 = (int64_t)(blockIdx.x % tiles) * kTileCols, gr = blockIdx.x / tiles;
+  const int64_t r0 = gr * kPanel + 32 * wave;
+  const int64_t c = c0 + 2 * lane;
+  Pair<T> v[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    v[i] = Pair<T>::zero();
+    if (r0 + i < rows && c < cols) v[i] = load_pair<VEC>(x + (r0 + i) * cols + c, (int)(cols - c < 2 ? 1 : 2));
+  }
+  uint4 w0, w1;
+  uint32_t b0, b1;
+  encode_cols(v, w0, w1, b0, b1);
   // column j's line: chunk `wave` at position wave ^ (j / 2 % 8), so that the
   // 64 lanes' 16-byte writes spread over the banks
   const int pos = 16 * (wave ^ (lane & 7));
-  *reinterpret_cast<uint4*>(lc + (2 * lane) * 128 + pos) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-  *reinterpret_cast<uint4*>(lc + (2 * lane + 1) * 128 + pos) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+  *reinterpret_cast<uint4*>(lc + (2 * lane) * 128 + pos) = w0;
+  *reinterpret_cast<uint4*>(lc + (2 * lane + 1) * 128 + pos) = w1;
   ls[(2 * lane) * 8 + wave] = (uint8_t)b0;
   ls[(2 * lane + 1) * 8 + wave] = (uint8_t)b1;
   if constexpr (BOTH) {
+    uint8_t* buf = lr + wave * 16 * kPitch;
+    const int64_t gc = c0 / kPanel;
+    const int half = (int)(c0 / kTileCols) & 1;     // which half of the rows' panel
+    const int r = lane >> 2, b = lane & 3;          // row of sixteen, block of four
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const uint32_t b = scale_byte(row16_max(umax(mag_bits(v0[i]), mag_bits(v1[i]))));
-      const uint32_t w = encode2<0>(0u, v0[i], v1[i], scale_value(b));
-      lr[(32 * wave + i) * 64 + lane] = (uint8_t)(b == 255u ? 0u : w);
-      if ((lane & 15) == 0) lrs[(32 * wave + i) * 4 + (lane >> 4)] = (uint8_t)b;
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) *reinterpret_cast<Pair<T>*>(buf + i * kPitch + (int)sizeof(Pair<T>) * lane) = v[16 * k + i];
+      wave_sync();
+      uint4 w;
+      uint32_t byte;
+      encode_row(reinterpret_cast<const T*>(buf + r * kPitch) + 32 * b, w, byte);
+      // the quad's four bytes in its first lane
+      uint32_t quad = byte;
+      quad |= (uint32_t)__builtin_amdgcn_mov_dpp((int)quad, 0xB1, 0xF, 0xF, true) << 8;    // lanes 0 and 2: own | next << 8
+      quad = (quad & 0xFFFFu) | (uint32_t)__builtin_amdgcn_mov_dpp((int)quad, 0x4E, 0xF, 0xF, true) << 16;
+      const int64_t row = r0 + 16 * k + r;
+      if (row < rows) {
+        *reinterpret_cast<uint4*>(codes_r + (gc * rows + row) * kPanelBytes + 64 * half + 16 * b) = w;
+        if (b == 0) *reinterpret_cast<uint32_t*>(scales_r + (gc * rows + row) * kPanelScales + 4 * half) = quad;
+      }
+      wave_sync();
     }
   }
   __syncthreads();
@@ -238,20 +356,6 @@ __global__ __launch_bounds__(512) void quant_cols_kernel(const T* __restrict__ x
   if (t < kTileCols && c0 + t < cols)
     *reinterpret_cast<uint2*>(scales_c + (gr * cols + c0 + t) * kPanelScales) =
         *reinterpret_cast<const uint2*>(ls + t * 8);
-  if constexpr (BOTH) {
-    const int64_t gc = c0 / kPanel;
-    const int half = (int)(c0 / kTileCols) & 1;       // which half of the row's panel
-    for (int k = t; k < 256 * 4; k += 512) {
-      const int r = k >> 2, p = k & 3;
-      const int64_t row = gr * kPanel + r;
-      if (row < rows)
-        *reinterpret_cast<uint4*>(codes_r + (gc * rows + row) * kPanelBytes + 64 * half + 16 * p) =
-            *reinterpret_cast<const uint4*>(lr + r * 64 + 16 * p);
-    }
-    if (t < 256 && gr * kPanel + t < rows)
-      *reinterpret_cast<uint32_t*>(scales_r + (gc * rows + gr * kPanel + t) * kPanelScales + 4 * half) =
-          *reinterpret_cast<const uint32_t*>(lrs + t * 4);
-  }
 }
 
 template <class T, bool VEC>
