@@ -16,6 +16,7 @@ Functions carry the C names:
     mxfp4_linear, mxfp4_linear_backward,
     ns_f16_workspace_bytes, ns_orthogonalize_f16, ns_orthogonalize_f16_grouped, ns_muon_step
 """
+import contextlib
 import ctypes
 import os
 
@@ -136,9 +137,22 @@ def _torch():
 def _stream(stream, device=None):
     """The stream to enqueue on: `stream`, else the current stream of the
     tensors' device."""
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    if device is None or device.index is None:
+        return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # the handle itself: building a Stream object costs 2 us a call
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device):
+    """Makes `device` the current one (nothing to do where it is already)."""
+    torch = _torch()
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _dt(t):
@@ -664,15 +678,13 @@ def mxfp4_quantize(x, axis=NVFP4_ROWS, codes=None, scales=None, stream=None):
     (NVFP4_ROWS, r = rows) or of x^T (NVFP4_COLS, r = columns), panels of 256
     elements along the blocked axis.
     """
-    torch = _torch()
-    _need_cuda(x)
     _need_2d(x, "x")
     rows, cols = x.shape
     r, c = (rows, cols) if axis == NVFP4_ROWS else (cols, rows)
     codes, scales = _mx_buffers(r, c, codes, scales, x.device)
     _need_cuda(x, codes, scales)
     _need_mx(codes, scales, "out", r, c)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         _check(_lib.mxfp4_quantize(_ptr(x), _dt(x), rows, cols, axis, _ptr(codes), _ptr(scales),
                                    _stream(stream, x.device)), "mxfp4_quantize")
     return codes, scales
@@ -681,8 +693,6 @@ def mxfp4_quantize(x, axis=NVFP4_ROWS, codes=None, scales=None, stream=None):
 def mxfp4_quantize_both(x, along=None, down=None, stream=None):
     """Both quantizations of x in one pass: ((codes, scales) of NVFP4_ROWS,
     (codes, scales) of NVFP4_COLS)."""
-    torch = _torch()
-    _need_cuda(x)
     _need_2d(x, "x")
     rows, cols = x.shape
     rc, rs = _mx_buffers(rows, cols, *(along or (None, None)), x.device)
@@ -690,7 +700,7 @@ def mxfp4_quantize_both(x, along=None, down=None, stream=None):
     _need_cuda(x, rc, rs, cc, cs)
     _need_mx(rc, rs, "along", rows, cols)
     _need_mx(cc, cs, "down", cols, rows)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         _check(_lib.mxfp4_quantize_both(_ptr(x), _dt(x), rows, cols, _ptr(rc), _ptr(rs), _ptr(cc),
                                         _ptr(cs), _stream(stream, x.device)), "mxfp4_quantize_both")
     return (rc, rs), (cc, cs)
@@ -706,7 +716,7 @@ def mxfp4_dequantize(codes, scales, rows, cols, axis=NVFP4_ROWS, out_dtype=NS_F3
     r, c = (rows, cols) if axis == NVFP4_ROWS else (cols, rows)
     _need_mx(codes, scales, "in", r, c)
     _need(out, "out", _floats(), rows * cols)
-    with torch.cuda.device(codes.device):
+    with _on(codes.device):
         _check(_lib.mxfp4_dequantize(_ptr(codes), _ptr(scales), rows, cols, axis, _ptr(out), _dt(out),
                                      _stream(stream, codes.device)), "mxfp4_dequantize")
     return out
@@ -732,20 +742,19 @@ def mxfp4_gemm(p, q, M, N, K, alpha=1.0, beta=0.0, addend=None, out_dtype=NS_F32
     allocated when none is given."""
     torch = _torch()
     (pc, ps), (qc, qs) = p, q
-    _need_cuda(pc, ps, qc, qs, addend, out)
     dev = pc.device
     if out is None:
         out = torch.empty((M, N), dtype=_out_dtype(out_dtype), device=dev)
     if workspace is not None or split:
         workspace = _mx_workspace(mxfp4_gemm_workspace_bytes(M, N, K), workspace, dev)
-    _need_cuda(pc, workspace)
+    _need_cuda(pc, ps, qc, qs, addend, out, workspace)
     _need_mx(pc, ps, "p", M, K)
     _need_mx(qc, qs, "q", N, K)
     _need(out, "out", _floats(), M * N)
     if float(beta) != 0.0:
         _need(addend, "addend", (torch.float32,), M * N)
     wsp, wsn = (_ptr(workspace), workspace.numel()) if workspace is not None else (_ptr(None), 0)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(_lib.mxfp4_gemm(_ptr(pc), _ptr(ps), _ptr(qc), _ptr(qs), M, N, K, float(alpha),
                                float(beta), _ptr(addend), _ptr(out), _dt(out), wsp, wsn,
                                _stream(stream, dev)), "mxfp4_gemm")
@@ -768,7 +777,6 @@ def mxfp4_linear(x, w, N, out=None, keep=False, kept=None, workspace=None, strea
     and returns (y, kept), kept = (codes, scales) for mxfp4_linear_backward."""
     torch = _torch()
     wc, ws_ = w
-    _need_cuda(x, wc, ws_, out)
     _need_2d(x, "x")
     T, K = x.shape
     dev = x.device
@@ -776,12 +784,12 @@ def mxfp4_linear(x, w, N, out=None, keep=False, kept=None, workspace=None, strea
         out = torch.empty((T, N), dtype=x.dtype, device=dev)
     kc, ks = _mx_buffers(K, T, *(kept or (None, None)), dev) if keep or kept else (None, None)
     workspace = _mx_workspace(mxfp4_linear_workspace_bytes(T, N, K), workspace, dev)
-    _need_cuda(x, kc, ks, workspace)
+    _need_cuda(x, wc, ws_, out, kc, ks, workspace)
     _need_mx(wc, ws_, "w", N, K)
     _need(out, "out", _floats(), T * N)
     if kc is not None:
         _need_mx(kc, ks, "kept", K, T)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(_lib.mxfp4_linear(_ptr(x), _dt(x), T, K, _ptr(wc), _ptr(ws_), N, _ptr(out), _dt(out),
                                  _ptr(kc), _ptr(ks), _ptr(workspace), workspace.numel(),
                                  _stream(stream, dev)), "mxfp4_linear")
@@ -797,7 +805,6 @@ def mxfp4_linear_backward(dy, wt, kept, K, dx=None, dw=None, need_dx=True, need_
     returned in its place).  dw = beta * dw + gradient (beta != 0 needs a
     float32 `dw`); new tensors take dy's dtype."""
     torch = _torch()
-    _need_cuda(dy, dx, dw)
     _need_2d(dy, "dy")
     T, N = dy.shape
     dev = dy.device
@@ -810,14 +817,14 @@ def mxfp4_linear_backward(dy, wt, kept, K, dx=None, dw=None, need_dx=True, need_
     dx, dw = dx if need_dx else None, dw if need_dw else None
     (wc, ws_), (kc, ks) = wt if need_dx else (None, None), kept if need_dw else (None, None)
     workspace = _mx_workspace(mxfp4_linear_backward_workspace_bytes(T, N, K), workspace, dev)
-    _need_cuda(dy, wc, ws_, kc, ks, workspace)
+    _need_cuda(dy, dx, dw, wc, ws_, kc, ks, workspace)
     if need_dx:
         _need_mx(wc, ws_, "wt", K, N)
         _need(dx, "dx", _floats(), T * K)
     if need_dw:
         _need_mx(kc, ks, "kept", K, T)
         _need(dw, "dw", _floats(), N * K)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(_lib.mxfp4_linear_backward(_ptr(dy), _dt(dy), T, N, K, _ptr(wc), _ptr(ws_), _ptr(kc),
                                           _ptr(ks), _ptr(dx), _dt(dx) if need_dx else NS_F32, _ptr(dw),
                                           _dt(dw) if need_dw else NS_F32, float(beta),
@@ -857,7 +864,7 @@ def ns_orthogonalize_f16(G, coeffs, clip=float("inf"), out_dtype=NS_F32, out=Non
     workspace = _mx_workspace(ns_f16_workspace_bytes([(m, n)]), workspace, G.device)
     _need_ns(G, out, workspace)
     carr, k = _coeff_array(coeffs)
-    with torch.cuda.device(G.device):
+    with _on(G.device):
         _check(_lib.ns_orthogonalize_f16(_ptr(G), _dt(G), m, n, carr, k, float(clip), _ptr(out),
                                          _dt(out), _ptr(workspace), workspace.numel(),
                                          _stream(stream, G.device)), "ns_orthogonalize_f16")
@@ -887,7 +894,7 @@ def ns_orthogonalize_f16_grouped(Gs, coeffs, clips=None, out_dtype=NS_F32, outs=
     ms, ns_ = _shape_arrays(shapes)
     cl = (ctypes.c_float * cnt)(*[float(c) for c in clips]) if clips is not None else None
     carr, k = _coeff_array(coeffs)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(_lib.ns_orthogonalize_f16_grouped(cnt, _pointers(Gs), ms, ns_, dt, carr, k, cl,
                                                  _pointers(outs), _dt(outs[0]), _ptr(workspace),
                                                  workspace.numel(), _stream(stream, dev)),
@@ -922,7 +929,7 @@ def ns_muon_step(Ws, Ms, Gs, coeffs, lr, momentum=0.95, weight_decay=0.0, nester
     sc = (ctypes.c_float * cnt)(*[float(c) for c in scales]) if scales is not None else None
     carr, k = _coeff_array(coeffs)
     opt = NsMuonOptions(float(lr), float(momentum), float(weight_decay), 1 if nesterov else 0)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(_lib.ns_muon_step(cnt, _pointers(Ws), _dt(Ws[0]), _pointers(Ms), _dt(Ms[0]),
                                  _pointers(Gs), _dt(Gs[0]), ms, ns_, carr, k, ctypes.byref(opt), sc,
                                  _ptr(workspace), workspace.numel(), _stream(stream, dev)),

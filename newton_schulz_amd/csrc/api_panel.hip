@@ -44,7 +44,18 @@ PanelProblem mx_product(const uint8_t* pc, const uint8_t* ps, const uint8_t* qc,
 }
 
 inline PanelPlan mx_plan(int64_t M, int64_t N, int64_t K, bool split) {
+  if (M <= nvfp4::kMxFewRows) return PanelPlan{};      // launch_mx_few: no plan, no workspace
   return nvfp4::plan_panel(M, N, mx_panels(K), false, 1, split, false);
+}
+
+// One product of operands in MXFP4, whichever way its rows call for.
+hipError_t mx_multiply(const uint8_t* pc, const uint8_t* ps, const uint8_t* qc, const uint8_t* qs, int64_t M, int64_t N,
+                       int64_t K, float alpha, float beta, const float* addend, void* out, Dt ot, void* ws,
+                       hipStream_t s) {
+  if (M <= nvfp4::kMxFewRows)
+    return nvfp4::launch_mx_few(pc, Dt::F32, ps, M, K, qc, qs, N, alpha, beta, beta != 0.0f ? addend : nullptr, out, ot, s);
+  return nvfp4::launch_panel(mx_product(pc, ps, qc, qs, M, N, K, alpha, beta, addend, out, ot),
+                             mx_plan(M, N, K, ws != nullptr), true, ws, s);
 }
 
 }  // namespace
@@ -124,8 +135,8 @@ ns_status mxfp4_gemm(const uint8_t* codes_p, const uint8_t* scales_p, const uint
       Q{codes_q, mx_codes(N, K)}, QS{scales_q, mx_scales(N, K)},
       A{beta != 0.0f && !in_place ? addend : nullptr, mn * sizeof(float)}, W{ws, ws ? ws_bytes : 0};
   if (hits(O, {P, PS, Q, QS, A, W}) || hits(W, {P, PS, Q, QS, A})) return NS_ERR_ARG;
-  NS_TRY(nvfp4::launch_panel(mx_product(codes_p, scales_p, codes_q, scales_q, M, N, K, alpha, beta, addend, out, (Dt)ot),
-                             plan, true, ws, as_stream(stream)));
+  NS_TRY(mx_multiply(codes_p, scales_p, codes_q, scales_q, M, N, K, alpha, beta, addend, out, (Dt)ot, ws,
+                     as_stream(stream)));
   return NS_OK;
 }
 
@@ -142,6 +153,7 @@ struct LinearLayout {
 };
 LinearLayout forward_layout(int64_t T, int64_t N, int64_t K) {
   LinearLayout L{};
+  if (T <= nvfp4::kMxFewRows) return L;    // quantized in the product's registers
   size_t o = 0;
   auto take = [&](size_t b) { const size_t at = o; o = align_up(o + b); return at; };
   L.c0 = take(mx_codes(T, K));
@@ -180,21 +192,26 @@ ns_status mxfp4_linear(const void* x, ns_dtype xt, int64_t T, int64_t K, const u
   if ((kept_codes == nullptr) != (kept_scales == nullptr)) return NS_ERR_ARG;
   if (!mx_dim(T) || !mx_dim(N) || !mx_dim(K)) return NS_ERR_SHAPE;
   const LinearLayout L = forward_layout(T, N, K);
-  if (!ws || ws_bytes < L.total) return NS_ERR_WORKSPACE;
+  if (ws_bytes < L.total || (L.total && !ws)) return NS_ERR_WORKSPACE;
   if (!al(x, 16) || !al(w_codes, 16) || !al(w_scales, 16) || !al(y, 16) || !al(kept_codes, 16) ||
       !al(kept_scales, 16) || !al(ws, 16))
     return NS_ERR_ARG;
   const Span X{x, (size_t)(T * K) * dtype_size(xt)}, W{w_codes, mx_codes(N, K)}, WS{w_scales, mx_scales(N, K)},
       Y{y, (size_t)(T * N) * dtype_size(yt)}, C{kept_codes, mx_codes(K, T)}, S{kept_scales, mx_scales(K, T)},
-      Z{ws, ws_bytes};
+      Z{ws, ws ? ws_bytes : 0};
   if (hits(Y, {X, W, WS, C, S, Z}) || hits(C, {X, W, WS, S, Z}) || hits(S, {X, W, WS, Z}) || hits(Z, {X, W, WS}))
     return NS_ERR_ARG;
   hipStream_t s = as_stream(stream);
   uint8_t* b = static_cast<uint8_t*>(ws);
+  if (T <= nvfp4::kMxFewRows) {
+    if (kept_codes)
+      NS_TRY(nvfp4::launch_mx_quantize(x, (Dt)xt, T, K, nvfp4::kMxCols, nullptr, nullptr, kept_codes, kept_scales, s));
+    NS_TRY(nvfp4::launch_mx_few(x, (Dt)xt, nullptr, T, K, w_codes, w_scales, N, 1.0f, 0.0f, nullptr, y, (Dt)yt, s));
+    return NS_OK;
+  }
   NS_TRY(nvfp4::launch_mx_quantize(x, (Dt)xt, T, K, kept_codes ? nvfp4::kMxRows | nvfp4::kMxCols : nvfp4::kMxRows,
                                    b + L.c0, b + L.s0, kept_codes, kept_scales, s));
-  NS_TRY(nvfp4::launch_panel(mx_product(b + L.c0, b + L.s0, w_codes, w_scales, T, N, K, 1.0f, 0.0f, nullptr, y, (Dt)yt),
-                             mx_plan(T, N, K, true), true, b + L.part, s));
+  NS_TRY(mx_multiply(b + L.c0, b + L.s0, w_codes, w_scales, T, N, K, 1.0f, 0.0f, nullptr, y, (Dt)yt, b + L.part, s));
   return NS_OK;
 }
 
@@ -228,12 +245,10 @@ ns_status mxfp4_linear_backward(const void* dy, ns_dtype dyt, int64_t T, int64_t
   NS_TRY(nvfp4::launch_mx_quantize(dy, (Dt)dyt, T, N, (dx ? nvfp4::kMxRows : 0) | (dw ? nvfp4::kMxCols : 0), b + L.c0,
                                    b + L.s0, b + L.c1, b + L.s1, s));
   if (dx)
-    NS_TRY(nvfp4::launch_panel(mx_product(b + L.c0, b + L.s0, wt_codes, wt_scales, T, K, N, 1.0f, 0.0f, nullptr, dx, (Dt)dxt),
-                               mx_plan(T, K, N, true), true, b + L.part, s));
+    NS_TRY(mx_multiply(b + L.c0, b + L.s0, wt_codes, wt_scales, T, K, N, 1.0f, 0.0f, nullptr, dx, (Dt)dxt, b + L.part, s));
   if (dw)
-    NS_TRY(nvfp4::launch_panel(mx_product(b + L.c1, b + L.s1, kept_codes, kept_scales, N, K, T, 1.0f, beta,
-                                          static_cast<const float*>(dw), dw, (Dt)dwt),
-                               mx_plan(N, K, T, true), true, b + L.part, s));
+    NS_TRY(mx_multiply(b + L.c1, b + L.s1, kept_codes, kept_scales, N, K, T, 1.0f, beta, static_cast<const float*>(dw), dw,
+                       (Dt)dwt, b + L.part, s));
   return NS_OK;
 }
 

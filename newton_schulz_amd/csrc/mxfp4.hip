@@ -178,28 +178,6 @@ __device__ __forceinline__ Pair<uint16_t> load_pair(const uint16_t* p, int n) {
   else return {(uint32_t)p[0] | (n > 1 ? (uint32_t)p[1] << 16 : 0u)};
 }
 
-typedef unsigned short ushortx2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  union { uint32_t u; ushortx2 v; } x{a}, y{b};
-  x.v = __builtin_elementwise_max(x.v, y.v);
-  return x.u;
-}
-// Two codes in byte SEL of `old`, from a pair of BF16 values.
-template <int SEL>
-__device__ __forceinline__ uint32_t encode2_bf16(uint32_t old, uint32_t pair, float scale) {
-  union { uint32_t u; bf16x2 v; } x{pair};
-  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, x.v, scale, SEL);
-}
-__device__ __forceinline__ uint32_t encode8_bf16(const uint32_t (&p)[4], uint32_t byte) {
-  const float s = scale_value(byte);
-  uint32_t w = 0;
-  w = encode2_bf16<0>(w, p[0], s);
-  w = encode2_bf16<1>(w, p[1], s);
-  w = encode2_bf16<2>(w, p[2], s);
-  w = encode2_bf16<3>(w, p[3], s);
-  return byte == 255u ? 0u : w;
-}
-
 // Both columns of a lane: codes (16 bytes) and scale byte of each.
 __device__ __forceinline__ void encode_cols(const Pair<float> (&v)[32], uint4& c0, uint4& c1, uint32_t& b0, uint32_t& b1) {
   uint32_t a0 = 0, a1 = 0;

@@ -82,5 +82,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r.u;
 }
 
+// BF16 in pairs, as they lie in memory: maxima by 16-bit integers, codes
+// without widening.
+typedef unsigned short ushortx2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  union { uint32_t u; ushortx2 v; } x{a}, y{b};
+  x.v = __builtin_elementwise_max(x.v, y.v);
+  return x.u;
+}
+// Two codes in byte SEL of `old`, from a pair of BF16 values.
+template <int SEL>
+__device__ __forceinline__ uint32_t encode2_bf16(uint32_t old, uint32_t pair, float scale) {
+  union { uint32_t u; bf16x2 v; } x{pair};
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, x.v, scale, SEL);
+}
+__device__ __forceinline__ uint32_t encode8_bf16(const uint32_t (&p)[4], uint32_t byte) {
+  const float s = scale_value(byte);
+  uint32_t w = 0;
+  w = encode2_bf16<0>(w, p[0], s);
+  w = encode2_bf16<1>(w, p[1], s);
+  w = encode2_bf16<2>(w, p[2], s);
+  w = encode2_bf16<3>(w, p[3], s);
+  return byte == 255u ? 0u : w;
+}
+
 }  // namespace mx
 }  // namespace nvfp4

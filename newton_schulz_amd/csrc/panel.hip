@@ -620,16 +620,16 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks* C::kWaves / 4) void panel_
   auto wait_loads = [&] { asm volatile("s_waitcnt vmcnt(%0)" ::"n"((C::NST - 2) * kLoads) : "memory"); };
 
   // NST - 1 stages in flight before the first is read, then always NST
-#pragma unroll
-  for (int s = 0; s < C::NST; ++s) {
-    if (s == C::NST - 1) {
-      wait_loads();
-      __builtin_amdgcn_s_barrier();
-    }
+#pragma unroll 1
+  for (int s = 0; s < C::NST - 1; ++s) {
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) next.load(lds0 + s * kStage, wave, k);
-    if (s < C::NST - 1) next.advance(a, run, wave, lane);
+    next.advance(a, run, wave, lane);
   }
+  wait_loads();
+  __builtin_amdgcn_s_barrier();
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) next.load(lds0 + (C::NST - 1) * kStage, wave, k);
 #pragma unroll
   for (int k = 0; k < kReads; ++k) {
     if constexpr (FP4) read_scale<C>(smem, soff, wm, wn, k, sc);

@@ -67,6 +67,17 @@ hipError_t launch_mx_quantize(const void* x, Dt xt, int64_t rows, int64_t cols, 
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, bool down,
                                 void* out, Dt ot, hipStream_t s);
 
+// ---- MXFP4 products with few rows (mxfp4_few.hip) -------------------------------
+// Up to this many rows of x a product reads w once, in one launch; above, the
+// tiled product's reuse of w counts (32 x 11008 x 4096 BF16: see DESIGN notes
+// at the kernel).
+constexpr int64_t kMxFewRows = 32;
+// out[T][N] = beta addend + alpha x w^T; x [T][K] FP32 or BF16, quantized along
+// K, or codes with x_scales (then xt is not used).  addend null: none.
+hipError_t launch_mx_few(const void* x, Dt xt, const uint8_t* x_scales, int64_t T, int64_t K, const uint8_t* w,
+                         const uint8_t* w_scales, int64_t N, float alpha, float beta, const float* addend, void* out,
+                         Dt ot, hipStream_t s);
+
 // ---- 16-bit Newton–Schulz prologue (ns16.hip) --------------------------------
 constexpr int kNs16Parts = 256;     // partial sums of squares per matrix
 struct Ns16Inputs {                 // host pointer tables of one batch, by value
