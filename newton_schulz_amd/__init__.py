@@ -727,11 +727,16 @@ def mxfp4_gemm_workspace_bytes(M, N, K):
 
 
 def _mx_workspace(need, workspace, dev):
+    """The given workspace, or a new one where the call needs any."""
     torch = _torch()
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _need(workspace, "workspace", (torch.uint8,), 0)
     return workspace
+
+
+def _ws_args(workspace):
+    return (_ptr(None), 0) if workspace is None else (_ptr(workspace), workspace.numel())
 
 
 def mxfp4_gemm(p, q, M, N, K, alpha=1.0, beta=0.0, addend=None, out_dtype=NS_F32, out=None,
@@ -753,11 +758,10 @@ def mxfp4_gemm(p, q, M, N, K, alpha=1.0, beta=0.0, addend=None, out_dtype=NS_F32
     _need(out, "out", _floats(), M * N)
     if float(beta) != 0.0:
         _need(addend, "addend", (torch.float32,), M * N)
-    wsp, wsn = (_ptr(workspace), workspace.numel()) if workspace is not None else (_ptr(None), 0)
     with _on(dev):
         _check(_lib.mxfp4_gemm(_ptr(pc), _ptr(ps), _ptr(qc), _ptr(qs), M, N, K, float(alpha),
-                               float(beta), _ptr(addend), _ptr(out), _dt(out), wsp, wsn,
-                               _stream(stream, dev)), "mxfp4_gemm")
+                               float(beta), _ptr(addend), _ptr(out), _dt(out),
+                               *_ws_args(workspace), _stream(stream, dev)), "mxfp4_gemm")
     return out
 
 
@@ -791,7 +795,7 @@ def mxfp4_linear(x, w, N, out=None, keep=False, kept=None, workspace=None, strea
         _need_mx(kc, ks, "kept", K, T)
     with _on(dev):
         _check(_lib.mxfp4_linear(_ptr(x), _dt(x), T, K, _ptr(wc), _ptr(ws_), N, _ptr(out), _dt(out),
-                                 _ptr(kc), _ptr(ks), _ptr(workspace), workspace.numel(),
+                                 _ptr(kc), _ptr(ks), *_ws_args(workspace),
                                  _stream(stream, dev)), "mxfp4_linear")
     return (out, (kc, ks)) if kc is not None else out
 
@@ -828,7 +832,7 @@ def mxfp4_linear_backward(dy, wt, kept, K, dx=None, dw=None, need_dx=True, need_
         _check(_lib.mxfp4_linear_backward(_ptr(dy), _dt(dy), T, N, K, _ptr(wc), _ptr(ws_), _ptr(kc),
                                           _ptr(ks), _ptr(dx), _dt(dx) if need_dx else NS_F32, _ptr(dw),
                                           _dt(dw) if need_dw else NS_F32, float(beta),
-                                          _ptr(workspace), workspace.numel(), _stream(stream, dev)),
+                                          *_ws_args(workspace), _stream(stream, dev)),
                "mxfp4_linear_backward")
     return dx, dw
 
@@ -866,7 +870,7 @@ def ns_orthogonalize_f16(G, coeffs, clip=float("inf"), out_dtype=NS_F32, out=Non
     carr, k = _coeff_array(coeffs)
     with _on(G.device):
         _check(_lib.ns_orthogonalize_f16(_ptr(G), _dt(G), m, n, carr, k, float(clip), _ptr(out),
-                                         _dt(out), _ptr(workspace), workspace.numel(),
+                                         _dt(out), *_ws_args(workspace),
                                          _stream(stream, G.device)), "ns_orthogonalize_f16")
     return out
 
@@ -896,8 +900,7 @@ def ns_orthogonalize_f16_grouped(Gs, coeffs, clips=None, out_dtype=NS_F32, outs=
     carr, k = _coeff_array(coeffs)
     with _on(dev):
         _check(_lib.ns_orthogonalize_f16_grouped(cnt, _pointers(Gs), ms, ns_, dt, carr, k, cl,
-                                                 _pointers(outs), _dt(outs[0]), _ptr(workspace),
-                                                 workspace.numel(), _stream(stream, dev)),
+                                                 _pointers(outs), _dt(outs[0]), *_ws_args(workspace), _stream(stream, dev)),
                "ns_orthogonalize_f16_grouped")
     return outs
 
@@ -932,6 +935,6 @@ def ns_muon_step(Ws, Ms, Gs, coeffs, lr, momentum=0.95, weight_decay=0.0, nester
     with _on(dev):
         _check(_lib.ns_muon_step(cnt, _pointers(Ws), _dt(Ws[0]), _pointers(Ms), _dt(Ms[0]),
                                  _pointers(Gs), _dt(Gs[0]), ms, ns_, carr, k, ctypes.byref(opt), sc,
-                                 _ptr(workspace), workspace.numel(), _stream(stream, dev)),
+                                 *_ws_args(workspace), _stream(stream, dev)),
                "ns_muon_step")
     return Ws

@@ -44,7 +44,7 @@ PanelProblem mx_product(const uint8_t* pc, const uint8_t* ps, const uint8_t* qc,
 }
 
 inline PanelPlan mx_plan(int64_t M, int64_t N, int64_t K, bool split) {
-  if (M <= nvfp4::kMxFewRows) return PanelPlan{};      // launch_mx_few: no plan, no workspace
+  if (nvfp4::mx_few(M, N, K)) return PanelPlan{};      // launch_mx_few: no plan, no workspace
   return nvfp4::plan_panel(M, N, mx_panels(K), false, 1, split, false);
 }
 
@@ -52,7 +52,7 @@ inline PanelPlan mx_plan(int64_t M, int64_t N, int64_t K, bool split) {
 hipError_t mx_multiply(const uint8_t* pc, const uint8_t* ps, const uint8_t* qc, const uint8_t* qs, int64_t M, int64_t N,
                        int64_t K, float alpha, float beta, const float* addend, void* out, Dt ot, void* ws,
                        hipStream_t s) {
-  if (M <= nvfp4::kMxFewRows)
+  if (nvfp4::mx_few(M, N, K))
     return nvfp4::launch_mx_few(pc, Dt::F32, ps, M, K, qc, qs, N, alpha, beta, beta != 0.0f ? addend : nullptr, out, ot, s);
   return nvfp4::launch_panel(mx_product(pc, ps, qc, qs, M, N, K, alpha, beta, addend, out, ot),
                              mx_plan(M, N, K, ws != nullptr), true, ws, s);
@@ -153,7 +153,7 @@ struct LinearLayout {
 };
 LinearLayout forward_layout(int64_t T, int64_t N, int64_t K) {
   LinearLayout L{};
-  if (T <= nvfp4::kMxFewRows) return L;    // quantized in the product's registers
+  if (nvfp4::mx_few(T, N, K)) return L;    // quantized in the product's registers
   size_t o = 0;
   auto take = [&](size_t b) { const size_t at = o; o = align_up(o + b); return at; };
   L.c0 = take(mx_codes(T, K));
@@ -203,7 +203,7 @@ ns_status mxfp4_linear(const void* x, ns_dtype xt, int64_t T, int64_t K, const u
     return NS_ERR_ARG;
   hipStream_t s = as_stream(stream);
   uint8_t* b = static_cast<uint8_t*>(ws);
-  if (T <= nvfp4::kMxFewRows) {
+  if (nvfp4::mx_few(T, N, K)) {
     if (kept_codes)
       NS_TRY(nvfp4::launch_mx_quantize(x, (Dt)xt, T, K, nvfp4::kMxCols, nullptr, nullptr, kept_codes, kept_scales, s));
     NS_TRY(nvfp4::launch_mx_few(x, (Dt)xt, nullptr, T, K, w_codes, w_scales, N, 1.0f, 0.0f, nullptr, y, (Dt)yt, s));

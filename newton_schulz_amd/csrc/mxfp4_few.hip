@@ -1,16 +1,16 @@
 // MXFP4 products with few rows on one side: out[t][n] = beta addend + alpha
-// sum_k x[t][k] w[n][k] for T <= 32 rows x, quantized on the way in (the
+// sum_k x[t][k] w[n][k] for up to 32 rows of x, quantized on the way in (the
 // linear layer's decode) or held in MXFP4 already.
 //
 // What counts is reading w once.  A workgroup takes 16 rows of w, its waves
-// divide the panels of K and have all their loads of w -- four panels, 8 KB a
-// wave -- in flight before anything waits; meanwhile the lanes quantize the
-// blocks of x that they multiply: in v_mfma_scale_f32_16x16x128 lane l holds
-// one 32-element block of row l % 16, so a block's values, scale and codes
-// never leave their lane.  The waves' sums meet in LDS, in wave order.
+// divide the panels of K and have their loads of w -- up to four panels, 8 KB
+// a wave -- in flight before anything waits; meanwhile a wave quantizes its
+// panels of x, a lane one 32-element block at a time, into LDS of its own.  In
+// v_mfma_scale_f32_16x16x128 lane l holds one block of row l % 16 of either
+// operand.  The waves' sums meet in LDS, in wave order.
 //
-// Measured, 1 x 11008 x 4096 BF16: 5.9 us (24 MB of weights; quantizing x and
-// a tiled product take 3 + 9 us and two launches).
+// Measured in a graph, x in BF16: 1 x 11008 x 4096 6.2 us (24 MB of weights and
+// scales, 3.9 TB/s with the launch in it), 16 x 4096 x 4096 6.2 us.
 #include "mxfp4_device.hpp"
 #include "panel.hpp"
 
@@ -21,8 +21,6 @@ using namespace mx;
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef int intx4 __attribute__((ext_vector_type(4)));
 typedef int intx8 __attribute__((ext_vector_type(8)));
-
-constexpr int kDeep = 4;          // panels of w in flight a wave
 
 struct Few {
   const void* x;                  // [T][K], or codes in panels of T rows
@@ -106,10 +104,21 @@ __device__ __forceinline__ floatx4 mfma(intx4 a, uint32_t sa, intx4 b, uint32_t 
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
-// X: float, uint16_t (BF16 bits) or uint8_t (codes).  TG: groups of 16 rows of x.
-template <class X, int TG, Dt OT, bool VEC, int WAVES>
+// Orders a wave's own LDS writes before its reads of other lanes' values.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// X: float, uint16_t (BF16 bits) or uint8_t (codes).  TG: groups of 16 rows of
+// x.  DEEP: panels a wave has in flight.
+template <class X, int TG, Dt OT, bool VEC, int WAVES, int DEEP>
 __global__ __launch_bounds__(64 * WAVES) void few_kernel(const Few f) {
+  constexpr bool kHeld = sizeof(X) == 1;
+  constexpr int kBlocks = 8 * DEEP;                         // blocks of a row in flight
   __shared__ floatx4 sums[WAVES][TG][64];
+  __shared__ intx4 xc[kHeld ? 1 : WAVES][kHeld ? 1 : 16 * TG * kBlocks];
+  __shared__ uint8_t xb[kHeld ? 1 : WAVES][kHeld ? 1 : 16 * TG * kBlocks];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = (int)blockIdx.x * 16;
@@ -118,42 +127,64 @@ __global__ __launch_bounds__(64 * WAVES) void few_kernel(const Few f) {
   floatx4 acc[TG];
 #pragma unroll
   for (int g = 0; g < TG; ++g) acc[g] = floatx4{0, 0, 0, 0};
-  for (int p = p0; p < p1; p += kDeep) {
-    intx4 wc[kDeep][2];
-    uint2 ws[kDeep];
+  for (int p = p0; p < p1; p += DEEP) {
+    intx4 wc[DEEP][2];
+    uint2 ws[DEEP];
+    Block held[kHeld ? DEEP : 1][2][TG];
 #pragma unroll
-    for (int i = 0; i < kDeep; ++i) {
+    for (int i = 0; i < DEEP; ++i) {
       const int64_t pi = p + i < p1 ? p + i : p1 - 1;       // the last again: not multiplied
       const uint8_t* c = f.w + (pi * f.N + row) * kPanelBytes + 16 * q;
       wc[i][0] = *reinterpret_cast<const intx4*>(c);
       wc[i][1] = *reinterpret_cast<const intx4*>(c + 64);
       ws[i] = *reinterpret_cast<const uint2*>(f.w_scales + (pi * f.N + row) * kPanelScales);
+      if constexpr (kHeld) {
+        // rows behind x's end: its last row, into columns that are not written
+#pragma unroll
+        for (int g = 0; g < TG; ++g) {
+          const int64_t at = pi * f.T + (16 * g + r < f.T ? 16 * g + r : f.T - 1);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            held[i][u][g].codes = *reinterpret_cast<const intx4*>(static_cast<const uint8_t*>(f.x) + at * kPanelBytes + 64 * u + 16 * q);
+            held[i][u][g].byte = f.x_scales[at * kPanelScales + 4 * u + q];
+          }
+        }
+      }
+    }
+    if constexpr (!kHeld) {
+      // block b of row t at slot t kBlocks + (b ^ t % 8): sixteen rows' reads
+      // of one block spread over the banks
+      const int live = (p1 - p < DEEP ? p1 - p : DEEP) * 8;
+      for (int k = lane; k < f.T * kBlocks; k += 64) {
+        const int t = k / kBlocks, b = k % kBlocks;
+        if (b >= live) continue;
+        const Block e = block_of<VEC>(static_cast<const X*>(f.x), f.K, t, (int64_t)p * kPanel + 32 * b);
+        xc[wave][t * kBlocks + (b ^ (t & 7))] = e.codes;
+        xb[wave][t * kBlocks + b] = (uint8_t)e.byte;
+      }
+      wave_sync();
     }
 #pragma unroll
-    for (int i = 0; i < kDeep; ++i) {
+    for (int i = 0; i < DEEP; ++i) {
       if (p + i >= p1) break;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const uint32_t sw = (u ? ws[i].y : ws[i].x) >> (8 * q);
 #pragma unroll
         for (int g = 0; g < TG; ++g) {
-          const int t = 16 * g + r;
           Block b;
-          b.codes = intx4{0, 0, 0, 0};
-          b.byte = 0;
-          if (t < f.T) {
-            if constexpr (sizeof(X) == 1) {
-              const int64_t at = (int64_t)(p + i) * f.T + t;
-              b.codes = *reinterpret_cast<const intx4*>(static_cast<const uint8_t*>(f.x) + at * kPanelBytes + 64 * u + 16 * q);
-              b.byte = f.x_scales[at * kPanelScales + 4 * u + q];
-            } else {
-              b = block_of<VEC>(static_cast<const X*>(f.x), f.K, t, (int64_t)(p + i) * kPanel + 128 * u + 32 * q);
-            }
+          if constexpr (kHeld) {
+            b = held[i][u][g];
+          } else {
+            const int t = 16 * g + r < f.T ? 16 * g + r : 0, k = 8 * i + 4 * u + q;
+            b.codes = xc[wave][t * kBlocks + (k ^ (t & 7))];
+            b.byte = xb[wave][t * kBlocks + k];
           }
           acc[g] = mfma(wc[i][u], sw, b.codes, b.byte, acc[g]);
         }
       }
     }
+    if constexpr (!kHeld) wave_sync();
   }
 #pragma unroll
   for (int g = 0; g < TG; ++g) sums[wave][g][lane] = acc[g];
@@ -190,9 +221,9 @@ hipError_t launch(const Few& f, hipStream_t s) {
   const int groups = (f.N + 15) / 16;
   // enough waves to cover the chip several times, none without a panel
   if (groups < 512 && f.panels >= 16)
-    few_kernel<X, TG, OT, VEC, 16><<<groups, 1024, 0, s>>>(f);
+    few_kernel<X, TG, OT, VEC, 16, 1><<<groups, 1024, 0, s>>>(f);
   else
-    few_kernel<X, TG, OT, VEC, 4><<<groups, 256, 0, s>>>(f);
+    few_kernel<X, TG, OT, VEC, 4, 4><<<groups, 256, 0, s>>>(f);
   return hipGetLastError();
 }
 template <class X, Dt OT, bool VEC>

@@ -68,10 +68,14 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
                                 void* out, Dt ot, hipStream_t s);
 
 // ---- MXFP4 products with few rows (mxfp4_few.hip) -------------------------------
-// Up to this many rows of x a product reads w once, in one launch; above, the
-// tiled product's reuse of w counts (32 x 11008 x 4096 BF16: see DESIGN notes
-// at the kernel).
+// Whether a product of T rows goes there: one launch that reads w once, against
+// a pass over x and a tiled product that reuses w.  Measured (us, x in BF16,
+// there / tiled): 11008 x 4096 weights, T = 1: 6 / 12, 16: 12 / 12, 32: 22 / 12;
+// 4096 x 4096, T = 16: 6 / 12, 32: 8 / 12.
 constexpr int64_t kMxFewRows = 32;
+inline bool mx_few(int64_t T, int64_t N, int64_t K) {
+  return T <= 16 || (T <= kMxFewRows && N * K <= (int64_t)1 << 24);
+}
 // out[T][N] = beta addend + alpha x w^T; x [T][K] FP32 or BF16, quantized along
 // K, or codes with x_scales (then xt is not used).  addend null: none.
 hipError_t launch_mx_few(const void* x, Dt xt, const uint8_t* x_scales, int64_t T, int64_t K, const uint8_t* w,
