@@ -738,13 +738,88 @@ __global__ __launch_bounds__(C::kThreads) void panel_sum_kernel(const Each e, Ar
                                      lane, smem + wave * kScratch);
 }
 
+// Small products: one 32 x 32 tile a workgroup, its eight waves dividing the
+// panels of K.  A lane loads its fragments straight from memory -- there is no
+// reuse worth an LDS stage -- and the waves' sums meet in LDS, in wave order.
+// The whole of a product's time is then one or two rounds of loads.  Step s
+// takes chunk 2 s + lane / 32 here, so that a load covers 32 bytes of a row.
+struct Tile32 {
+  static constexpr int B = 32, WM = 1, WN = 1, FM = 1, FN = 1, kWaves = 8, kThreads = 512, kBlocks = 2, kAcc = 16;
+};
+
+template <bool FP4, PanelEp EP, Dt OT, bool VEC>
+__global__ __launch_bounds__(512, 2) void panel_direct_kernel(const Each e, Args a) {
+  __shared__ float4 sums[Tile32::kWaves][4][64];
+  __shared__ __attribute__((aligned(16))) uint8_t scratch[kScratch];
+  int y, I, J;
+  place_of(a, (int)blockIdx.x, y, I, J);
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g0 = a.panels * wave / Tile32::kWaves, g1 = a.panels * (wave + 1) / Tile32::kWaves;
+  const int64_t off = (int64_t)y * a.bstride;
+  const int pr = I * 32 + r < a.M ? I * 32 + r : a.M - 1, qr = J * 32 + r < a.N ? J * 32 + r : a.N - 1;
+  const uint8_t* p = a.p.data + off + ((int64_t)g0 * a.p.rows + pr) * 128 + 16 * h;
+  const uint8_t* q = a.q.data + off + ((int64_t)g0 * a.q.rows + qr) * 128 + 16 * h;
+  const uint8_t* ps = FP4 ? a.p.scales + ((int64_t)g0 * a.p.rows + pr) * 8 : nullptr;
+  const uint8_t* qs = FP4 ? a.q.scales + ((int64_t)g0 * a.q.rows + qr) * 8 : nullptr;
+  floatx16 acc[1][1];
+  clear<Tile32>(acc);
+#pragma unroll 2
+  for (int g = g0; g < g1; ++g) {
+    intx4 x[4], w[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      x[s] = *reinterpret_cast<const intx4*>(p + 32 * s);
+      w[s] = *reinterpret_cast<const intx4*>(q + 32 * s);
+    }
+    p += a.p.rows * 128;
+    q += a.q.rows * 128;
+    uint2 sx = make_uint2(0, 0), sw = make_uint2(0, 0);
+    if constexpr (FP4) {
+      sx = *reinterpret_cast<const uint2*>(ps);
+      sw = *reinterpret_cast<const uint2*>(qs);
+      ps += a.p.rows * 8;
+      qs += a.q.rows * 8;
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int shift = 16 * (s & 1) + 8 * h;      // byte 2 s + h of the eight
+      if constexpr (FP4)
+        acc[0][0] = mfma_fp4<0>(x[s], w[s], acc[0][0], (s < 2 ? sx.x : sx.y) >> shift, (s < 2 ? sw.x : sw.y) >> shift);
+      else
+        acc[0][0] = mfma_f16(x[s], w[s], acc[0][0]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    sums[wave][k][lane] = make_float4(acc[0][0][4 * k], acc[0][0][4 * k + 1], acc[0][0][4 * k + 2], acc[0][0][4 * k + 3]);
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int v = 1; v < Tile32::kWaves; ++v)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 o = sums[v][k][lane];
+      acc[0][0][4 * k] += o.x;
+      acc[0][0][4 * k + 1] += o.y;
+      acc[0][0][4 * k + 2] += o.z;
+      acc[0][0][4 * k + 3] += o.w;
+    }
+  epilogue<Tile32, EP, OT, VEC>(a, e.n, acc, y, I, J, 0, 0, lane, scratch);
+}
+
 template <class C, bool FP4, PanelEp EP, Dt OT, bool VEC>
 hipError_t launch_one(const Each& e, const Args& a, const PanelPlan& p, hipStream_t s) {
-  panel_kernel<C, FP4, EP, OT, VEC><<<dim3((unsigned)p.groups), C::kThreads, 0, s>>>(e, a);
-  const hipError_t r = hipGetLastError();
-  if (r != hipSuccess || p.split_tiles == 0) return r;
-  panel_sum_kernel<C, EP, OT, VEC><<<dim3((unsigned)(p.split_tiles * C::FM * C::FN)), C::kThreads, 0, s>>>(e, a);
-  return hipGetLastError();
+  if constexpr (C::B == 32) {
+    panel_direct_kernel<FP4, EP, OT, VEC><<<dim3((unsigned)p.groups), C::kThreads, 0, s>>>(e, a);
+    return hipGetLastError();
+  } else {
+    panel_kernel<C, FP4, EP, OT, VEC><<<dim3((unsigned)p.groups), C::kThreads, 0, s>>>(e, a);
+    const hipError_t r = hipGetLastError();
+    if (r != hipSuccess || p.split_tiles == 0) return r;
+    panel_sum_kernel<C, EP, OT, VEC><<<dim3((unsigned)(p.split_tiles * C::FM * C::FN)), C::kThreads, 0, s>>>(e, a);
+    return hipGetLastError();
+  }
 }
 
 template <class C, bool FP4, PanelEp EP, Dt OT>
@@ -796,6 +871,7 @@ PanelPlan plan_tile(int64_t M, int64_t N, bool sym, int batch, int parts) {
   PanelPlan p;
   p.tile = C::B;
   p.parts = parts;
+  p.ws_bytes = 0;
   p.TM = (int)((M + C::B - 1) / C::B);
   p.TN = (int)((N + C::B - 1) / C::B);
   p.tiles = sym ? p.TM * (p.TM + 1) / 2 : p.TM * p.TN;
@@ -808,7 +884,7 @@ PanelPlan plan_tile(int64_t M, int64_t N, bool sym, int batch, int parts) {
     most = r.units > most ? r.units : most;
     if (parts > 1) p.split_tiles += (r.units - r.whole) / parts;
   }
-  p.groups = (most < p.slots ? most : p.slots) * kXcds;
+  p.groups = C::B == 32 ? p.tiles * batch : (most < p.slots ? most : p.slots) * kXcds;
   p.ws_bytes = (size_t)p.split_tiles * parts * C::kAcc * C::kThreads * sizeof(float);
   return p;
 }
@@ -817,7 +893,8 @@ PanelPlan plan_at(int tile, int64_t M, int64_t N, bool sym, int batch, int parts
   switch (tile) {
     case 256: return plan_tile<Tile256>(M, N, sym, batch, parts);
     case 128: return plan_tile<Tile128>(M, N, sym, batch, parts);
-    default: return plan_tile<Tile64>(M, N, sym, batch, parts);
+    case 64: return plan_tile<Tile64>(M, N, sym, batch, parts);
+    default: return plan_tile<Tile32>(M, N, sym, batch, parts);
   }
 }
 
@@ -829,11 +906,14 @@ PanelPlan plan_at(int tile, int64_t M, int64_t N, bool sym, int batch, int parts
 //    256    256    64: 1.20   256: 1.75          3         6
 //    128    512   256: 0.62   512: 1.10          2         4
 //     64    512   256: 0.36   512: 0.47          1         3
+//     32    256   2.0 per panel of a wave (an eighth of them), 0.4 a round, 2 once
 // Measured against this: 4096^2 x 4096 38 us on 256 (43 on 128, 73 on 64),
 // 2048^2 x 4096 16 us on 128 (27 on 256, 20 on 64), 1024^2 x 4096 9 us on 64
 // (26 and 14).  A split adds its partials' traffic and the second kernel:
-// 1024^2 x 16384 takes 43 us on 128 whole, 23 in 4 parts.
+// 1024^2 x 16384 takes 43 us on 128 whole, 23 in 4 parts.  64^2 x 4096 takes
+// 6.4 us on 32 (7.7 on 64), 1000 x 777 x 1501 11.9 (7.3).
 double plan_cost(const PanelPlan& p, int64_t panels, int batch) {
+  if (p.tile == 32) return 2.0 + ((int64_t)p.tiles * batch + 255) / 256 * (0.4 + 2.0 * ((panels + 7) / 8));
   const double slots = p.slots * kXcds;
   const int few = p.tile == 256 ? 64 : 256;
   const double low = p.tile == 256 ? 1.20 : p.tile == 128 ? 0.62 : 0.36;
@@ -860,10 +940,10 @@ double plan_cost(const PanelPlan& p, int64_t panels, int batch) {
 PanelPlan plan_panel(int64_t M, int64_t N, int64_t panels, bool sym, int batch, bool allow_split, bool poly) {
   PanelPlan best{};
   double least = 0.0;
-  for (int tile : {256, 128, 64}) {
+  for (int tile : {256, 128, 64, 32}) {
     if (tile == 256 && poly) continue;
     for (int parts : {1, 2, 4, 8}) {
-      if (parts > 1 && (!allow_split || parts > panels)) break;
+      if (parts > 1 && (!allow_split || parts > panels || tile == 32)) break;
       const PanelPlan p = plan_at(tile, M, N, sym, batch, parts);
       const double us = plan_cost(p, panels, batch);
       if (least == 0.0 || us < least) {
@@ -913,7 +993,8 @@ hipError_t launch_panel(const PanelProblem& g, const PanelPlan& p, bool fp4, voi
   switch (p.tile) {
     case 256: return launch_tile<Tile256>(g, e, a, p, fp4, s);
     case 128: return launch_tile<Tile128>(g, e, a, p, fp4, s);
-    default: return launch_tile<Tile64>(g, e, a, p, fp4, s);
+    case 64: return launch_tile<Tile64>(g, e, a, p, fp4, s);
+    default: return launch_tile<Tile32>(g, e, a, p, fp4, s);
   }
 }
 

@@ -48,7 +48,7 @@ struct PanelProblem {
 constexpr int kMaxPanelBatch = 32;
 
 struct PanelPlan {
-  int tile;                // rows and columns of a tile
+  int tile;                // rows and columns of a tile: 256, 128, 64 or 32
   int parts;               // K-parts of each tile left over after equal rounds (1: none)
   int TM, TN, tiles;       // of one problem
   int slots;               // workgroups per XCD
@@ -56,7 +56,8 @@ struct PanelPlan {
   size_t ws_bytes;         // FP32 partials of the whole batch
 };
 // poly: for the Poly epilogue, which has no 256 x 256 tiles: A's values next to
-// the 128 accumulators of a lane spill there (4 x 2048^2: 73 us, 50 us on 128).
+// the 128 accumulators of a lane spill there (4 x 2048^2: 73 us,
+// 50 us on 128).
 PanelPlan plan_panel(int64_t M, int64_t N, int64_t panels, bool sym, int batch, bool allow_split, bool poly);
 hipError_t launch_panel(const PanelProblem& g, const PanelPlan& p, bool fp4, void* ws, hipStream_t s);
 
