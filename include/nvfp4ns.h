@@ -370,7 +370,7 @@ ns_status ns_orthogonalize_grouped_on(int count, const void* const* G, const int
  * blocks (codes 0; b = 0 for blocks without elements).  NVFP4_COLS stores the
  * transpose: its rows are the matrix's columns.
  *
- * Dimensions are 1 .. 2^24, of any parity.
+ * Dimensions are 1 .. 2^24, of any parity, a matrix up to 2^36 elements.
  * ====================================================================== */
 size_t mxfp4_codes_bytes(int64_t rows, int64_t cols, nvfp4_axis axis);
 size_t mxfp4_scales_bytes(int64_t rows, int64_t cols, nvfp4_axis axis);

@@ -3,6 +3,8 @@
 // and launch sequences.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "api_common.hpp"
 #include "mxfp4_device.hpp"
 #include "panel.hpp"
@@ -18,6 +20,10 @@ namespace {
 // Offsets inside a panel are 32-bit and row numbers int.
 constexpr int64_t kMaxDim = (int64_t)1 << 24;
 inline bool mx_dim(int64_t a) { return a > 0 && a <= kMaxDim; }
+// Elements of one matrix: keeps every launch's thread count below 2^32.
+constexpr int64_t kMaxCount = (int64_t)1 << 36;
+inline bool mx_dims(int64_t rows, int64_t cols) { return mx_dim(rows) && mx_dim(cols) && rows * cols <= kMaxCount; }
+inline bool mx_dims(int64_t M, int64_t N, int64_t K) { return mx_dims(M, N) && mx_dims(M, K) && mx_dims(N, K); }
 inline bool axis_ok(int a) { return a == NVFP4_ROWS || a == NVFP4_COLS; }
 inline int64_t mx_panels(int64_t n) { return (n + nvfp4::mx::kPanel - 1) / nvfp4::mx::kPanel; }
 // Bytes of an operand of `rows` rows blocked along `cols`.
@@ -63,19 +69,19 @@ hipError_t mx_multiply(const uint8_t* pc, const uint8_t* ps, const uint8_t* qc, 
 extern "C" {
 
 size_t mxfp4_codes_bytes(int64_t rows, int64_t cols, nvfp4_axis axis) {
-  if (!mx_dim(rows) || !mx_dim(cols) || !axis_ok(axis)) return 0;
+  if (!mx_dims(rows, cols) || !axis_ok(axis)) return 0;
   return axis == NVFP4_ROWS ? mx_codes(rows, cols) : mx_codes(cols, rows);
 }
 
 size_t mxfp4_scales_bytes(int64_t rows, int64_t cols, nvfp4_axis axis) {
-  if (!mx_dim(rows) || !mx_dim(cols) || !axis_ok(axis)) return 0;
+  if (!mx_dims(rows, cols) || !axis_ok(axis)) return 0;
   return axis == NVFP4_ROWS ? mx_scales(rows, cols) : mx_scales(cols, rows);
 }
 
 ns_status mxfp4_quantize(const void* x, ns_dtype xt, int64_t rows, int64_t cols, nvfp4_axis axis, uint8_t* codes,
                          uint8_t* scales, void* stream) {
   if (!x || !codes || !scales || !dtype_ok(xt) || !axis_ok(axis)) return NS_ERR_ARG;
-  if (!mx_dim(rows) || !mx_dim(cols)) return NS_ERR_SHAPE;
+  if (!mx_dims(rows, cols)) return NS_ERR_SHAPE;
   if (!al(x, 16) || !al(codes, 16) || !al(scales, 16)) return NS_ERR_ARG;
   const Span X{x, (size_t)(rows * cols) * dtype_size(xt)}, C{codes, mxfp4_codes_bytes(rows, cols, axis)},
       S{scales, mxfp4_scales_bytes(rows, cols, axis)};
@@ -90,7 +96,7 @@ ns_status mxfp4_quantize(const void* x, ns_dtype xt, int64_t rows, int64_t cols,
 ns_status mxfp4_quantize_both(const void* x, ns_dtype xt, int64_t rows, int64_t cols, uint8_t* codes_rows,
                               uint8_t* scales_rows, uint8_t* codes_cols, uint8_t* scales_cols, void* stream) {
   if (!x || !codes_rows || !scales_rows || !codes_cols || !scales_cols || !dtype_ok(xt)) return NS_ERR_ARG;
-  if (!mx_dim(rows) || !mx_dim(cols)) return NS_ERR_SHAPE;
+  if (!mx_dims(rows, cols)) return NS_ERR_SHAPE;
   if (!al(x, 16) || !al(codes_rows, 16) || !al(scales_rows, 16) || !al(codes_cols, 16) || !al(scales_cols, 16))
     return NS_ERR_ARG;
   const Span X{x, (size_t)(rows * cols) * dtype_size(xt)}, C{codes_rows, mx_codes(rows, cols)},
@@ -104,7 +110,7 @@ ns_status mxfp4_quantize_both(const void* x, ns_dtype xt, int64_t rows, int64_t 
 ns_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, nvfp4_axis axis,
                            void* out, ns_dtype ot, void* stream) {
   if (!codes || !scales || !out || !dtype_ok(ot) || !axis_ok(axis)) return NS_ERR_ARG;
-  if (!mx_dim(rows) || !mx_dim(cols)) return NS_ERR_SHAPE;
+  if (!mx_dims(rows, cols)) return NS_ERR_SHAPE;
   if (!al(codes, 16) || !al(scales, 16) || !al(out, 16)) return NS_ERR_ARG;
   const Span O{out, (size_t)(rows * cols) * dtype_size(ot)};
   if (hits(O, {Span{codes, mxfp4_codes_bytes(rows, cols, axis)}, Span{scales, mxfp4_scales_bytes(rows, cols, axis)}}))
@@ -114,7 +120,7 @@ ns_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t 
 }
 
 size_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (!mx_dim(M) || !mx_dim(N) || !mx_dim(K)) return 0;
+  if (!mx_dims(M, N, K)) return 0;
   return mx_plan(M, N, K, true).ws_bytes;
 }
 
@@ -123,7 +129,7 @@ ns_status mxfp4_gemm(const uint8_t* codes_p, const uint8_t* scales_p, const uint
                      ns_dtype ot, void* ws, size_t ws_bytes, void* stream) {
   if (!codes_p || !scales_p || !codes_q || !scales_q || !out || !dtype_ok(ot)) return NS_ERR_ARG;
   if (!std::isfinite(alpha) || !std::isfinite(beta) || (beta != 0.0f && !addend)) return NS_ERR_ARG;
-  if (!mx_dim(M) || !mx_dim(N) || !mx_dim(K)) return NS_ERR_SHAPE;
+  if (!mx_dims(M, N, K)) return NS_ERR_SHAPE;
   const PanelPlan plan = mx_plan(M, N, K, ws != nullptr);
   if (ws && ws_bytes < plan.ws_bytes) return NS_ERR_WORKSPACE;
   if (!al(codes_p, 16) || !al(scales_p, 16) || !al(codes_q, 16) || !al(scales_q, 16) || !al(out, 16) ||
@@ -181,7 +187,7 @@ LinearLayout backward_layout(int64_t T, int64_t N, int64_t K) {
 extern "C" {
 
 size_t mxfp4_linear_workspace_bytes(int64_t T, int64_t N, int64_t K) {
-  if (!mx_dim(T) || !mx_dim(N) || !mx_dim(K)) return 0;
+  if (!mx_dims(T, N, K)) return 0;
   return forward_layout(T, N, K).total;
 }
 
@@ -190,7 +196,7 @@ ns_status mxfp4_linear(const void* x, ns_dtype xt, int64_t T, int64_t K, const u
                        uint8_t* kept_scales, void* ws, size_t ws_bytes, void* stream) {
   if (!x || !w_codes || !w_scales || !y || !dtype_ok(xt) || !dtype_ok(yt)) return NS_ERR_ARG;
   if ((kept_codes == nullptr) != (kept_scales == nullptr)) return NS_ERR_ARG;
-  if (!mx_dim(T) || !mx_dim(N) || !mx_dim(K)) return NS_ERR_SHAPE;
+  if (!mx_dims(T, N, K)) return NS_ERR_SHAPE;
   const LinearLayout L = forward_layout(T, N, K);
   if (ws_bytes < L.total || (L.total && !ws)) return NS_ERR_WORKSPACE;
   if (!al(x, 16) || !al(w_codes, 16) || !al(w_scales, 16) || !al(y, 16) || !al(kept_codes, 16) ||
@@ -216,7 +222,7 @@ ns_status mxfp4_linear(const void* x, ns_dtype xt, int64_t T, int64_t K, const u
 }
 
 size_t mxfp4_linear_backward_workspace_bytes(int64_t T, int64_t N, int64_t K) {
-  if (!mx_dim(T) || !mx_dim(N) || !mx_dim(K)) return 0;
+  if (!mx_dims(T, N, K)) return 0;
   return backward_layout(T, N, K).total;
 }
 
@@ -228,7 +234,7 @@ ns_status mxfp4_linear_backward(const void* dy, ns_dtype dyt, int64_t T, int64_t
   if (dx && (!wt_codes || !wt_scales)) return NS_ERR_ARG;
   if (dw && (!kept_codes || !kept_scales)) return NS_ERR_ARG;
   if (!std::isfinite(beta) || (beta != 0.0f && (!dw || dwt != NS_F32))) return NS_ERR_ARG;
-  if (!mx_dim(T) || !mx_dim(N) || !mx_dim(K)) return NS_ERR_SHAPE;
+  if (!mx_dims(T, N, K)) return NS_ERR_SHAPE;
   const LinearLayout L = backward_layout(T, N, K);
   if (!ws || ws_bytes < L.total) return NS_ERR_WORKSPACE;
   if (!al(dy, 16) || !al(wt_codes, 16) || !al(wt_scales, 16) || !al(kept_codes, 16) || !al(kept_scales, 16) ||
@@ -384,10 +390,8 @@ hipError_t ns16_batch(const nvfp4::Ns16Inputs& in, void* const* out, const float
   return hipSuccess;
 }
 
-// The next batch of a group: matrices of the shape of the first one not
-// taken yet, in call order.  `done` marks the matrices before `from` by shape
-// alone: matrix j is taken with the first matrix of its shape, in batches of
-// kMaxPanelBatch.
+// A batch of a group: matrices of one shape, in call order.  Matrix j is taken
+// with the first matrix of its shape, kMaxPanelBatch at a time.
 struct Ns16Batch {
   int count, index[nvfp4::kMaxPanelBatch];
 };
@@ -430,23 +434,47 @@ ns_status coeffs_ok(const float* coeffs, int k) {
   return NS_OK;
 }
 
-// One array of each matrix of a group; `written` arrays may overlap nothing.
+// One array of each matrix of a group.
 struct Arrays {
   const void* const* p;
   ns_dtype t;
   bool written;
 };
-bool group_clear(int count, const int64_t* m, const int64_t* n, std::initializer_list<Arrays> arrays, Span ws) {
+// Whether no array that is written shares a byte with another, and none with
+// the workspace: the ranges in order of their starts, each against the
+// furthest end before it (of all ranges if it is written itself, else of the
+// written ones).  NS_ERR_ARG if some do.
+ns_status group_clear(int count, const int64_t* m, const int64_t* n, std::initializer_list<Arrays> arrays, Span ws) {
+  struct Range {
+    uintptr_t from, to;
+    bool written;
+  };
+  constexpr size_t kStack = 64;
+  const size_t total = arrays.size() * (size_t)count + 1;
+  Range few[kStack];
+  Range* r = few;
+  if (total > kStack) {
+    r = static_cast<Range*>(std::malloc(total * sizeof(Range)));
+    if (!r) return NS_ERR_ARG;
+  }
+  size_t k = 0;
+  auto add = [&](const void* p, size_t bytes, bool written) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    r[k++] = Range{at, at + bytes, written};
+  };
+  add(ws.p, ws.n, true);
   for (const Arrays& a : arrays)
-    for (int i = 0; i < count; ++i) {
-      const Span A{a.p[i], (size_t)(m[i] * n[i]) * dtype_size(a.t)};
-      if (hits(ws, {A})) return false;
-      if (!a.written) continue;
-      for (const Arrays& b : arrays)
-        for (int j = 0; j < count; ++j)
-          if (!(&a == &b && i == j) && hits(A, {Span{b.p[j], (size_t)(m[j] * n[j]) * dtype_size(b.t)}})) return false;
-    }
-  return true;
+    for (int i = 0; i < count; ++i) add(a.p[i], (size_t)(m[i] * n[i]) * dtype_size(a.t), a.written);
+  std::sort(r, r + k, [](const Range& x, const Range& y) { return x.from < y.from; });
+  uintptr_t all = 0, written = 0;
+  bool clear = true;
+  for (size_t i = 0; i < k && clear; ++i) {
+    clear = r[i].from >= (r[i].written ? all : written);
+    all = r[i].to > all ? r[i].to : all;
+    if (r[i].written) written = r[i].to > written ? r[i].to : written;
+  }
+  if (r != few) std::free(r);
+  return clear ? NS_OK : NS_ERR_ARG;
 }
 
 }  // namespace
@@ -480,7 +508,8 @@ ns_status ns_orthogonalize_f16_grouped(int count, const void* const* G, const in
   if (!al(ws, 16)) return NS_ERR_ARG;
   for (int i = 0; i < count; ++i)
     if (!al(G[i], 16) || !al(out[i], 16)) return NS_ERR_ARG;
-  if (!group_clear(count, m, n, {{G, gt, false}, {out, ot, true}}, Span{ws, ws_bytes})) return NS_ERR_ARG;
+  st = group_clear(count, m, n, {{G, gt, false}, {out, ot, true}}, Span{ws, ws_bytes});
+  if (st != NS_OK) return st;
   Ns16Call c{};
   c.gt = (Dt)gt;
   c.mt = Dt::F32;
@@ -521,7 +550,8 @@ ns_status ns_muon_step(int count, void* const* W, ns_dtype wt, void* const* M, n
   if (!al(ws, 16)) return NS_ERR_ARG;
   for (int i = 0; i < count; ++i)
     if (!al(W[i], 16) || !al(M[i], 16) || !al(G[i], 16)) return NS_ERR_ARG;
-  if (!group_clear(count, m, n, {{W, wt, true}, {M, mt, true}, {G, gt, false}}, Span{ws, ws_bytes})) return NS_ERR_ARG;
+  st = group_clear(count, m, n, {{W, wt, true}, {M, mt, true}, {G, gt, false}}, Span{ws, ws_bytes});
+  if (st != NS_OK) return st;
   Ns16Call c{};
   c.gt = (Dt)gt;
   c.mt = (Dt)mt;

@@ -203,6 +203,10 @@ __device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t
   asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
 }
 
+// s_barrier that no memory access moves across (the builtin alone does not
+// keep LDS reads behind it).
+__device__ __forceinline__ void all_waves() { asm volatile("s_barrier" ::: "memory"); }
+
 // Depends on r % 32 alone, so that a fragment's LDS address is one per-lane
 // offset for each step plus a constant for its 32-row block.
 __device__ __forceinline__ int swizzle(int r) { return (r ^ ((r & 31) >> 3)) & 7; }
@@ -627,7 +631,7 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks* C::kWaves / 4) void panel_
     next.advance(a, run, wave, lane);
   }
   wait_loads();
-  __builtin_amdgcn_s_barrier();
+  all_waves();
 #pragma unroll
   for (int k = 0; k < kLoads; ++k) next.load(lds0 + (C::NST - 1) * kStage, wave, k);
 #pragma unroll
@@ -660,7 +664,7 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks* C::kWaves / 4) void panel_
       // waves are here, and the next stage's loads have landed
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       wait_loads();
-      __builtin_amdgcn_s_barrier();
+      all_waves();
       const uint32_t freed = lds0 + cur * kStage;
       cur = cur + 1 == C::NST ? 0 : cur + 1;
       const uint8_t* nst = smem + cur * kStage;

@@ -131,6 +131,98 @@ def test_gemm_matches_float64(M, N, K):
     assert np.all(np.abs(b - want) <= tol + U16 * (np.abs(want) + tol))
 
 
+# 64-, 128- and 256-wide tiles over several rounds of workgroups, and each with
+# leftover tiles split along K
+LARGE = [(330, 330, 5000), (200, 1760, 5000), (2100, 2050, 2100), (2410, 3450, 2000), (2020, 4100, 2000),
+         (8190, 4090, 300), (3970, 4100, 5000)]
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_large_gemm_matches_float64(M, N, K):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(M + N + K)
+    p = ns.mxfp4_quantize(torch.randn(M, K, generator=gen, device=DEV))
+    q = ns.mxfp4_quantize(torch.randn(N, K, generator=gen, device=DEV))
+    pv, qv = (ns.mxfp4_dequantize(*t, r, K).double() for t, r in ((p, M), (q, N)))
+    want = pv @ qv.t()
+    tol = (K + 4) * U32 * (pv.abs() @ qv.abs().t())
+    first = ns.mxfp4_gemm(p, q, M, N, K)
+    for split in (True, False):
+        assert bool(((ns.mxfp4_gemm(p, q, M, N, K, split=split) - want).abs() <= tol).all()), split
+    add = torch.randn(M, N, generator=gen, device=DEV)
+    got = ns.mxfp4_gemm(p, q, M, N, K, beta=0.5, addend=add, out_dtype=ns.NS_BF16)
+    w = want + 0.5 * add.double()
+    assert bool(((got - w).abs() <= tol + 4 * U32 * (want.abs() + add.abs()) + U16 * (w.abs() + tol)).all())
+    assert torch.equal(ns.mxfp4_gemm(p, q, M, N, K), first)          # the same bits every time
+
+
+def test_offsets_past_32_bits():
+    rows, cols = 70000, 32768                                        # 2.3e9 elements
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(1)
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV)
+    for r in range(0, rows, 10000):
+        x[r:r + 10000] = torch.randn(10000, cols, generator=gen, device=DEV).to(torch.bfloat16)
+    along, down = ns.mxfp4_quantize_both(x)
+    assert all(torch.equal(a, b) for a, b in zip(ns.mxfp4_quantize(x), along))
+    tail = ns.mxfp4_quantize(x[-300:].contiguous())
+    assert torch.equal(along[0][:, -300:], tail[0]) and torch.equal(along[1][:, -300:], tail[1])
+    tail = ns.mxfp4_quantize(x[:, -200:].contiguous(), ns.NVFP4_COLS)
+    assert torch.equal(down[0][:, -200:], tail[0]) and torch.equal(down[1][:, -200:], tail[1])
+    v = ns.mxfp4_dequantize(*along, rows, cols, out_dtype=ns.NS_BF16)
+    assert torch.equal(v[-300:], ns.mxfp4_dequantize(*(t[:, -300:].contiguous() for t in along), 300, cols,
+                                                     out_dtype=ns.NS_BF16))
+    del v, along, down
+    K, N = 64, 33000
+    p = ns.mxfp4_quantize(x[:, :K].contiguous())
+    q = ns.mxfp4_quantize(torch.randn(N, K, generator=gen, device=DEV))
+    y = ns.mxfp4_gemm(p, q, rows, N, K, out_dtype=ns.NS_BF16)        # 2.3e9 elements too
+    few = ns.mxfp4_gemm(tuple(t[:, -300:].contiguous() for t in p), q, 300, N, K, out_dtype=ns.NS_BF16)
+    assert torch.equal(y[-300:], few)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with workspaces of their own do not meet."""
+    T, N, K = 1100, 1024, 9000
+    x = [_x(T, K, s, "bf16")[0] for s in (1, 2)]
+    w = ns.mxfp4_quantize(_x(N, K, 3, "f32")[0])
+    want = [ns.mxfp4_linear(v, w, N) for v in x]
+    streams = [torch.cuda.Stream() for _ in x]
+    got = [torch.empty_like(v) for v in want]
+    wss = [torch.empty(ns.mxfp4_linear_workspace_bytes(T, N, K), dtype=torch.uint8, device=DEV) for _ in x]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for v, o, ws, s in zip(x, got, wss, streams):
+            ns.mxfp4_linear(v, w, N, out=o, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_binding_refuses():
+    x = torch.randn(64, 96, device=DEV)
+    q = ns.mxfp4_quantize(x)
+    with pytest.raises(ValueError):
+        ns.mxfp4_quantize(x.t())                                     # not contiguous
+    with pytest.raises(ValueError):
+        ns.mxfp4_quantize(x[0])                                      # not a matrix
+    with pytest.raises(ValueError):
+        ns.mxfp4_quantize(x, codes=q[0][:, :32].contiguous())        # too short
+    with pytest.raises(TypeError):
+        ns.mxfp4_quantize(x.half())
+    with pytest.raises(ValueError):
+        ns.mxfp4_gemm(q, q, 64, 64, 300)                             # K past the panels
+    with pytest.raises(ValueError):
+        ns.mxfp4_gemm(q, q, 64, 64, 96, beta=1.0, addend=torch.zeros(64, 32, device=DEV))
+    with pytest.raises(ValueError):
+        ns.mxfp4_linear(x, q, 65)
+    with pytest.raises(ValueError):
+        ns.mxfp4_linear(x, (q[0].cpu(), q[1]), 64)
+    with pytest.raises(ValueError):
+        ns.mxfp4_linear_backward(x, q, None, 64, need_dw=False, dx=torch.empty(64, 10, device=DEV))
+    with pytest.raises(ValueError):
+        ns.mxfp4_linear_backward(x, q, q, 64, beta=1.0)              # adds to nothing
+
+
 def test_gemm_nan_blocks_meet_their_rows_and_columns_only():
     p, q = O.quantize(_x(70, 600, 1, "f32")[1]), O.quantize(_x(90, 600, 2, "f32")[1])
     p[1][1, 13, 2] = 255

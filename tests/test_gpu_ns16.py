@@ -80,6 +80,29 @@ def test_five_steps(m, n, ty):
     assert rel_fro(host(ns.ns_orthogonalize_f16(G, [QUINTIC] * 5, out_dtype=ns.NS_BF16)), want) <= FIVE + UBF
 
 
+def _ns64_gpu(G, coeffs):
+    X = G.double().t() if G.shape[0] > G.shape[1] else G.double()
+    X = X / (X.norm() + 1e-7)
+    for a, b, c in coeffs:
+        A = X @ X.t()
+        X = a * X + (b * A + c * A @ A) @ X
+    return X.t() if G.shape[0] > G.shape[1] else X
+
+
+# every tile size of the three products, whole and split along K
+@pytest.mark.parametrize("m,n", [(200, 600), (900, 1300), (2300, 900), (2000, 2800), (2050, 2050), (3100, 2700), (3100, 3000)])
+def test_five_steps_large(m, n):
+    G = synth.device_lowrank_bf16(m, n, m + n, DEV)
+    want = _ns64_gpu(G, [QUINTIC] * 5)
+    got = ns.ns_orthogonalize_f16(G, [QUINTIC] * 5)
+    err = float((got - want).norm() / want.norm())
+    print(f"[ns16] {m}x{n}: {err:.2e}", flush=True)
+    assert err <= FIVE
+    assert torch.equal(ns.ns_orthogonalize_f16(G, [QUINTIC] * 5), got)       # the same bits every time
+    pair = ns.ns_orthogonalize_f16_grouped([G, G], [QUINTIC] * 5)
+    assert torch.equal(pair[0], pair[1]) and float((pair[0] - want).norm() / want.norm()) <= FIVE
+
+
 def test_clip_and_cubic():
     G, Gv = _g(200, 333, 4)
     clip = 0.02
@@ -172,6 +195,65 @@ def test_muon_step(shapes, types, nesterov):
             off = np.linalg.norm(host(Ws[i]) - want)
             assert off <= FIVE * np.linalg.norm(upd) + (uw + 2 * U32) * np.linalg.norm(want)
             assert np.array_equal(host(Gs[i]), g0[i])
+
+
+def test_muon_of_one_step_and_without_scales():
+    W = torch.from_numpy(0.02 * synth.gaussian(70, 200, 1)).to(DEV)
+    M = torch.zeros(70, 200, device=DEV)
+    G, Gv = _g(70, 200, 2)
+    w0 = host(W).astype(np.float64)
+    ns.ns_muon_step([W], [M], [G], [CUBIC], lr=0.5, momentum=0.0, nesterov=False)
+    upd = 0.5 * ns64(Gv, [CUBIC])
+    assert np.array_equal(host(M), host(G))
+    assert np.linalg.norm(host(W) - (w0 - upd)) <= FIVE * np.linalg.norm(upd) + 2 * U32 * np.linalg.norm(w0)
+
+
+def test_muon_non_finite_and_zero_gradients():
+    W = torch.ones(40, 50, device=DEV, dtype=torch.bfloat16)
+    M = torch.zeros(40, 50, device=DEV)
+    ns.ns_muon_step([W], [M], [torch.zeros(40, 50, device=DEV)], [QUINTIC] * 5, lr=0.5, weight_decay=0.5)
+    assert (host(W) == 0.75).all() and (host(M) == 0).all()          # decay alone
+    G = torch.ones(40, 50, device=DEV)
+    G[1, 2] = float("nan")
+    ns.ns_muon_step([W], [M], [G], [QUINTIC] * 5, lr=0.5)
+    assert np.isnan(host(W)).all() and np.isnan(host(M)).sum() == 1
+
+
+def test_muon_writes_only_its_arrays():
+    for m, n in ((33, 70), (70, 33)):
+        buf = [torch.full((m * n + 128,), 2.0, dtype=t, device=DEV) for t in (torch.bfloat16, torch.float32)]
+        W, M = (b[:m * n].view(m, n) for b in buf)
+        G, _ = _g(m, n, 3, "bf16")
+        g0 = G.clone()
+        ns.ns_muon_step([W], [M], [G], [QUINTIC] * 2, lr=0.1)
+        assert all((host(b)[-128:] == 2.0).all() for b in buf) and torch.equal(G, g0)
+
+
+def test_binding_refuses():
+    G, _ = _g(33, 70, 1)
+    with pytest.raises(ValueError):
+        ns.ns_orthogonalize_f16(G.t(), [QUINTIC])                    # not contiguous
+    with pytest.raises(ValueError):
+        ns.ns_orthogonalize_f16(G, [QUINTIC], out=torch.empty(70, 33, device=DEV))
+    with pytest.raises(ns.NSError):
+        ns.ns_orthogonalize_f16(G, [QUINTIC], out=G)
+    with pytest.raises(ns.NSError):
+        ns.ns_orthogonalize_f16(G, [QUINTIC], clip=0.0)
+    with pytest.raises(ns.NSError):
+        ns.ns_orthogonalize_f16(G, [])
+    with pytest.raises(ValueError):
+        ns.ns_orthogonalize_f16_grouped([G, G], [QUINTIC], clips=[1.0])
+    W, M = torch.zeros_like(G), torch.zeros_like(G)
+    with pytest.raises(ValueError):
+        ns.ns_muon_step([W], [M], [], [QUINTIC], lr=0.1)
+    with pytest.raises(ValueError):
+        ns.ns_muon_step([W], [M[:, :35].contiguous()], [G], [QUINTIC], lr=0.1)
+    with pytest.raises(TypeError):
+        ns.ns_muon_step([W, W.bfloat16()], [M, M], [G, G], [QUINTIC], lr=0.1)
+    with pytest.raises(ns.NSError):
+        ns.ns_muon_step([W], [W], [G], [QUINTIC], lr=0.1)
+    with pytest.raises(ns.NSError):
+        ns.ns_muon_step([W], [M], [G], [QUINTIC], lr=float("nan"))
 
 
 def test_muon_in_a_graph_with_the_layer_it_trains():
