@@ -271,7 +271,7 @@ constexpr int64_t kMaxElems16 = (int64_t)1 << 31;
 // one while it writes the other), A and B, partials and scalars.
 struct Ns16Layout {
   int64_t mp, np;
-  size_t x, xt[2], a, b, part, fac, total;   // of one matrix
+  size_t x, xt[2], a, b, da, rb, part, fac, total;   // of one matrix
   size_t split;                              // the batch's split tiles' partials, behind its matrices
   PanelPlan gram, poly, iter, last;
 };
@@ -294,6 +294,10 @@ Ns16Layout ns16_layout(int64_t m, int64_t n, int batch) {
   L.xt[1] = take((size_t)(L.mp * L.np) * 2);
   L.a = take((size_t)(L.mp * L.mp) * 2);
   L.b = take((size_t)(L.mp * L.mp) * 2);
+  // per row: what f16 takes from A's diagonal, and B's over its rounding (read
+  // by whole tiles, so up to 255 rows further than they are written)
+  L.da = take((size_t)(L.mp + 256) * sizeof(float));
+  L.rb = take((size_t)(L.mp + 256) * sizeof(float));
   L.part = take(nvfp4::kNs16Parts * sizeof(double));
   L.fac = take(2 * sizeof(float));
   L.total = o;
@@ -323,6 +327,7 @@ hipError_t ns16_batch(const nvfp4::Ns16Inputs& in, void* const* out, const float
   uint8_t *X = ws + L.x, *A = ws + L.a, *B = ws + L.b;
   double* part = reinterpret_cast<double*>(ws + L.part);
   float* fac = reinterpret_cast<float*>(ws + L.fac);
+  float *da = reinterpret_cast<float*>(ws + L.da), *rb = reinterpret_cast<float*>(ws + L.rb);
   hipError_t e = nvfp4::launch_ns16_norm(in, batch, c.gt, c.mt, m * n, c.mu, c.nesterov, part, stride, s);
   if (e != hipSuccess) return e;
   e = nvfp4::launch_ns16_start(in, batch, c.gt, c.mt, m, n, tr, c.mu, c.nesterov, part, X, ws + L.xt[0], L.mp, L.np,
@@ -343,6 +348,7 @@ hipError_t ns16_batch(const nvfp4::Ns16Inputs& in, void* const* out, const float
     g.alpha = 1.0f / (nvfp4::kNs16Scale * nvfp4::kNs16Scale);
     g.dalpha = it == 0 ? fac + 1 : nullptr;
     g.out = A;
+    g.dout = da;
     e = nvfp4::launch_panel(g, L.gram, false, ws + (size_t)batch * L.total, s);
     if (e != hipSuccess) return e;
     g.p = g.q = oa;
@@ -355,6 +361,8 @@ hipError_t ns16_batch(const nvfp4::Ns16Inputs& in, void* const* out, const float
     g.cb = c.coeffs[3 * it + 1];
     g.cc = c.coeffs[3 * it + 2];
     g.out = B;
+    g.din = da;
+    g.dout = rb;
     e = nvfp4::launch_panel(g, L.poly, false, ws + (size_t)batch * L.total, s);
     if (e != hipSuccess) return e;
     PanelProblem u;
@@ -362,6 +370,7 @@ hipError_t ns16_batch(const nvfp4::Ns16Inputs& in, void* const* out, const float
     u.bstride = stride;
     u.panels = L.mp / 64;
     u.dalpha = it == 0 ? fac : nullptr;
+    u.din = rb;
     if (it + 1 < c.k) {
       u.p = ob;
       u.q = oxt;
@@ -375,6 +384,7 @@ hipError_t ns16_batch(const nvfp4::Ns16Inputs& in, void* const* out, const float
       // rows of the output are rows of X, or of its transpose when m > n
       u.p = tr ? oxt : ob;
       u.q = tr ? ob : oxt;
+      u.din_cols = tr;
       u.M = m;
       u.N = n;
       u.ep = c.step ? PanelEp::Step : PanelEp::Out;

@@ -73,6 +73,9 @@ struct Args {
   uint8_t* out;
   uint8_t* out_t;
   const uint8_t* a;
+  const float* din;
+  float* dout;
+  int din_cols;
   int64_t bstride;
 };
 
@@ -411,11 +414,41 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// Factors on a tile's values: alpha, and per row or per column where an array
+// gives them.  A lane's are loaded together, before the blocks that use them:
+// the accumulators stay as they are (scaled in place they would be kept twice,
+// and spill).
+template <class C>
+struct Factors {
+  float row[C::FM][2];          // by_rows: row 16 half + lane / 4 of block row i
+  float col[C::FN][8];          // and the lane's eight columns of block column j
+
+  __device__ __forceinline__ Factors(float alpha, const float* din, bool cols, int m0, int n0, int wm, int wn, int lane) {
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) row[i][0] = row[i][1] = alpha;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) col[j][e] = 1.0f;
+    if (din && !cols) {
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) row[i][h] *= din[m0 + (wm * C::FM + i) * 32 + 16 * h + (lane >> 2)];
+    } else if (din) {
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) col[j][e] = din[n0 + (wn * C::FN + j) * 32 + (lane & 3) * 8 + e];
+    }
+  }
+};
+
 // f(row, column, v): eight neighbouring values of a tile row, each lane its
 // own; the wave's 32 x 32 blocks pass through LDS sixteen rows at a time.
 template <class C, class F>
-__device__ __forceinline__ void by_rows(const floatx16 (&acc)[C::FM][C::FN], int wm, int wn, int lane, uint8_t* lds,
-                                        F&& f) {
+__device__ __forceinline__ void by_rows(const floatx16 (&acc)[C::FM][C::FN], const Factors<C>& k, int wm, int wn, int lane,
+                                        uint8_t* lds, F&& f) {
   constexpr int kPitch = 36;             // floats; 16 rows are 2304 bytes
   float* t = reinterpret_cast<float*>(lds);
 #pragma unroll
@@ -435,28 +468,42 @@ __device__ __forceinline__ void by_rows(const floatx16 (&acc)[C::FM][C::FN], int
         const float4 hi = *reinterpret_cast<const float4*>(t + r * kPitch + c8 + 4);
         v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
         v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= k.row[i][half] * k.col[j][e];
         f((wm * C::FM + i) * 32 + 16 * half + r, (wn * C::FN + j) * 32 + c8, v);
         wave_sync();
         __builtin_amdgcn_sched_barrier(0);
       }
 }
 
-// f(column, row, w): eight neighbouring values of a tile column times mul as
-// f16.
+// f(column, row, w): eight neighbouring values of a tile column as f16, times
+// alpha and din[row], whose values load one block row ahead (din null: alpha).
 template <class C, class F>
-__device__ __forceinline__ void by_cols(const floatx16 (&acc)[C::FM][C::FN], float mul, int wm, int wn, int lane, uint8_t* lds,
-                                        F&& f) {
+__device__ __forceinline__ void by_cols(const floatx16 (&acc)[C::FM][C::FN], float alpha, const float* din, int wm, int wn,
+                                        int lane, uint8_t* lds, F&& f) {
   constexpr int kPitch = 80;             // bytes; 32 columns of 32 rows
+  float4 k[2][4];
+  auto load = [&](int i) {
 #pragma unroll
-  for (int i = 0; i < C::FM; ++i)
+    for (int q = 0; q < 4; ++q)
+      k[i & 1][q] = din ? *reinterpret_cast<const float4*>(din + (wm * C::FM + i) * 32 + 8 * q + 4 * (lane >> 5))
+                        : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+  };
+  load(0);
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) {
+    if (i + 1 < C::FM) load(i + 1);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
       const int el = renewed(lane), h = el >> 5, c = el & 31, r = el >> 2, c8 = (el & 3) * 8;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < 4; ++q) {
+        const float4 d = k[i & 1][q];
         *reinterpret_cast<uint2*>(lds + c * kPitch + 2 * (8 * q + 4 * h)) =
-            make_uint2(pack_f16(mul * acc[i][j][4 * q], mul * acc[i][j][4 * q + 1]),
-                       pack_f16(mul * acc[i][j][4 * q + 2], mul * acc[i][j][4 * q + 3]));
+            make_uint2(pack_f16(alpha * d.x * acc[i][j][4 * q], alpha * d.y * acc[i][j][4 * q + 1]),
+                       pack_f16(alpha * d.z * acc[i][j][4 * q + 2], alpha * d.w * acc[i][j][4 * q + 3]));
+      }
       wave_sync();
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -466,6 +513,18 @@ __device__ __forceinline__ void by_cols(const floatx16 (&acc)[C::FM][C::FN], flo
       wave_sync();
       __builtin_amdgcn_sched_barrier(0);
     }
+  }
+}
+
+// The diagonal of a 32 x 32 block on it: the lanes whose column c is one of
+// their rows (lane / 32 == c / 4 % 2) hold it at 4 (c / 8) + c % 4.
+__device__ __forceinline__ bool on_diagonal(int lane) { return (lane >> 5) == ((lane >> 2) & 1); }
+__device__ __forceinline__ float diagonal_of(const floatx16& v, int lane) {
+  const int c = lane & 31, at = 4 * (c >> 3) + (c & 3);
+  float d = v[0];
+#pragma unroll
+  for (int r = 1; r < 16; ++r) d = r == at ? v[r] : d;
+  return d;
 }
 
 // Eight neighbours of an f16 panel operand: row r, columns from c (a multiple
@@ -490,13 +549,12 @@ __device__ __forceinline__ void epilogue(const Args& a, int neach, floatx16 (&ac
   if constexpr (EP == PanelEp::Step || EP == PanelEp::Out) {
     // VEC: rows of whole 16-byte units, so that eight neighbours are in or out
     // together and move as such
-    by_rows<C>(acc, wm, wn, lane, lds, [&](int dr, int dc, float (&v)[8]) {
+    const Factors<C> k(alpha, moved(a.din, off), a.din_cols != 0, m0, n0, wm, wn, lane);
+    by_rows<C>(acc, k, wm, wn, lane, lds, [&](int dr, int dc, float (&v)[8]) {
       const int row = m0 + dr, col = n0 + dc;
       if (row >= a.M || col >= a.N) return;
       const int64_t at = (int64_t)row * a.N + col;
       const int n = a.N - col < 8 ? a.N - col : 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= alpha;
       float o[8];                        // the addend, or the weights
       if constexpr (EP == PanelEp::Step) {
         if constexpr (VEC) load8<OT>(out, at, o);
@@ -517,6 +575,7 @@ __device__ __forceinline__ void epilogue(const Args& a, int neach, floatx16 (&ac
       // A is symmetric: four neighbours of a column are four of a row; a
       // batch's loads go out before the first is used
       const uint8_t* A = a.a + off;
+      const float* D = moved(a.din, off);
       constexpr int kBatch = C::FM * C::FN > 4 ? 2 : C::FM;      // block rows at a time
       const int h = lane >> 5, c = lane & 31;
 #pragma unroll
@@ -543,14 +602,17 @@ __device__ __forceinline__ void epilogue(const Args& a, int neach, floatx16 (&ac
           for (int j = 0; j < C::FN; ++j) {
             // row - column of the lane's first value
             const int d = m0 - n0 + (wm * C::FM + i) * 32 - (wn * C::FN + j) * 32 + 4 * h - c;
+            const float dj = D[n0 + (wn * C::FN + j) * 32 + c];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
+              const float4 d4 = *reinterpret_cast<const float4*>(D + m0 + (wm * C::FM + i) * 32 + 8 * q + 4 * h);
+              const float di[4] = {d4.x, d4.y, d4.z, d4.w};
               const uint2 u = w[i - i0][j][q];
               const float av[4] = {f16_lo(u.x), f16_hi(u.x), f16_lo(u.y), f16_hi(u.y)};
 #pragma unroll
               for (int t = 0; t < 4; ++t) {
-                const float v = fmaf(a.cc, acc[i][j][4 * q + t], a.cb * av[t]);
-                acc[i][j][4 * q + t] = d + 8 * q + t == 0 ? v + a.ca : v;
+                const float v = fmaf(a.cc, fmaf(di[t] + dj, av[t], acc[i][j][4 * q + t]), a.cb * av[t]);
+                acc[i][j][4 * q + t] = d + 8 * q + t == 0 ? v + fmaf(a.cb, dj, a.ca) : v;
               }
             }
             // here, not where the stores need it (with A's values kept till then)
@@ -558,20 +620,36 @@ __device__ __forceinline__ void epilogue(const Args& a, int neach, floatx16 (&ac
           }
       }
     }
-    const float mul = EP == PanelEp::Poly ? 1.0f : alpha;
+    if constexpr (EP != PanelEp::Iter) {
+      if (I == J) {
+        float* dout = moved(a.dout, off);
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j) {
+            const int row = m0 + (wm * C::FM + i) * 32 + (lane & 31);
+            if (wm * C::FM + i != wn * C::FN + j || !on_diagonal(lane) || row >= a.M) continue;
+            const float v = (EP == PanelEp::Poly ? 1.0f : alpha) * diagonal_of(acc[i][j], lane), r = (float)(_Float16)v;
+            dout[row] = EP == PanelEp::Gram ? v - r : r != 0.0f ? v / r : 1.0f;
+          }
+      }
+    }
     // the transpose; a symmetric product's mirror (a diagonal tile is its own)
     constexpr bool kIter = EP == PanelEp::Iter;
     uint8_t* tdst = kIter ? a.out_t + off : out;
-    by_cols<C>(acc, mul, wm, wn, lane, lds, [&](int dc, int dr, uint4 w) {
+    const float mul = EP == PanelEp::Poly ? 1.0f : alpha;
+    const float* din = kIter ? moved(a.din, off) : nullptr;
+    by_cols<C>(acc, mul, din ? din + m0 : nullptr, wm, wn, lane, lds, [&](int dc, int dr, uint4 w) {
       if (n0 + dc < a.N && m0 + dr < a.M) *reinterpret_cast<uint4*>(panel_at(tdst, a.N, n0 + dc, m0 + dr)) = w;
     });
-    if (kIter || I != J)
-      by_rows<C>(acc, wm, wn, lane, lds, [&](int dr, int dc, float (&v)[8]) {
+    if (kIter || I != J) {
+      const Factors<C> k(mul, din, false, m0, n0, wm, wn, lane);
+      by_rows<C>(acc, k, wm, wn, lane, lds, [&](int dr, int dc, float (&v)[8]) {
         if (m0 + dr < a.M && n0 + dc < a.N)
           *reinterpret_cast<uint4*>(panel_at(out, a.M, m0 + dr, n0 + dc)) =
-              make_uint4(pack_f16(mul * v[0], mul * v[1]), pack_f16(mul * v[2], mul * v[3]),
-                         pack_f16(mul * v[4], mul * v[5]), pack_f16(mul * v[6], mul * v[7]));
+              make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
       });
+    }
   }
 }
 
@@ -986,6 +1064,9 @@ hipError_t launch_panel(const PanelProblem& g, const PanelPlan& p, bool fp4, voi
   a.out = static_cast<uint8_t*>(g.out);
   a.out_t = static_cast<uint8_t*>(g.out_t);
   a.a = g.a;
+  a.din = g.din;
+  a.dout = g.dout;
+  a.din_cols = g.din_cols ? 1 : 0;
   a.bstride = g.bstride;
   Each e;
   runs_of(p.tiles * g.batch, p.slots, p.parts, e.run);
