@@ -22,6 +22,9 @@ constexpr int kPanelScales = 8;    // scale bytes per panel row
 
 typedef float floatx2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+// neighbours in memory that are aligned to one element only
+typedef float float4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint16_t bf16x8u __attribute__((ext_vector_type(8), aligned(2)));
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }

@@ -10,15 +10,19 @@ namespace nvfp4 {
 namespace {
 using namespace mx;
 
-// Eight neighbouring elements; `n` < 8 at the end of the data.
+// Eight neighbouring elements, at any alignment; `n` < 8 at the end of a row
+// or of the data.
 template <Dt T>
 __device__ __forceinline__ void load8(const void* p, int64_t at, int n, float (&v)[8]) {
   if constexpr (T == Dt::F32) {
     const float* f = static_cast<const float*>(p) + at;
     if (n == 8) {
-      const float4 a = *reinterpret_cast<const float4*>(f), b = *reinterpret_cast<const float4*>(f + 4);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      const float4u a = *reinterpret_cast<const float4u*>(f), b = *reinterpret_cast<const float4u*>(f + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = i < n ? f[i] : 0.0f;
@@ -26,20 +30,14 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, int n, float (&
   } else {
     const uint16_t* f = static_cast<const uint16_t*>(p) + at;
     if (n == 8) {
-      const uint4 a = *reinterpret_cast<const uint4*>(f);
-      v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
-      v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z); v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
+      const bf16x8u a = *reinterpret_cast<const bf16x8u*>(f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float((uint32_t)a[i] << 16);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = i < n ? __uint_as_float((uint32_t)f[i] << 16) : 0.0f;
     }
   }
-}
-
-template <Dt T>
-__device__ __forceinline__ float load1(const void* p, int64_t at) {
-  if constexpr (T == Dt::F32) return static_cast<const float*>(p)[at];
-  else return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[at] << 16);
 }
 
 // v as it reads back after it was stored as T, and the store itself.
@@ -77,34 +75,43 @@ __device__ __forceinline__ float clamp_keep_nan(float v, float clip) {
   return v > clip ? clip : (v < -clip ? -clip : v);
 }
 
-// Sum of 256 threads' doubles, in a fixed order, left in every thread.
+// Sum of a workgroup's doubles, in a fixed order, left in every thread.
+template <int THREADS>
 __device__ __forceinline__ double block_sum(double v, double* lds) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) v += __shfl_down(v, d, 64);
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
-  return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+  v = lds[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 64; ++w) v += lds[w];
+  return v;
 }
 
+// One workgroup a CU, bound by the reads: four 16-byte loads of G are in
+// flight in each of a CU's 512 lanes (11008 x 4096 BF16: 61 us with one in
+// each of 256, 25 us so).  The momentum form has three streams and one load
+// of each (8 x 1024 x 4096, 335 MB: 67 us with 256 lanes, 56 us so).
+constexpr int kNormThreads = 512;
 template <Dt GT, Dt MT, bool MOM>
-__global__ __launch_bounds__(256) void norm_kernel(const Ns16Inputs in, int64_t count, float mu, int nesterov,
-                                                   double* part, int64_t bstride) {
-  __shared__ double lds[4];
+__global__ __launch_bounds__(kNormThreads) void norm_kernel(const Ns16Inputs in, int64_t count, float mu, int nesterov,
+                                                            double* part, int64_t bstride) {
+  constexpr int kAhead = MOM ? 1 : 4;
+  constexpr int64_t kStep = (int64_t)kNs16Parts * kNormThreads * 8;
+  __shared__ double lds[kNormThreads / 64];
   const int y = (int)blockIdx.y;
   const void* g = in.g[y];
   void* mom = in.mom[y];
   const float clip = in.clip[y];
   double sum = 0.0;
-  for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; at < count; at += (int64_t)kNs16Parts * 256 * 8) {
-    const int n = count - at < 8 ? (int)(count - at) : 8;
-    float v[8];
-    load8<GT>(g, at, n, v);
+  int64_t at = ((int64_t)blockIdx.x * kNormThreads + threadIdx.x) * 8;
+  auto one = [&](int64_t i0, int n, float (&v)[8]) {
     if constexpr (MOM) {
       float m[8];
-      load8<MT>(mom, at, n, m);
+      load8<MT>(mom, i0, n, m);
 #pragma unroll
       for (int i = 0; i < 8; ++i) m[i] = fmaf(mu, m[i], v[i]);
-      store8<MT>(mom, at, n, m);
+      store8<MT>(mom, i0, n, m);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = nesterov ? fmaf(mu, m[i], v[i]) : m[i];
     } else {
@@ -114,8 +121,22 @@ __global__ __launch_bounds__(256) void norm_kernel(const Ns16Inputs in, int64_t 
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < n) sum += (double)v[i] * (double)v[i];
+  };
+  for (; at + (kAhead - 1) * kStep + 8 <= count; at += kAhead * kStep) {
+    float v[kAhead][8];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) load8<GT>(g, at + k * kStep, 8, v[k]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) one(at + k * kStep, 8, v[k]);
   }
-  sum = block_sum(sum, lds);
+  for (; at < count; at += kStep) {
+    const int n = count - at < 8 ? (int)(count - at) : 8;
+    float v[8];
+    load8<GT>(g, at, n, v);
+    one(at, n, v);
+  }
+  sum = block_sum<kNormThreads>(sum, lds);
   if (threadIdx.x == 0)
     reinterpret_cast<double*>(reinterpret_cast<uint8_t*>(part) + (int64_t)y * bstride)[blockIdx.x] = sum;
 }
@@ -131,7 +152,7 @@ __global__ __launch_bounds__(256) void start_kernel(const Ns16Inputs in, int64_t
   const int y = (int)blockIdx.y, t = threadIdx.x;
   const int64_t off = (int64_t)y * bstride;
   const double* pp = reinterpret_cast<const double*>(reinterpret_cast<const uint8_t*>(part) + off);
-  const double norm = sqrt(block_sum(pp[t], lds)) + 1e-7;      // kNs16Parts == 256 threads
+  const double norm = sqrt(block_sum<256>(pp[t], lds)) + 1e-7;      // kNs16Parts == 256 threads
   const double s = (double)kNs16Scale / norm;
   const bool ok = isfinite(norm);
   const int e = ok ? ilogb(s) : 0;                             // 2^e <= s < 2^(e + 1)
@@ -148,32 +169,21 @@ __global__ __launch_bounds__(256) void start_kernel(const Ns16Inputs in, int64_t
   const float clip = in.clip[y];
   const int r = t >> 2, c = (t & 3) * 16;
   union { _Float16 h[16]; uint4 w[2]; } v;
-  const bool vec = cols % 8 == 0;
+  float x[2][8], m[2][8];
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
-    float x[8], m[8];
     const int64_t col = C + c + 8 * b, at = (R + r) * cols + col;
-    int n = R + r < rows && col < cols ? (cols - col < 8 ? (int)(cols - col) : 8) : 0;
-    if (vec || n == 0) {
-      if (n) {
-        load8<GT>(g, at, 8, x);
-        if constexpr (MOM) load8<MT>(mom, at, 8, m);
-      } else {
+    const int n = R + r < rows && col < cols ? (cols - col < 8 ? (int)(cols - col) : 8) : 0;
+    load8<GT>(g, at, n, x[b]);
+    if constexpr (MOM) load8<MT>(mom, at, n, m[b]);
+  }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = m[i] = 0.0f;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = i < n ? load1<GT>(g, at + i) : 0.0f;
-        if constexpr (MOM) m[i] = i < n ? load1<MT>(mom, at + i) : 0.0f;
-      }
-    }
+  for (int b = 0; b < 2; ++b) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float u;
-      if constexpr (MOM) u = nesterov ? fmaf(mu, m[i], x[i]) : m[i];
-      else u = clamp_keep_nan(x[i], clip);
+      if constexpr (MOM) u = nesterov ? fmaf(mu, m[b][i], x[b][i]) : m[b][i];
+      else u = clamp_keep_nan(x[b][i], clip);
       v.h[8 * b + i] = (_Float16)ldexpf(u, e);
     }
   }
@@ -212,7 +222,7 @@ hipError_t launch_ns16_norm(const Ns16Inputs& in, int batch, Dt gt, Dt mt, int64
   const dim3 grid(kNs16Parts, (unsigned)batch);
   return by_type(gt, mt, in.mom[0] != nullptr, [&](auto G, auto M, auto mom) {
     norm_kernel<decltype(G)::value, decltype(M)::value, decltype(mom)::value>
-        <<<grid, 256, 0, s>>>(in, count, mu, nesterov, part, bstride);
+        <<<grid, kNormThreads, 0, s>>>(in, count, mu, nesterov, part, bstride);
   });
 }
 
