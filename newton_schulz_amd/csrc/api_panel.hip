@@ -273,6 +273,7 @@ struct Ns16Layout {
   int64_t mp, np;
   size_t x, xt[2], a, b, da, rb, part, fac, total;   // of one matrix
   size_t split;                              // the batch's split tiles' partials, behind its matrices
+  bool fused;                                // B made by the products that use it
   PanelPlan gram, poly, iter, last;
 };
 
@@ -285,6 +286,11 @@ Ns16Layout ns16_layout(int64_t m, int64_t n, int batch) {
   L.poly = nvfp4::plan_panel(L.mp, L.mp, L.mp / 64, true, batch, true, true);
   L.iter = nvfp4::plan_panel(L.mp, L.np, L.mp / 64, false, batch, true, false);
   L.last = nvfp4::plan_panel(m, n, L.mp / 64, false, batch, true, false);
+  L.fused = nvfp4::poly_in_product(L.mp, L.np, batch);
+  if (L.fused) {
+    L.iter = nvfp4::plan_panel_poly(L.mp, L.np, batch);
+    L.last = nvfp4::plan_panel_poly(m, n, batch);
+  }
   size_t part = 0;
   for (const PanelPlan* p : {&L.gram, &L.poly, &L.iter, &L.last}) part = p->ws_bytes > part ? p->ws_bytes : part;
   size_t o = 0;
@@ -363,14 +369,23 @@ hipError_t ns16_batch(const nvfp4::Ns16Inputs& in, void* const* out, const float
     g.out = B;
     g.din = da;
     g.dout = rb;
-    e = nvfp4::launch_panel(g, L.poly, false, ws + (size_t)batch * L.total, s);
-    if (e != hipSuccess) return e;
+    if (!L.fused) {
+      e = nvfp4::launch_panel(g, L.poly, false, ws + (size_t)batch * L.total, s);
+      if (e != hipSuccess) return e;
+    }
     PanelProblem u;
     u.batch = batch;
     u.bstride = stride;
     u.panels = L.mp / 64;
     u.dalpha = it == 0 ? fac : nullptr;
     u.din = rb;
+    if (L.fused) {
+      u.da = da;
+      u.a = A;
+      u.ca = g.ca;
+      u.cb = g.cb;
+      u.cc = g.cc;
+    }
     if (it + 1 < c.k) {
       u.p = ob;
       u.q = oxt;

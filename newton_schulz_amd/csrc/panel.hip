@@ -74,8 +74,10 @@ struct Args {
   uint8_t* out_t;
   const uint8_t* a;
   const float* din;
+  const float* da;
   float* dout;
   int din_cols;
+  int wave_blocks;              // panel_poly_kernel: 32-row blocks of the other operand
   int64_t bstride;
 };
 
@@ -467,7 +469,8 @@ struct Factors {
   float row[C::FM][2];          // by_rows: row 16 half + lane / 4 of block row i
   float col[C::FN][8];          // and the lane's eight columns of block column j
 
-  __device__ __forceinline__ Factors(float alpha, const float* din, bool cols, int m0, int n0, int wm, int wn, int lane) {
+  // din: the tile's first row or column
+  __device__ __forceinline__ Factors(float alpha, const float* din, bool cols, int wm, int wn, int lane) {
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) row[i][0] = row[i][1] = alpha;
 #pragma unroll
@@ -478,12 +481,12 @@ struct Factors {
 #pragma unroll
       for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) row[i][h] *= din[m0 + (wm * C::FM + i) * 32 + 16 * h + (lane >> 2)];
+        for (int h = 0; h < 2; ++h) row[i][h] *= din[(wm * C::FM + i) * 32 + 16 * h + (lane >> 2)];
     } else if (din) {
 #pragma unroll
       for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) col[j][e] = din[n0 + (wn * C::FN + j) * 32 + (lane & 3) * 8 + e];
+        for (int e = 0; e < 8; ++e) col[j][e] = din[(wn * C::FN + j) * 32 + (lane & 3) * 8 + e];
     }
   }
 };
@@ -577,10 +580,16 @@ __device__ __forceinline__ uint8_t* panel_at(uint8_t* p, int rows, int r, int c)
   return p + ((int64_t)(c >> 6) * rows + r) * 128 + (c & 63) * 2;
 }
 
-// lds: this wave's kScratch bytes.  y: problem of the batch.
+// The factors of a tile's rows, or of its columns.
+__device__ __forceinline__ const float* tile_din(const Args& a, int y, int m0, int n0) {
+  return a.din ? moved(a.din, (int64_t)y * a.bstride) + (a.din_cols ? n0 : m0) : nullptr;
+}
+
+// lds: this wave's kScratch bytes.  y: problem of the batch.  din: tile_din
+// (Poly takes a.din itself).
 template <class C, PanelEp EP, Dt OT, bool VEC>
 __device__ __forceinline__ void epilogue(const Args& a, int neach, floatx16 (&acc)[C::FM][C::FN], int y, int I, int J,
-                                         int wm, int wn, int lane, uint8_t* lds) {
+                                         int wm, int wn, int lane, uint8_t* lds, const float* din) {
   const int m0 = I * C::B, n0 = J * C::B;
   const int64_t off = (int64_t)y * a.bstride;
   float alpha = a.alpha;
@@ -593,7 +602,7 @@ __device__ __forceinline__ void epilogue(const Args& a, int neach, floatx16 (&ac
   if constexpr (EP == PanelEp::Step || EP == PanelEp::Out) {
     // VEC: rows of whole 16-byte units, so that eight neighbours are in or out
     // together and move as such
-    const Factors<C> k(alpha, moved(a.din, off), a.din_cols != 0, m0, n0, wm, wn, lane);
+    const Factors<C> k(alpha, din, a.din_cols != 0, wm, wn, lane);
     by_rows<C>(acc, k, wm, wn, lane, lds, [&](int dr, int dc, float (&v)[8]) {
       const int row = m0 + dr, col = n0 + dc;
       if (row >= a.M || col >= a.N) return;
@@ -682,12 +691,12 @@ __device__ __forceinline__ void epilogue(const Args& a, int neach, floatx16 (&ac
     constexpr bool kIter = EP == PanelEp::Iter;
     uint8_t* tdst = kIter ? a.out_t + off : out;
     const float mul = EP == PanelEp::Poly ? 1.0f : alpha;
-    const float* din = kIter ? moved(a.din, off) : nullptr;
-    by_cols<C>(acc, mul, din ? din + m0 : nullptr, wm, wn, lane, lds, [&](int dc, int dr, uint4 w) {
+    if (!kIter) din = nullptr;
+    by_cols<C>(acc, mul, din, wm, wn, lane, lds, [&](int dc, int dr, uint4 w) {
       if (n0 + dc < a.N && m0 + dr < a.M) *reinterpret_cast<uint4*>(panel_at(tdst, a.N, n0 + dc, m0 + dr)) = w;
     });
     if (kIter || I != J) {
-      const Factors<C> k(mul, din, false, m0, n0, wm, wn, lane);
+      const Factors<C> k(mul, din, false, wm, wn, lane);
       by_rows<C>(acc, k, wm, wn, lane, lds, [&](int dr, int dc, float (&v)[8]) {
         if (m0 + dr < a.M && n0 + dc < a.N)
           *reinterpret_cast<uint4*>(panel_at(out, a.M, m0 + dr, n0 + dc)) =
@@ -815,7 +824,8 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks* C::kWaves / 4) void panel_
     } else {
       int y, I, J;
       place_of(a, un.tile, y, I, J);
-      epilogue<C, EP, OT, VEC>(a, e.n, acc, y, I, J, wm, wn, renewed(lane), scratch);
+      epilogue<C, EP, OT, VEC>(a, e.n, acc, y, I, J, wm, wn, renewed(lane), scratch,
+                               tile_din(a, y, I * C::B, J * C::B));
     }
     l += a.slots;
   } while (unit_of(a, run, l, un));
@@ -861,7 +871,8 @@ __global__ __launch_bounds__(C::kThreads) void panel_sum_kernel(const Each e, Ar
       acc[0][0][4 * q + 3] += v.w;
     }
   epilogue<OneBlock<C>, EP, OT, VEC>(a, e.n, acc, y, I, J, wave / C::WN * C::FM + b / C::FN, wave % C::WN * C::FN + b % C::FN,
-                                     lane, smem + wave * kScratch);
+                                     lane, smem + wave * kScratch,
+                                   tile_din(a, y, I * C::B, J * C::B));
 }
 
 // Small products: one 32 x 32 tile a workgroup, its eight waves dividing the
@@ -931,11 +942,123 @@ __global__ __launch_bounds__(512, 2) void panel_direct_kernel(const Each e, Args
       acc[0][0][4 * k + 2] += o.z;
       acc[0][0][4 * k + 3] += o.w;
     }
-  epilogue<Tile32, EP, OT, VEC>(a, e.n, acc, y, I, J, 0, 0, lane, scratch);
+  epilogue<Tile32, EP, OT, VEC>(a, e.n, acc, y, I, J, 0, 0, lane, scratch, tile_din(a, y, I * 32, J * 32));
+}
+
+// Small matrices: B's rows are made where they are used, by every workgroup
+// for itself, and never leave LDS -- one launch for B = a I + b A + c A^2 and
+// the product with it.  A workgroup has 32 rows of B: the whole of A comes
+// into LDS, eight waves divide the rows' 32 x 32 blocks, and then take one
+// 32-row block of the other operand each.  B's blocks are computed transposed,
+// so that a lane's four neighbours are neighbours of B's row.  Bound by its
+// launch and three trips to memory, 4 to 8 us.
+// FLIP: B is the product's right operand.
+template <PanelEp EP, Dt OT, bool VEC, bool FLIP>
+__global__ __launch_bounds__(512, 2) void panel_poly_kernel(const Each e, Args a) {
+  // A, then (where both fit, behind it) each wave's block of the other
+  // operand, whose place becomes the wave's epilogue scratch
+  constexpr int kRoom = kPolyPanels * kPolyPanels * 8192;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kRoom + kPolyPanels * 4096];
+  __shared__ __attribute__((aligned(16))) float factor[32];
+  uint8_t* bt = smem + kRoom;
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int stripes = FLIP ? a.TN : a.TM, blocks = FLIP ? a.TM : a.TN, groups = (blocks + a.wave_blocks - 1) / a.wave_blocks;
+  const int S = (int)blockIdx.x % stripes, rest = (int)blockIdx.x / stripes;
+  const int y = rest / groups, T = rest % groups * a.wave_blocks + wave;
+  const int64_t off = (int64_t)y * a.bstride;
+  const int panels = a.panels, lim = FLIP ? a.M : a.N;
+  const PanelOperand& o = FLIP ? a.p : a.q;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+  const int asize = panels * panels * 8192, xsize = panels * 4096;       // bytes; xsize: of a wave's block
+  const bool both = asize + a.wave_blocks * xsize <= kRoom;
+  const int x0 = (both ? asize : 0) + wave * xsize;
+
+  const uint8_t* A = a.a + off;
+  {
+    const uint32_t src = (uint32_t)((lane >> 3) * 128 + (((lane & 7) ^ swizzle(8 * wave + (lane >> 3))) << 4));
+    for (int i = wave; i < panels * panels * 8; i += 8) dma16(A, src + i * 1024u, lds0 + i * 1024u);
+  }
+  const bool mine = wave < a.wave_blocks && T < blocks;
+  auto load_x = [&] {
+    const uint8_t* data = o.data + off;
+    for (int g = 0; g < panels; ++g, data += o.rows * 128)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        // rows behind the operand's end read its last row: the epilogue drops them
+        int row = T * 32 + 8 * k + (lane >> 3);
+        row = row < lim ? row : lim - 1;
+        dma16(data, (uint32_t)row * 128u + (uint32_t)(((lane & 7) ^ swizzle(8 * k + (lane >> 3))) << 4),
+              lds0 + (uint32_t)(x0 + (g * 4 + k) * 1024));
+      }
+  };
+  if (both && mine) load_x();
+  const float* D = moved(a.da, off);
+  const float ds = D[S * 32 + r];
+  float4 dj[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    dj[k] = *reinterpret_cast<const float4*>(D + (wave < 2 * panels ? wave : 0) * 32 + 8 * k + 4 * h);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  all_waves();
+
+  // a 32-row block's fragment of step s, chunk 2 s + h of each row
+  auto frag = [&](const uint8_t* block, int s) {
+    return *reinterpret_cast<const intx4*>(block + r * 128 + (((2 * s + h) ^ swizzle(r)) << 4));
+  };
+  floatx16 acc[1][1];
+  static_assert(2 * kPolyPanels <= 8, "a block of B each");
+  if (wave < 2 * panels) {
+    const int j = wave;
+    clear<Tile32>(acc);
+    for (int g = 0; g < panels; ++g)
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        acc[0][0] = mfma_f16(frag(smem + g * panels * 8192 + j * 4096, s), frag(smem + g * panels * 8192 + S * 4096, s), acc[0][0]);
+    // value 4 k + t: column 32 j + 8 k + 4 h + t of B's row 32 S + r
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int chunk = (((j & 1) * 4 + k) ^ swizzle(r)) << 4;
+      const uint2 w = *reinterpret_cast<const uint2*>(smem + (j >> 1) * panels * 8192 + (S * 32 + r) * 128 + chunk + 8 * h);
+      const float dv[4] = {dj[k].x, dj[k].y, dj[k].z, dj[k].w};
+      const float av[4] = {f16_lo(w.x), f16_hi(w.x), f16_lo(w.y), f16_hi(w.y)};
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float v = fmaf(a.cc, fmaf(dv[t] + ds, av[t], acc[0][0][4 * k + t]), a.cb * av[t]);
+        acc[0][0][4 * k + t] = j == S && 8 * k + 4 * h + t == r ? v + fmaf(a.cb, ds, a.ca) : v;
+      }
+      *reinterpret_cast<uint2*>(bt + (j >> 1) * 4096 + r * 128 + chunk + 8 * h) =
+          make_uint2(pack_f16(acc[0][0][4 * k], acc[0][0][4 * k + 1]),
+                     pack_f16(acc[0][0][4 * k + 2], acc[0][0][4 * k + 3]));
+    }
+    if (j == S && on_diagonal(lane)) {
+      const float v = diagonal_of(acc[0][0], lane), d = (float)(_Float16)v;
+      factor[r] = d != 0.0f ? v / d : 1.0f;
+    }
+  }
+  // B is there, and nobody reads A any more
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  all_waves();
+  if (!mine) return;
+  if (!both) {
+    load_x();
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+  clear<Tile32>(acc);
+  for (int g = 0; g < panels; ++g)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const intx4 b = frag(bt + g * 4096, s), x = frag(smem + x0 + g * 4096, s);
+      acc[0][0] = FLIP ? mfma_f16(x, b, acc[0][0]) : mfma_f16(b, x, acc[0][0]);
+    }
+  wave_sync();
+  epilogue<Tile32, EP, OT, VEC>(a, e.n, acc, y, FLIP ? T : S, FLIP ? S : T, 0, 0, lane, smem + x0, factor);
 }
 
 template <class C, bool FP4, PanelEp EP, Dt OT, bool VEC>
 hipError_t launch_one(const Each& e, const Args& a, const PanelPlan& p, hipStream_t s) {
+  if constexpr (C::B == 32 && !FP4 && (EP == PanelEp::Out || EP == PanelEp::Step || EP == PanelEp::Iter))
+    if (a.da) return launch_poly<EP, OT, VEC>(e, a, s);
   if constexpr (C::B == 32) {
     panel_direct_kernel<FP4, EP, OT, VEC><<<dim3((unsigned)p.groups), C::kThreads, 0, s>>>(e, a);
     return hipGetLastError();
@@ -953,6 +1076,29 @@ hipError_t launch(const Each& e, const Args& a, const PanelPlan& p, hipStream_t 
   if constexpr (EP == PanelEp::Out || EP == PanelEp::Step)
     if (a.N % 8 != 0) return launch_one<C, FP4, EP, OT, false>(e, a, p, s);
   return launch_one<C, FP4, EP, OT, true>(e, a, p, s);
+}
+
+// Workgroups of panel_poly_kernel: `stripes` of B's rows, each with the other
+// operand's `blocks`, `each` to a workgroup.
+int64_t poly_groups(int64_t stripes, int64_t blocks, int each, int batch) {
+  return stripes * ((blocks + each - 1) / each) * batch;
+}
+
+template <PanelEp EP, Dt OT, bool VEC>
+hipError_t launch_poly(const Each& e, Args a, hipStream_t s) {
+  const int stripes = a.din_cols ? a.TN : a.TM, blocks = a.din_cols ? a.TM : a.TN;
+  // the fewest blocks a workgroup that leave one workgroup to a CU (256 x 512:
+  // 67 us with 1, 73 with 8; 128 x 4096: 108 with 1, in two rounds, 89 with 4)
+  a.wave_blocks = 1;
+  while (a.wave_blocks < 8 && poly_groups(stripes, blocks, a.wave_blocks, a.batch) > kXcds * kCusPerXcd) a.wave_blocks *= 2;
+  const dim3 grid((unsigned)poly_groups(stripes, blocks, a.wave_blocks, a.batch));
+  if constexpr (EP != PanelEp::Iter)
+    if (a.din_cols) {
+      panel_poly_kernel<EP, OT, VEC, true><<<grid, 512, 0, s>>>(e, a);
+      return hipGetLastError();
+    }
+  panel_poly_kernel<EP, OT, VEC, false><<<grid, 512, 0, s>>>(e, a);
+  return hipGetLastError();
 }
 
 template <class C>
@@ -1063,6 +1209,11 @@ double plan_cost(const PanelPlan& p, int64_t panels, int batch) {
 
 }  // namespace
 
+bool poly_in_product(int64_t mp, int64_t np, int batch) {
+  return mp <= 64 * kPolyPanels && poly_groups(mp / 32, np / 32, 8, batch) <= kXcds * kCusPerXcd;
+}
+PanelPlan plan_panel_poly(int64_t M, int64_t N, int batch) { return plan_tile<Tile32>(M, N, false, batch, 1); }
+
 PanelPlan plan_panel(int64_t M, int64_t N, int64_t panels, bool sym, int batch, bool allow_split, bool poly) {
   PanelPlan best{};
   double least = 0.0;
@@ -1109,6 +1260,7 @@ hipError_t launch_panel(const PanelProblem& g, const PanelPlan& p, bool fp4, voi
   a.out_t = static_cast<uint8_t*>(g.out_t);
   a.a = g.a;
   a.din = g.din;
+  a.da = g.da;
   a.dout = g.dout;
   a.din_cols = g.din_cols ? 1 : 0;
   a.bstride = g.bstride;

@@ -48,6 +48,11 @@ struct PanelProblem {
   const float* din = nullptr;
   float* dout = nullptr;
   bool din_cols = false;
+  // Iter, Out and Step with `da` given: the left operand (the right one when
+  // din_cols) is a I + b A + c A^2 with the coefficients above, made from A's
+  // panels `a` and da = its d, and din's factors come from it; p (or q) is not
+  // read.  Only with a plan_panel_poly plan.
+  const float* da = nullptr;
   // `batch` problems, each with its pointers moved by `bstride` bytes; the
   // row-major outputs may be given one by one, with their own alpha
   int batch = 1;
@@ -69,6 +74,16 @@ struct PanelPlan {
 // the 128 accumulators of a lane spill there (4 x 2048^2: 73 us,
 // 50 us on 128).
 PanelPlan plan_panel(int64_t M, int64_t N, int64_t panels, bool sym, int batch, bool allow_split, bool poly);
+// Whether the products with B (mp x mp, times mp x np) make it on the way:
+// while A fits LDS and one round of workgroups does it, a launch less per step
+// is worth more than B computed once.  Five steps (us, there / B by itself):
+// 50 x 512: 52 / 71, 128 x 1000: 72 / 92, 256 x 512: 67 / 76, four of
+// 256 x 2048: 130 / 139; the worst are 256 x 4096: 123 / 119 and sixteen of
+// 192 x 300: 95 / 88.  In two rounds:
+// 256 x 16384 213 / 200, four of 192 x 4096 154 / 150.
+constexpr int kPolyPanels = 4;
+bool poly_in_product(int64_t mp, int64_t np, int batch);
+PanelPlan plan_panel_poly(int64_t M, int64_t N, int batch);
 hipError_t launch_panel(const PanelProblem& g, const PanelPlan& p, bool fp4, void* ws, hipStream_t s);
 
 // ---- MXFP4 quantizers (mxfp4.hip) -------------------------------------------

@@ -69,6 +69,27 @@ def test_one_step_within_the_roundings_bound(m, n, ty):
         assert np.all(np.abs(got - want) <= tol + u * (np.abs(want) + tol)), float(np.max(np.abs(got - want) / tol))
 
 
+# Up to 256 rows the product with B makes B itself, with 1, 2, 4 or 8 blocks of
+# 32 columns to a workgroup (the third number), until a round of workgroups no
+# longer takes it (0).
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,blocks", [(64, 1000, 1), (130, 70, 1), (1500, 190, 2), (190, 2050, 2), (256, 1025, 2),
+                                        (250, 4096, 4), (4096, 256, 4), (129, 5000, 4), (60, 16300, 4), (7000, 256, 8),
+                                        (250, 6000, 8), (256, 8200, 0), (8200, 230, 0)])
+def test_one_step_with_b_made_in_the_product(m, n, blocks, ty):
+    test_one_step_within_the_roundings_bound(m, n, ty)
+
+
+@pytest.mark.parametrize("m,n,count", [(64, 300, 20), (300, 64, 32), (128, 1000, 16), (200, 700, 5), (256, 512, 16), (256, 520, 16)])
+def test_group_of_small_matrices(m, n, count):
+    gs = [_g(m, n, 50 + i) for i in range(count)]
+    outs = ns.ns_orthogonalize_f16_grouped([g for g, _ in gs], [QUINTIC] * 5)
+    for o, (_, v) in zip(outs, gs):
+        assert rel_fro(host(o), ns64(v, [QUINTIC] * 5)) <= FIVE
+    again = ns.ns_orthogonalize_f16_grouped([g for g, _ in gs], [QUINTIC] * 5)
+    assert all(torch.equal(a, b) for a, b in zip(outs, again))
+
+
 @pytest.mark.parametrize("ty", ["f32", "bf16"])
 @pytest.mark.parametrize("m,n", [(48, 64), (64, 64), (130, 100), (256, 512), (512, 300), (1000, 333), (1100, 1024)])
 def test_five_steps(m, n, ty):
