@@ -9,6 +9,7 @@ Projections, Optimizers, and Attention" (arXiv 2607.04422):
   closed form and encoded by exact comparison (round to nearest, ties to even).
 * ``nvfp4``    — the 1x16 / 16x1 block quantizer and the dequantizer
   (x_hat = x_E2M1 * s * s_g, §2 "NVFP4 format"; RTN per §3.4).
+* ``mxfp4``    — the MXFP4 quantizer, its storage in panels and the dequantizer.
 * ``rht``      — the random 16 x 16 Hadamard transform that §3.4 applies to
   every quantized operand along the contraction axis.
 * ``quantile`` — the p99 clip threshold as an order statistic of |G| (§3.4
