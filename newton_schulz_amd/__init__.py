@@ -644,18 +644,30 @@ def ns_orthogonalize_grouped_on(Gs, coeffs, streams, clips=None, clip_quantile=0
 
 # ----------------------------------------------------------------- MXFP4 --
 
+def _empty(shape, dtype, dev, stream):
+    """A new tensor, of the stream that the call enqueues on: the allocator may
+    give its memory away again as soon as that stream's work is in order."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if stream.device != dev:
+        raise ValueError(f"a stream of {stream.device} for tensors on {dev}")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _mx_panels(n):
     return -(-n // 256)
 
 
-def _mx_buffers(rows, cols, codes, scales, dev):
+def _mx_buffers(rows, cols, codes, scales, dev, stream):
     """Codes and scales of an operand of `rows` rows blocked along `cols`."""
     torch = _torch()
     p = _mx_panels(cols)
     if codes is None:
-        codes = torch.empty((p, rows, 128), dtype=torch.uint8, device=dev)
+        codes = _empty((p, rows, 128), torch.uint8, dev, stream)
     if scales is None:
-        scales = torch.empty((p, rows, 8), dtype=torch.uint8, device=dev)
+        scales = _empty((p, rows, 8), torch.uint8, dev, stream)
     return codes, scales
 
 
@@ -681,7 +693,7 @@ def mxfp4_quantize(x, axis=NVFP4_ROWS, codes=None, scales=None, stream=None):
     _need_2d(x, "x")
     rows, cols = x.shape
     r, c = (rows, cols) if axis == NVFP4_ROWS else (cols, rows)
-    codes, scales = _mx_buffers(r, c, codes, scales, x.device)
+    codes, scales = _mx_buffers(r, c, codes, scales, x.device, stream)
     _need_cuda(x, codes, scales)
     _need_mx(codes, scales, "out", r, c)
     with _on(x.device):
@@ -695,8 +707,8 @@ def mxfp4_quantize_both(x, along=None, down=None, stream=None):
     (codes, scales) of NVFP4_COLS)."""
     _need_2d(x, "x")
     rows, cols = x.shape
-    rc, rs = _mx_buffers(rows, cols, *(along or (None, None)), x.device)
-    cc, cs = _mx_buffers(cols, rows, *(down or (None, None)), x.device)
+    rc, rs = _mx_buffers(rows, cols, *(along or (None, None)), x.device, stream)
+    cc, cs = _mx_buffers(cols, rows, *(down or (None, None)), x.device, stream)
     _need_cuda(x, rc, rs, cc, cs)
     _need_mx(rc, rs, "along", rows, cols)
     _need_mx(cc, cs, "down", cols, rows)
@@ -709,10 +721,9 @@ def mxfp4_quantize_both(x, along=None, down=None, stream=None):
 def mxfp4_dequantize(codes, scales, rows, cols, axis=NVFP4_ROWS, out_dtype=NS_F32, out=None,
                      stream=None):
     """The values of an MXFP4 tensor, in the original rows x cols orientation."""
-    torch = _torch()
     _need_cuda(codes, scales, out)
     if out is None:
-        out = torch.empty((rows, cols), dtype=_out_dtype(out_dtype), device=codes.device)
+        out = _empty((rows, cols), _out_dtype(out_dtype), codes.device, stream)
     r, c = (rows, cols) if axis == NVFP4_ROWS else (cols, rows)
     _need_mx(codes, scales, "in", r, c)
     _need(out, "out", _floats(), rows * cols)
@@ -726,11 +737,11 @@ def mxfp4_gemm_workspace_bytes(M, N, K):
     return int(_lib.mxfp4_gemm_workspace_bytes(M, N, K))
 
 
-def _mx_workspace(need, workspace, dev):
+def _mx_workspace(need, workspace, dev, stream):
     """The given workspace, or a new one where the call needs any."""
     torch = _torch()
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        return _empty(need, torch.uint8, dev, stream) if need else None
     _need(workspace, "workspace", (torch.uint8,), 0)
     return workspace
 
@@ -749,9 +760,9 @@ def mxfp4_gemm(p, q, M, N, K, alpha=1.0, beta=0.0, addend=None, out_dtype=NS_F32
     (pc, ps), (qc, qs) = p, q
     dev = pc.device
     if out is None:
-        out = torch.empty((M, N), dtype=_out_dtype(out_dtype), device=dev)
+        out = _empty((M, N), _out_dtype(out_dtype), dev, stream)
     if workspace is not None or split:
-        workspace = _mx_workspace(mxfp4_gemm_workspace_bytes(M, N, K), workspace, dev)
+        workspace = _mx_workspace(mxfp4_gemm_workspace_bytes(M, N, K), workspace, dev, stream)
     _need_cuda(pc, ps, qc, qs, addend, out, workspace)
     _need_mx(pc, ps, "p", M, K)
     _need_mx(qc, qs, "q", N, K)
@@ -779,15 +790,14 @@ def mxfp4_linear(x, w, N, out=None, keep=False, kept=None, workspace=None, strea
 
     keep=True (or a `kept` pair of buffers) also quantizes x along the tokens
     and returns (y, kept), kept = (codes, scales) for mxfp4_linear_backward."""
-    torch = _torch()
     wc, ws_ = w
     _need_2d(x, "x")
     T, K = x.shape
     dev = x.device
     if out is None:
-        out = torch.empty((T, N), dtype=x.dtype, device=dev)
-    kc, ks = _mx_buffers(K, T, *(kept or (None, None)), dev) if keep or kept else (None, None)
-    workspace = _mx_workspace(mxfp4_linear_workspace_bytes(T, N, K), workspace, dev)
+        out = _empty((T, N), x.dtype, dev, stream)
+    kc, ks = _mx_buffers(K, T, *(kept or (None, None)), dev, stream) if keep or kept else (None, None)
+    workspace = _mx_workspace(mxfp4_linear_workspace_bytes(T, N, K), workspace, dev, stream)
     _need_cuda(x, wc, ws_, out, kc, ks, workspace)
     _need_mx(wc, ws_, "w", N, K)
     _need(out, "out", _floats(), T * N)
@@ -808,19 +818,18 @@ def mxfp4_linear_backward(dy, wt, kept, K, dx=None, dw=None, need_dx=True, need_
     returned by mxfp4_linear.  need_dx / need_dw False leaves one out (None is
     returned in its place).  dw = beta * dw + gradient (beta != 0 needs a
     float32 `dw`); new tensors take dy's dtype."""
-    torch = _torch()
     _need_2d(dy, "dy")
     T, N = dy.shape
     dev = dy.device
     if need_dx and dx is None:
-        dx = torch.empty((T, K), dtype=dy.dtype, device=dev)
+        dx = _empty((T, K), dy.dtype, dev, stream)
     if need_dw and dw is None:
         if float(beta) != 0.0:
             raise ValueError("beta != 0 adds to a dw that is given")
-        dw = torch.empty((N, K), dtype=dy.dtype, device=dev)
+        dw = _empty((N, K), dy.dtype, dev, stream)
     dx, dw = dx if need_dx else None, dw if need_dw else None
     (wc, ws_), (kc, ks) = wt if need_dx else (None, None), kept if need_dw else (None, None)
-    workspace = _mx_workspace(mxfp4_linear_backward_workspace_bytes(T, N, K), workspace, dev)
+    workspace = _mx_workspace(mxfp4_linear_backward_workspace_bytes(T, N, K), workspace, dev, stream)
     _need_cuda(dy, dx, dw, wc, ws_, kc, ks, workspace)
     if need_dx:
         _need_mx(wc, ws_, "wt", K, N)
@@ -859,13 +868,12 @@ def ns_orthogonalize_f16(G, coeffs, clip=float("inf"), out_dtype=NS_F32, out=Non
                          stream=None):
     """k Newton–Schulz steps with f16 operands on one m x n float32/bfloat16
     matrix of any shape."""
-    torch = _torch()
     _need_cuda(G, out)
     _need_2d(G, "G")
     m, n = G.shape
     if out is None:
-        out = torch.empty((m, n), dtype=_out_dtype(out_dtype), device=G.device)
-    workspace = _mx_workspace(ns_f16_workspace_bytes([(m, n)]), workspace, G.device)
+        out = _empty((m, n), _out_dtype(out_dtype), G.device, stream)
+    workspace = _mx_workspace(ns_f16_workspace_bytes([(m, n)]), workspace, G.device, stream)
     _need_ns(G, out, workspace)
     carr, k = _coeff_array(coeffs)
     with _on(G.device):
@@ -879,7 +887,6 @@ def ns_orthogonalize_f16_grouped(Gs, coeffs, clips=None, out_dtype=NS_F32, outs=
                                  workspace=None, stream=None):
     """ns_orthogonalize_f16 over a list of matrices; those of one shape run as
     one batch."""
-    torch = _torch()
     cnt = len(Gs)
     _need_cuda(*Gs)
     dt = _dt(Gs[0])
@@ -890,8 +897,8 @@ def ns_orthogonalize_f16_grouped(Gs, coeffs, clips=None, out_dtype=NS_F32, outs=
     shapes = [tuple(g.shape) for g in Gs]
     dev = Gs[0].device
     if outs is None:
-        outs = [torch.empty(s, dtype=_out_dtype(out_dtype), device=dev) for s in shapes]
-    workspace = _mx_workspace(ns_f16_workspace_bytes(shapes), workspace, dev)
+        outs = [_empty(s, _out_dtype(out_dtype), dev, stream) for s in shapes]
+    workspace = _mx_workspace(ns_f16_workspace_bytes(shapes), workspace, dev, stream)
     _need_group(Gs, outs, workspace)
     if clips is not None and len(clips) != cnt:
         raise ValueError("one clip per matrix")
@@ -900,7 +907,8 @@ def ns_orthogonalize_f16_grouped(Gs, coeffs, clips=None, out_dtype=NS_F32, outs=
     carr, k = _coeff_array(coeffs)
     with _on(dev):
         _check(_lib.ns_orthogonalize_f16_grouped(cnt, _pointers(Gs), ms, ns_, dt, carr, k, cl,
-                                                 _pointers(outs), _dt(outs[0]), *_ws_args(workspace), _stream(stream, dev)),
+                                                 _pointers(outs), _dt(outs[0]),
+                                                 *_ws_args(workspace), _stream(stream, dev)),
                "ns_orthogonalize_f16_grouped")
     return outs
 
@@ -910,7 +918,6 @@ def ns_muon_step(Ws, Ms, Gs, coeffs, lr, momentum=0.95, weight_decay=0.0, nester
     """One Muon step, in place on the weights Ws and momenta Ms (lists of
     matrices, each list of one dtype): M <- momentum M + G; U = G + momentum M
     (nesterov) or M; W <- (1 - lr weight_decay) W - lr scale NS(U)."""
-    torch = _torch()
     cnt = len(Ws)
     if cnt == 0 or len(Ms) != cnt or len(Gs) != cnt:
         raise ValueError("one momentum and one gradient per weight matrix, at least one")
@@ -926,7 +933,7 @@ def ns_muon_step(Ws, Ms, Gs, coeffs, lr, momentum=0.95, weight_decay=0.0, nester
     if scales is not None and len(scales) != cnt:
         raise ValueError("one scale per matrix")
     dev = Ws[0].device
-    workspace = _mx_workspace(ns_f16_workspace_bytes(shapes), workspace, dev)
+    workspace = _mx_workspace(ns_f16_workspace_bytes(shapes), workspace, dev, stream)
     _need_cuda(Ws[0], workspace)
     ms, ns_ = _shape_arrays(shapes)
     sc = (ctypes.c_float * cnt)(*[float(c) for c in scales]) if scales is not None else None

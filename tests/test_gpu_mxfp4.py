@@ -198,6 +198,35 @@ def test_two_streams_at_once():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_tensors_that_a_call_makes_belong_to_its_stream():
+    """With `stream` given and nothing else, the call's own workspace and
+    outputs are not handed to the current stream's work while it runs."""
+    T, N, K = 700, 640, 2048
+    x = torch.randn(T, K, device=DEV)
+    w = ns.mxfp4_quantize(torch.randn(N, K, device=DEV))
+    dy = torch.randn(T, N, device=DEV)
+    wt = ns.mxfp4_quantize(torch.randn(N, K, device=DEV), ns.NVFP4_COLS)
+    G = torch.randn(300, 700, device=DEV)
+    calls = [lambda s: ns.mxfp4_linear(x, w, N, keep=True, stream=s), lambda s: ns.mxfp4_quantize_both(x, stream=s),
+             lambda s: ns.mxfp4_linear_backward(dy, wt, kept, K, stream=s),
+             lambda s: ns.ns_orthogonalize_f16(G, [(3.4445, -4.775, 2.0315)] * 5, stream=s)]
+    kept = ns.mxfp4_linear(x, w, N, keep=True)[1]
+    flat = lambda v: [v] if isinstance(v, torch.Tensor) else [t for u in v for t in flat(u)]
+    want = [flat(c(None)) for c in calls]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got, noise = [], []
+    for _ in range(6):
+        for c in calls:
+            got.append(flat(c(side)))
+            # the current stream's memory, in the sizes that the call has used
+            noise = [torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV) for n in (1 << 20, 4 << 20, 1 << 22)]
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % len(calls)])), i
+    assert all(bool((n == 0xFF).all()) for n in noise)
+
+
 def test_binding_refuses():
     x = torch.randn(64, 96, device=DEV)
     q = ns.mxfp4_quantize(x)
