@@ -956,10 +956,12 @@ __global__ __launch_bounds__(512, 2) void panel_direct_kernel(const Each e, Args
 template <PanelEp EP, Dt OT, bool VEC, bool FLIP>
 __global__ __launch_bounds__(512, 2) void panel_poly_kernel(const Each e, Args a) {
   // A, then (where both fit, behind it) each wave's block of the other
-  // operand, whose place becomes the wave's epilogue scratch
-  constexpr int kRoom = kPolyPanels * kPolyPanels * 8192;
+  // operand, whose place becomes the wave's epilogue scratch: all of the
+  // largest A and one wave's block, so that a wave with A's time to load its
+  // own does (256 x 512: 67.6 us with the block loaded afterwards, 66.0 so).
+  // With B's rows that is the whole LDS; their factors go where A was.
+  constexpr int kRoom = kPolyPanels * kPolyPanels * 8192 + kPolyPanels * 4096;
   __shared__ __attribute__((aligned(16))) uint8_t smem[kRoom + kPolyPanels * 4096];
-  __shared__ __attribute__((aligned(16))) float factor[32];
   uint8_t* bt = smem + kRoom;
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -973,6 +975,7 @@ __global__ __launch_bounds__(512, 2) void panel_poly_kernel(const Each e, Args a
   const int asize = panels * panels * 8192, xsize = panels * 4096;       // bytes; xsize: of a wave's block
   const bool both = asize + a.wave_blocks * xsize <= kRoom;
   const int x0 = (both ? asize : 0) + wave * xsize;
+  float* factor = reinterpret_cast<float*>(smem + (both ? 0 : kRoom - 128));
 
   const uint8_t* A = a.a + off;
   {
@@ -1007,6 +1010,7 @@ __global__ __launch_bounds__(512, 2) void panel_poly_kernel(const Each e, Args a
     return *reinterpret_cast<const intx4*>(block + r * 128 + (((2 * s + h) ^ swizzle(r)) << 4));
   };
   floatx16 acc[1][1];
+  float mine_factor = 0.0f;
   static_assert(2 * kPolyPanels <= 8, "a block of B each");
   if (wave < 2 * panels) {
     const int j = wave;
@@ -1033,10 +1037,13 @@ __global__ __launch_bounds__(512, 2) void panel_poly_kernel(const Each e, Args a
     }
     if (j == S && on_diagonal(lane)) {
       const float v = diagonal_of(acc[0][0], lane), d = (float)(_Float16)v;
-      factor[r] = d != 0.0f ? v / d : 1.0f;
+      mine_factor = d != 0.0f ? v / d : 1.0f;
     }
   }
   // B is there, and nobody reads A any more
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  all_waves();
+  if (wave == S && on_diagonal(lane)) factor[r] = mine_factor;
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   all_waves();
   if (!mine) return;
