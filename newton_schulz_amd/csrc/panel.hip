@@ -876,73 +876,95 @@ __global__ __launch_bounds__(C::kThreads) void panel_sum_kernel(const Each e, Ar
 }
 
 // Small products: one 32 x 32 tile a workgroup, its eight waves dividing the
-// panels of K.  A lane loads its fragments straight from memory -- there is no
-// reuse worth an LDS stage -- and the waves' sums meet in LDS, in wave order.
-// The whole of a product's time is then one or two rounds of loads.  Step s
-// takes chunk 2 s + lane / 32 here, so that a load covers 32 bytes of a row.
+// panels of K, each through a double buffer of LDS of its own: no barriers
+// until the waves' sums meet, in wave order.  The whole of a product's time is
+// then one or two trips to memory.  (Fragments loaded straight into registers
+// touch 32 lines an instruction and fetch each line for every quarter of it.)
 struct Tile32 {
   static constexpr int B = 32, WM = 1, WN = 1, FM = 1, FN = 1, kWaves = 8, kThreads = 512, kBlocks = 2, kAcc = 16;
 };
 
 template <bool FP4, PanelEp EP, Dt OT, bool VEC>
 __global__ __launch_bounds__(512, 2) void panel_direct_kernel(const Each e, Args a) {
-  __shared__ float4 sums[Tile32::kWaves][4][64];
-  __shared__ __attribute__((aligned(16))) uint8_t scratch[kScratch];
+  constexpr int kBuf = 2 * 4096 + (FP4 ? 512 : 0);      // 32 rows of either operand, and their scales
+  constexpr int kLoads = FP4 ? 10 : 8;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[Tile32::kWaves * 2 * kBuf];
   int y, I, J;
   place_of(a, (int)blockIdx.x, y, I, J);
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g0 = a.panels * wave / Tile32::kWaves, g1 = a.panels * (wave + 1) / Tile32::kWaves;
+  uint8_t* mine = smem + wave * 2 * kBuf;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(mine));
   const int64_t off = (int64_t)y * a.bstride;
-  const int pr = I * 32 + r < a.M ? I * 32 + r : a.M - 1, qr = J * 32 + r < a.N ? J * 32 + r : a.N - 1;
-  const uint8_t* p = a.p.data + off + ((int64_t)g0 * a.p.rows + pr) * 128 + 16 * h;
-  const uint8_t* q = a.q.data + off + ((int64_t)g0 * a.q.rows + qr) * 128 + 16 * h;
-  const uint8_t* ps = FP4 ? a.p.scales + ((int64_t)g0 * a.p.rows + pr) * 8 : nullptr;
-  const uint8_t* qs = FP4 ? a.q.scales + ((int64_t)g0 * a.q.rows + qr) * 8 : nullptr;
+  // rows behind an operand's end read its last row: the epilogue drops them
+  auto row_of = [&](int first, int lim) { return (uint32_t)(first < lim ? first : lim - 1); };
+  auto load = [&](int g, int buf) {
+    const uint32_t to = lds0 + (uint32_t)(buf * kBuf);
+    const uint8_t* p = a.p.data + off + (int64_t)g * a.p.rows * 128;
+    const uint8_t* q = a.q.data + off + (int64_t)g * a.q.rows * 128;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // what the buffer held has been read
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int dr = 8 * k + (lane >> 3);
+      const uint32_t chunk = (uint32_t)(((lane & 7) ^ swizzle(dr)) << 4);
+      dma16(p, row_of(I * 32 + dr, a.M) * 128u + chunk, to + (uint32_t)(k * 1024));
+      dma16(q, row_of(J * 32 + dr, a.N) * 128u + chunk, to + (uint32_t)(4096 + k * 1024));
+    }
+    if constexpr (FP4) {
+      const uint32_t word = 4u * (uint32_t)(lane & 1);
+      dma4(a.p.scales + (int64_t)g * a.p.rows * 8, row_of(I * 32 + (lane >> 1), a.M) * 8u + word, to + 8192u);
+      dma4(a.q.scales + (int64_t)g * a.q.rows * 8, row_of(J * 32 + (lane >> 1), a.N) * 8u + word, to + 8448u);
+    }
+  };
   floatx16 acc[1][1];
   clear<Tile32>(acc);
-#pragma unroll 2
+  if (g0 < g1) load(g0, 0);
   for (int g = g0; g < g1; ++g) {
-    intx4 x[4], w[4];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      x[s] = *reinterpret_cast<const intx4*>(p + 32 * s);
-      w[s] = *reinterpret_cast<const intx4*>(q + 32 * s);
+    const int buf = (g - g0) & 1;
+    if (g + 1 < g1) {
+      load(g + 1, buf ^ 1);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
-    p += a.p.rows * 128;
-    q += a.q.rows * 128;
+    const uint8_t* st = mine + buf * kBuf + r * 128;
     uint2 sx = make_uint2(0, 0), sw = make_uint2(0, 0);
     if constexpr (FP4) {
-      sx = *reinterpret_cast<const uint2*>(ps);
-      sw = *reinterpret_cast<const uint2*>(qs);
-      ps += a.p.rows * 8;
-      qs += a.q.rows * 8;
+      sx = *reinterpret_cast<const uint2*>(mine + buf * kBuf + 8192 + r * 8);
+      sw = *reinterpret_cast<const uint2*>(mine + buf * kBuf + 8448 + r * 8);
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
+      const int at = ((2 * s + h) ^ swizzle(r)) << 4;
+      const intx4 x = *reinterpret_cast<const intx4*>(st + at), w = *reinterpret_cast<const intx4*>(st + 4096 + at);
       const int shift = 16 * (s & 1) + 8 * h;      // byte 2 s + h of the eight
       if constexpr (FP4)
-        acc[0][0] = mfma_fp4<0>(x[s], w[s], acc[0][0], (s < 2 ? sx.x : sx.y) >> shift, (s < 2 ? sw.x : sw.y) >> shift);
+        acc[0][0] = mfma_fp4<0>(x, w, acc[0][0], (s < 2 ? sx.x : sx.y) >> shift, (s < 2 ? sw.x : sw.y) >> shift);
       else
-        acc[0][0] = mfma_f16(x[s], w[s], acc[0][0]);
+        acc[0][0] = mfma_f16(x, w, acc[0][0]);
     }
   }
+  // the sums take the first buffers' place, the epilogue wave 0's second
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  wave_sync();
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    sums[wave][k][lane] = make_float4(acc[0][0][4 * k], acc[0][0][4 * k + 1], acc[0][0][4 * k + 2], acc[0][0][4 * k + 3]);
+    *reinterpret_cast<float4*>(mine + (k * 64 + lane) * 16) =
+        make_float4(acc[0][0][4 * k], acc[0][0][4 * k + 1], acc[0][0][4 * k + 2], acc[0][0][4 * k + 3]);
   __syncthreads();
   if (wave != 0) return;
 #pragma unroll
   for (int v = 1; v < Tile32::kWaves; ++v)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float4 o = sums[v][k][lane];
+      const float4 o = *reinterpret_cast<const float4*>(smem + v * 2 * kBuf + (k * 64 + lane) * 16);
       acc[0][0][4 * k] += o.x;
       acc[0][0][4 * k + 1] += o.y;
       acc[0][0][4 * k + 2] += o.z;
       acc[0][0][4 * k + 3] += o.w;
     }
-  epilogue<Tile32, EP, OT, VEC>(a, e.n, acc, y, I, J, 0, 0, lane, scratch, tile_din(a, y, I * 32, J * 32));
+  epilogue<Tile32, EP, OT, VEC>(a, e.n, acc, y, I, J, 0, 0, lane, smem + kBuf, tile_din(a, y, I * 32, J * 32));
 }
 
 // Small matrices: B's rows are made where they are used, by every workgroup
