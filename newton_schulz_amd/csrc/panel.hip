@@ -1207,14 +1207,15 @@ PanelPlan plan_at(int tile, int64_t M, int64_t N, bool sym, int batch, int parts
 //    256    256    64: 1.20   256: 1.75          3         6
 //    128    512   256: 0.62   512: 1.10          2         4
 //     64    512   256: 0.36   512: 0.47          1         3
-//     32    256   2.0 per panel of a wave (an eighth of them), 0.4 a round, 2 once
+//     32    256   0.55 per panel of a wave (an eighth of them), 2.3 a round, 0.8 once
 // Measured against this: 4096^2 x 4096 38 us on 256 (43 on 128, 73 on 64),
 // 2048^2 x 4096 16 us on 128 (27 on 256, 20 on 64), 1024^2 x 4096 9 us on 64
 // (26 and 14).  A split adds its partials' traffic and the second kernel:
-// 1024^2 x 16384 takes 43 us on 128 whole, 23 in 4 parts.  64^2 x 4096 takes
-// 6.4 us on 32 (7.7 on 64), 1000 x 777 x 1501 11.9 (7.3).
+// 1024^2 x 16384 takes 43 us on 128 whole, 23 in 4 parts.  Tiles of 32 against
+// 64: 64^2 with 32 panels 5.5 us (9.0), 512 x 768 with 16 panels 7.9 (10.9), with
+// 2 panels 6.0 (4.6), 1024^2 with 16 panels 15.0 (11.8).
 double plan_cost(const PanelPlan& p, int64_t panels, int batch) {
-  if (p.tile == 32) return 2.0 + ((int64_t)p.tiles * batch + 255) / 256 * (0.4 + 2.0 * ((panels + 7) / 8));
+  if (p.tile == 32) return 0.8 + ((int64_t)p.tiles * batch + 255) / 256 * (2.3 + 0.55 * ((panels + 7) / 8));
   const double slots = p.slots * kXcds;
   const int few = p.tile == 256 ? 64 : 256;
   const double low = p.tile == 256 ? 1.20 : p.tile == 128 ? 0.62 : 0.36;
