@@ -77,10 +77,10 @@ PanelPlan plan_panel(int64_t M, int64_t N, int64_t panels, bool sym, int batch, 
 // Whether the products with B (mp x mp, times mp x np) make it on the way:
 // while A fits LDS and one round of workgroups does it, a launch less per step
 // is worth more than B computed once.  Five steps (us, there / B by itself):
-// 50 x 512: 52 / 71, 128 x 1000: 72 / 92, 256 x 512: 67 / 76, four of
-// 256 x 2048: 130 / 139; the worst are 256 x 4096: 123 / 119 and sixteen of
-// 192 x 300: 95 / 88.  In two rounds:
-// 256 x 16384 213 / 200, four of 192 x 4096 154 / 150.
+// 50 x 512: 47 / 65, 128 x 1000: 55 / 69, 256 x 512: 61 / 68, four of
+// 256 x 2048: 112 / 124; the worst are 256 x 4096: 114 / 111 and sixteen of
+// 192 x 300: 94 / 87.  In two rounds: 256 x 16384 218 / 202, four of 256 x 4096
+// 182 / 160.
 constexpr int kPolyPanels = 4;
 bool poly_in_product(int64_t mp, int64_t np, int batch);
 PanelPlan plan_panel_poly(int64_t M, int64_t N, int batch);
@@ -96,8 +96,9 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
 // ---- MXFP4 products with few rows (mxfp4_few.hip) -------------------------------
 // Whether a product of T rows goes there: one launch that reads w once, against
 // a pass over x and a tiled product that reuses w.  Measured (us, x in BF16,
-// there / tiled): 11008 x 4096 weights, T = 1: 6 / 12, 16: 12 / 12, 32: 22 / 12;
-// 4096 x 4096, T = 16: 6 / 12, 32: 8 / 12.
+// there / tiled) on the GPU: 11008 x 4096 weights, T = 1: 6.1 / 9.4, 8: 8.9 / 9.4,
+// 16: 12.0 / 9.8, 32: 22 / 11; 4096 x 4096, T = 16: 6.1 / 6.6, 32: 8.4 / 7.5; launched
+// one by one from Python 11 / 16, which decides up to 16.
 constexpr int64_t kMxFewRows = 32;
 inline bool mx_few(int64_t T, int64_t N, int64_t K) {
   return T <= 16 || (T <= kMxFewRows && N * K <= (int64_t)1 << 24);
