@@ -973,7 +973,7 @@ __global__ __launch_bounds__(512, 2) void panel_direct_kernel(const Each e, Args
 // into LDS, eight waves divide the rows' 32 x 32 blocks, and then take one
 // 32-row block of the other operand each.  B's blocks are computed transposed,
 // so that a lane's four neighbours are neighbours of B's row.  Bound by its
-// launch and three trips to memory, 4 to 8 us.
+// launch and two or three trips to memory, 5 to 8 us.
 // FLIP: B is the product's right operand.
 template <PanelEp EP, Dt OT, bool VEC, bool FLIP>
 __global__ __launch_bounds__(512, 2) void panel_poly_kernel(const Each e, Args a) {
