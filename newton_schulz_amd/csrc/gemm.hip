@@ -276,16 +276,17 @@ __device__ __forceinline__ void tile_of(const FastArgs& a, int t, int64_t& I, in
 // treat the asynchronous LDS write as pending before every later LDS read;
 // the kernel orders it explicitly with s_waitcnt vmcnt + s_barrier.  The
 // instruction has no register results; its address operands are read at
-// issue.
+// issue.  It takes the LDS base from M0, which has to be written a wait state
+// before (s_nop; the compiler does not look inside the asm).
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
                : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds)
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds)
                : "memory", "m0");
 }
 

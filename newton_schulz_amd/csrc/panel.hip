@@ -197,15 +197,17 @@ __device__ __forceinline__ int renewed(int v) {
 // Global -> LDS DMA: lane l's bytes land at lds + 16 l (4 l).  Inline asm, so
 // that the compiler does not take the LDS write as pending before every later
 // LDS read; ordered by s_waitcnt vmcnt and the stage's barrier.  There are no
-// register results, and the address operands are read at issue.
+// register results, and the address operands are read at issue.  The LDS base
+// comes from M0, which has to be written a wait state before (s_nop; the
+// compiler does not look inside the asm).
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
 }
 
 // s_barrier that no memory access moves across (the builtin alone does not
