@@ -576,6 +576,15 @@ __device__ __forceinline__ float diagonal_of(const floatx16& v, int lane) {
   return d;
 }
 
+// What B's row is multiplied by for its diagonal's sake, B_ii / f16(B_ii): within
+// 2^-11 of 1 while f16 holds B_ii as a normal number.  Below that the quotient
+// may be anything from 0.5 to 2 and would scale the entries that carry the row,
+// for a loss of 2^-25 at most: such a row is left alone.
+__device__ __forceinline__ float row_factor(float v) {
+  const float r = (float)(_Float16)v;
+  return fabsf(r) >= 0x1p-14f ? v / r : 1.0f;
+}
+
 // Eight neighbours of an f16 panel operand: row r, columns from c (a multiple
 // of 8) of an operand with `rows` rows a panel.
 __device__ __forceinline__ uint8_t* panel_at(uint8_t* p, int rows, int r, int c) {
@@ -684,8 +693,8 @@ __device__ __forceinline__ void epilogue(const Args& a, int neach, floatx16 (&ac
           for (int j = 0; j < C::FN; ++j) {
             const int row = m0 + (wm * C::FM + i) * 32 + (lane & 31);
             if (wm * C::FM + i != wn * C::FN + j || !on_diagonal(lane) || row >= a.M) continue;
-            const float v = (EP == PanelEp::Poly ? 1.0f : alpha) * diagonal_of(acc[i][j], lane), r = (float)(_Float16)v;
-            dout[row] = EP == PanelEp::Gram ? v - r : r != 0.0f ? v / r : 1.0f;
+            const float v = (EP == PanelEp::Poly ? 1.0f : alpha) * diagonal_of(acc[i][j], lane);
+            dout[row] = EP == PanelEp::Gram ? v - (float)(_Float16)v : row_factor(v);
           }
       }
     }
@@ -1059,10 +1068,7 @@ __global__ __launch_bounds__(512, 2) void panel_poly_kernel(const Each e, Args a
           make_uint2(pack_f16(acc[0][0][4 * k], acc[0][0][4 * k + 1]),
                      pack_f16(acc[0][0][4 * k + 2], acc[0][0][4 * k + 3]));
     }
-    if (j == S && on_diagonal(lane)) {
-      const float v = diagonal_of(acc[0][0], lane), d = (float)(_Float16)v;
-      mine_factor = d != 0.0f ? v / d : 1.0f;
-    }
+    if (j == S && on_diagonal(lane)) mine_factor = row_factor(diagonal_of(acc[0][0], lane));
   }
   // B is there, and nobody reads A any more
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

@@ -41,7 +41,8 @@ struct PanelProblem {
   // What f16 takes from the diagonals, which carry most of A's and B's norm,
   // is put back in FP32: Gram writes d = A_ii - f16(A_ii) to dout; Poly takes
   // it as din -- A^2 is A~^2 + (d_i + d_j) A~_ij to first order -- and writes
-  // B_ii / f16(B_ii) to dout; Iter, Out and Step multiply their rows by din
+  // B_ii / f16(B_ii) to dout (1 where f16 holds B_ii as a subnormal number);
+  // Iter, Out and Step multiply their rows by din
   // (columns when din_cols), which is B's diagonal put right as long as that
   // dominates its rows.  Halves the error of five steps (92 x 868: 2.0e-3 ->
   // 1.05e-3).  Arrays of M rounded up to 256 rows; null: none.
