@@ -458,11 +458,19 @@ ns_status mxfp4_linear_backward(const void* dy, ns_dtype dyt, int64_t T, int64_t
  *   A = X X^T;  B = a I + b A + c A A;  X <- B X
  * X (times 256), A and B are rounded to f16 once per step, and what that
  * takes from A's and B's diagonals is put back in FP32; BF16 sources enter
- * without rounding.  Five quintic steps stay within 2e-3 of exact arithmetic
- * (relative Frobenius norm, before the output's own rounding; 0.7e-3 to
- * 1.6e-3 measured) on matrices whose singular values span three decades or
- * less; directions further below the norm are amplified together with the
- * rounding of those above them.  |X| beyond 255 (divergent coefficients)
+ * without rounding.  The rounding of X leaves an error of 2e-4 of its norm,
+ * spread evenly over all directions, and the steps amplify it there as they
+ * amplify X: small directions by up to the product of the a's (485 for five
+ * quintic steps).  What five quintic steps are off by (relative Frobenius norm,
+ * before the output's own rounding) therefore goes by the spectrum of G:
+ *   singular values alike                     0.4e-3 to 2e-3
+ *   spread evenly (log scale) over a decade   1e-3
+ *   over two decades                          2e-3 to 4e-3
+ *   over three decades                        3e-3 (2048 rows) to 1.5e-2 (16)
+ *   up to 32 above a floor of 1/100 of them   0.5e-3 (2048 rows) to 1.5e-2
+ *   the same, a floor of 1/1000               0.5e-2 to 6e-2
+ * and it is at most 2e-3 + 0.2 / ||X_k||_F.  BF16 sources, without the rounding
+ * of X_0, are off by up to 40% less.  |X| beyond 255 (divergent coefficients)
  * overflows to infinities and NaN.  NaN or infinity in a matrix makes
  * its result NaN; a zero matrix gives zero.  Dimensions are 1 .. 2^24, of any
  * parity, m * n < 2^31.
@@ -498,7 +506,8 @@ typedef struct {
  *   M <- momentum M + G                      (stored in M's type)
  *   U = G + momentum M  or  M                (M as stored)
  *   W <- (1 - lr weight_decay) W - lr scale_i NS(U)
- * with NS the k steps above (no clipping).
+ * with NS the k steps above (no clipping): f16 operands, off by what the list
+ * above says for U's spectrum.  U itself is FP32.
  *   W, M    HOST arrays of device pointers, updated in place, FP32 or BF16
  *           (wt, mt); G likewise (gt), read only.  m, n  HOST arrays.
  *   scale   HOST array of one factor per matrix (such as

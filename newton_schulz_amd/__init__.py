@@ -867,7 +867,11 @@ def _pointers(ts):
 def ns_orthogonalize_f16(G, coeffs, clip=float("inf"), out_dtype=NS_F32, out=None, workspace=None,
                          stream=None):
     """k Newton–Schulz steps with f16 operands on one m x n float32/bfloat16
-    matrix of any shape."""
+    matrix of any shape.
+
+    Five quintic steps are off by 0.4e-3 to 2e-3 (relative Frobenius norm) for
+    singular values alike or within a decade, 4e-3 within two, up to 1.5e-2
+    within three, and at most 2e-3 + 0.2 / ||result||_F."""
     _need_cuda(G, out)
     _need_2d(G, "G")
     m, n = G.shape
@@ -917,7 +921,10 @@ def ns_muon_step(Ws, Ms, Gs, coeffs, lr, momentum=0.95, weight_decay=0.0, nester
                  workspace=None, stream=None):
     """One Muon step, in place on the weights Ws and momenta Ms (lists of
     matrices, each list of one dtype): M <- momentum M + G; U = G + momentum M
-    (nesterov) or M; W <- (1 - lr weight_decay) W - lr scale NS(U)."""
+    (nesterov) or M; W <- (1 - lr weight_decay) W - lr scale NS(U).
+
+    NS runs on f16 operands, whatever the arrays' types, and is off by as much
+    as ns_orthogonalize_f16."""
     cnt = len(Ws)
     if cnt == 0 or len(Ms) != cnt or len(Gs) != cnt:
         raise ValueError("one momentum and one gradient per weight matrix, at least one")

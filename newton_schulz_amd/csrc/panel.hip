@@ -578,7 +578,7 @@ __device__ __forceinline__ float diagonal_of(const floatx16& v, int lane) {
 
 // What B's row is multiplied by for its diagonal's sake, B_ii / f16(B_ii): within
 // 2^-11 of 1 while f16 holds B_ii as a normal number.  Below that the quotient
-// may be anything from 0.5 to 2 and would scale the entries that carry the row,
+// may be anything from 0.5 to 1.5 and would scale the entries that carry the row,
 // for a loss of 2^-25 at most: such a row is left alone.
 __device__ __forceinline__ float row_factor(float v) {
   const float r = (float)(_Float16)v;

@@ -1,4 +1,5 @@
-"""What 16-bit Newton–Schulz rounds and what it puts back, against float64."""
+"""What 16-bit Newton–Schulz rounds and what it puts back, against float64:
+the factors of B's rows, and the error by spectrum."""
 import numpy as np
 import pytest
 import torch
@@ -55,3 +56,113 @@ def test_a_vanishing_diagonal_of_b_leaves_its_row_alone(m, n):
         got = host(ns.ns_orthogonalize_f16(_dev(src), [(a, -1.0, 0.0)]))
         got = got if m <= n else got.T
         assert np.all(np.abs(got - want) <= tol + U32 * np.abs(want)), (eps, float(np.max(np.abs(got - want) / (tol + 1e-45))))
+
+
+# ---- the error by spectrum -------------------------------------------------------
+
+# Rounding to f16 changes a value by up to half a step, evenly: 2^-11 / sqrt(3)
+# of the binade's lower end in the root mean square; over a binade of values
+# spread evenly on a logarithmic scale that is this much of the value.
+RMS16 = U16 / np.sqrt(3) * np.sqrt(0.75 / (2 * np.log(2)))
+
+
+def _through(s, coeffs):
+    """p(s) of the steps and its derivative."""
+    p, dp = s.copy(), np.ones_like(s)
+    for a, b, c in coeffs:
+        dp = (a + 3 * b * p ** 2 + 5 * c * p ** 4) * dp
+        p = a * p + b * p ** 3 + c * p ** 5
+    return p, dp
+
+
+def _gains(s, coeffs):
+    """What the steps make of a small change E of X = U diag(s) V^T, in that
+    basis: entry by entry, of E's symmetric and antisymmetric part and (right of
+    the square) of each row."""
+    p, dp = _through(s, coeffs)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        sym = np.where(np.abs(s[:, None] - s) > 1e-9 * (s[:, None] + s), (p[:, None] - p) / (s[:, None] - s),
+                       (dp[:, None] + dp) / 2)
+    return sym, (p[:, None] + p) / (s[:, None] + s), p / s
+
+
+def _expected_error(s, n, coeffs, x0_rounded):
+    """Relative error (Frobenius norm) that the f16 roundings make, to first
+    order and as independent errors spread evenly over the entries: X_0 (FP32
+    sources) to X_k-1, and of every step A and B outside their diagonals."""
+    m, var, cur = len(s), 0.0, s / np.linalg.norm(s)
+    for it, (a, b, c) in enumerate(coeffs):
+        if it or x0_rounded:
+            sym, anti, right = _gains(cur, coeffs[it:])
+            var += np.sum(cur ** 2) / (m * n) * (np.sum(sym ** 2) / 2 + np.sum(anti ** 2) / 2 + (n - m) * np.sum(right ** 2))
+        lam = cur ** 2
+        bl = a + b * lam + c * lam ** 2
+        after = _gains(bl * cur, coeffs[it + 1:])
+        for off, gain in ((np.sum(lam ** 2) - np.sum(lam) ** 2 / m, (b + c * (lam[:, None] + lam)) * cur),
+                          # B's rows are also multiplied by what its diagonals lost
+                          (2 * (np.sum(bl ** 2) - np.sum(bl) ** 2 / m), np.broadcast_to(cur, (m, m)))):
+            sym, anti = (gain + gain.T) / 2 * after[0], (gain - gain.T) / 2 * after[1]
+            var += max(off, 0.0) / (m * m) * (np.sum(sym ** 2) + np.sum(anti ** 2))
+        cur = bl * cur
+    return RMS16 * np.sqrt(var) / np.linalg.norm(cur)
+
+
+def _spectrum(kind, m):
+    if kind == "alike":
+        return np.ones(m)
+    if kind.startswith("decades"):
+        return np.logspace(0, -float(kind[7:]), m)
+    few, floor = kind[4:].split("over")
+    s = np.full(m, float(floor))
+    s[:int(few)] = 1
+    return s
+
+
+def _with_spectrum(s, n, seed):
+    g = np.random.default_rng(seed)
+    u = np.linalg.qr(g.standard_normal((len(s), len(s))))[0]
+    return (u * s) @ np.linalg.qr(g.standard_normal((n, len(s))))[0].T
+
+
+@pytest.mark.parametrize("ty", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["alike", "decades1", "decades2", "decades3", "few 8over0.01", "few 8over0.001",
+                                  "few 32over0.001"])
+@pytest.mark.parametrize("m,n", [(64, 100), (256, 512), (512, 512), (300, 1000), (1000, 333), (900, 1100)])
+def test_five_steps_by_spectrum(m, n, kind, ty):
+    """The error is what the roundings make of this spectrum, times at most 1.5:
+    1.36 if all values sat at their binades' lower ends, and the spread of a sum
+    of many independent errors."""
+    k, kn = min(m, n), max(m, n)
+    G = _with_spectrum(_spectrum(kind, k), kn, m + n)
+    src = _dev(G if m <= n else G.T, ty)
+    G = src.double().cpu().numpy()
+    G = G if m <= n else G.T
+    u, s, vt = np.linalg.svd(G, full_matrices=False)
+    p, _ = _through(s / np.linalg.norm(s), [QUINTIC] * 5)
+    want = (u * p) @ vt
+    got = host(ns.ns_orthogonalize_f16(src, [QUINTIC] * 5))
+    err = np.linalg.norm((got if m <= n else got.T) - want) / np.linalg.norm(p)
+    expected = _expected_error(s, kn, [QUINTIC] * 5, ty == torch.float32)
+    print(f"[spectrum] {m}x{n} {kind} {ty}: {err:.2e}, expected {expected:.2e}", flush=True)
+    assert err <= 1.5 * expected
+    assert err <= 2e-3 + 0.2 / np.linalg.norm(p)                 # the documented bound
+
+
+CUBIC = (1.5, -0.5, 0.0)
+
+
+@pytest.mark.parametrize("name,coeffs", [("seven", [QUINTIC] * 7), ("cubic", [CUBIC] * 8), ("mixed", [QUINTIC] * 3 + [CUBIC] * 2),
+                                         ("falling", [(4.0, -6.5, 3.0), (3.6, -5.4, 2.5), (3.0, -4.0, 1.8), (2.2, -2.0, 0.7)])])
+@pytest.mark.parametrize("m,n", [(100, 160), (400, 700), (700, 400)])
+def test_other_schedules_by_spectrum(m, n, name, coeffs):
+    """Steps with coefficients of their own, more and fewer of them."""
+    k, kn = min(m, n), max(m, n)
+    for kind in ("decades1", "decades2"):
+        G = _with_spectrum(_spectrum(kind, k), kn, m + 2 * n)
+        src = _dev(G if m <= n else G.T)
+        G = src.double().cpu().numpy()
+        u, s, vt = np.linalg.svd(G if m <= n else G.T, full_matrices=False)
+        p, _ = _through(s / np.linalg.norm(s), coeffs)
+        got = host(ns.ns_orthogonalize_f16(src, coeffs))
+        err = np.linalg.norm((got if m <= n else got.T) - (u * p) @ vt) / np.linalg.norm(p)
+        assert err <= 1.5 * _expected_error(s, kn, coeffs, True), kind
