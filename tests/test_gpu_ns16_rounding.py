@@ -1,5 +1,5 @@
 """What 16-bit Newton–Schulz rounds and what it puts back, against float64:
-the factors of B's rows, and the error by spectrum."""
+the factors of B's rows, the corrected diagonals, and the error by spectrum."""
 import numpy as np
 import pytest
 import torch
@@ -56,6 +56,82 @@ def test_a_vanishing_diagonal_of_b_leaves_its_row_alone(m, n):
         got = host(ns.ns_orthogonalize_f16(_dev(src), [(a, -1.0, 0.0)]))
         got = got if m <= n else got.T
         assert np.all(np.abs(got - want) <= tol + U32 * np.abs(want)), (eps, float(np.max(np.abs(got - want) / (tol + 1e-45))))
+
+
+# ---- the corrected diagonals -----------------------------------------------------
+
+def _orthogonal_rows(k, kn, seed):
+    """k orthogonal rows of kn columns, d_i times +-1 or 0, d_i integers of seven
+    bits, sixteen times as large in four rows (which then hold most of A)."""
+    g = np.random.default_rng(seed)
+    d = g.integers(65, 128, size=k).astype(np.float64)
+    d[g.permutation(k)[:4]] *= 16
+    size = min(1024, 1 << (kn.bit_length() - 1))     # sums of d_i d_j stay within 24 bits
+    h = _hadamard(size)
+    h = h[g.permutation(size)[:k]]
+    G = np.zeros((k, kn))
+    G[:, np.sort(g.permutation(kn)[:size])] = h
+    return d[:, None] * G, d, size
+
+
+def _rows_recursion(d, size, coeffs):
+    """The scale x_i of every row of X_k = x_i times its +-1, with X rounded to
+    f16 behind each step but the last as the iteration does; which rows stay
+    clear of ties by more than FP32's errors; the relative error allowed."""
+    x = d / (np.sqrt(size * np.sum(d ** 2)) + 1e-7)
+    clear = np.ones(len(d), bool)
+    plain = np.zeros(len(d))                  # what uncorrected diagonals would be off by
+    for it, (a, b, c) in enumerate(coeffs):
+        A = size * x * x
+        B = a + b * A + c * A * A
+        # A: the factors t and t^2 and the scaling (6), the sum itself exact but
+        # for squares of rounded values, which may lose half a unit each; B:
+        # four operations on terms of these sizes, c d^2 left out; then the row's
+        # factor, the product and two scalings (6)
+        sums = 6 + (size / 2 if it else 0)
+        half = 2.0 ** (np.floor(np.log2(A)) - 11)
+        tol = U32 * (sums * (abs(b) * A + 2 * abs(c) * A * A) + 4 * (abs(a) + abs(b) * A + abs(c) * A * A)) / np.abs(B) \
+            + abs(c) * half ** 2 / np.abs(B) + 6 * U32
+        Ah = A.astype(np.float16).astype(np.float64)
+        Bh = (a + b * Ah + c * Ah * Ah).astype(np.float16).astype(np.float64)
+        plain = np.maximum(plain, np.abs(Bh / B - 1))
+        x = B * x
+        if it + 1 < len(coeffs):
+            v = 256 * x
+            step = 2.0 ** (np.floor(np.log2(v)) - 10)
+            away = np.abs(v / step - np.floor(v / step) - 0.5) * step      # from the tie
+            clear &= away > 2 * tol * v
+            x = v.astype(np.float16).astype(np.float64) / 256
+    return x, clear, tol, plain
+
+
+# B made in the product (up to 256 rows) and by itself, on every tile size; the
+# factors of rows and, where m > n, of columns; batches
+@pytest.mark.parametrize("ty", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,n,count", [(8, 8, 1), (64, 100, 1), (100, 64, 3), (256, 512, 1), (512, 256, 1), (200, 1000, 4),
+                                       (300, 1000, 1), (1000, 300, 2), (512, 600, 8), (1000, 512, 4), (1000, 4100, 1),
+                                       (4100, 1000, 2), (1024, 4096, 8), (2900, 1000, 8)])
+@pytest.mark.parametrize("steps", [1, 2])
+def test_what_f16_takes_from_the_diagonals_is_put_back(m, n, count, steps, ty):
+    """Of orthogonal rows A and B are diagonal, and a row's scale is a recursion
+    of its own: it holds to FP32, though f16 holds neither A_ii nor B_ii."""
+    k, kn = min(m, n), max(m, n)
+    coeffs = [QUINTIC] * steps
+    made = [_orthogonal_rows(k, kn, 1000 * steps + i) for i in range(count)]
+    src = [_dev(G if m <= n else G.T, ty) for G, _, _ in made]
+    outs = ns.ns_orthogonalize_f16_grouped(src, coeffs)
+    lr, W, M = 0.5, [torch.zeros(m, n, device=DEV) for _ in made], [torch.zeros(m, n, device=DEV) for _ in made]
+    scales = [1.0 + i for i in range(count)]
+    ns.ns_muon_step(W, M, src, coeffs, lr=lr, momentum=0.0, nesterov=False, scales=scales)
+    for o, w, sc, (G, d, size) in zip(outs, W, scales, made):
+        x, clear, tol, plain = _rows_recursion(d, size, coeffs)
+        assert clear.mean() > 0.9 and np.max(plain / tol) > 50          # the test can tell
+        signs = np.sign(G)
+        for got, f, more in ((host(o), 1.0, 0), (host(w), -lr * sc, 3 * U32)):
+            got = (got if m <= n else got.T) / f
+            assert np.all(got[signs == 0] == 0)
+            off = np.abs(got * signs - np.abs(signs) * x[:, None]).max(1) / x
+            assert np.all(off[clear] <= tol[clear] + more), float(np.max(off[clear] / tol[clear]))
 
 
 # ---- the error by spectrum -------------------------------------------------------
