@@ -656,6 +656,14 @@ def _empty(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _wrote(given):
+    """Tells autograd of the caller's tensors that a call has written (None:
+    not given), so that one saved for a backward pass is reported."""
+    given = [t for t in given if t is not None]
+    if given:
+        _torch().autograd.graph.increment_version(given)
+
+
 def _mx_panels(n):
     return -(-n // 256)
 
@@ -691,6 +699,7 @@ def mxfp4_quantize(x, axis=NVFP4_ROWS, codes=None, scales=None, stream=None):
     elements along the blocked axis.
     """
     _need_2d(x, "x")
+    given = codes, scales
     rows, cols = x.shape
     r, c = (rows, cols) if axis == NVFP4_ROWS else (cols, rows)
     codes, scales = _mx_buffers(r, c, codes, scales, x.device, stream)
@@ -699,6 +708,7 @@ def mxfp4_quantize(x, axis=NVFP4_ROWS, codes=None, scales=None, stream=None):
     with _on(x.device):
         _check(_lib.mxfp4_quantize(_ptr(x), _dt(x), rows, cols, axis, _ptr(codes), _ptr(scales),
                                    _stream(stream, x.device)), "mxfp4_quantize")
+    _wrote(given)
     return codes, scales
 
 
@@ -715,6 +725,7 @@ def mxfp4_quantize_both(x, along=None, down=None, stream=None):
     with _on(x.device):
         _check(_lib.mxfp4_quantize_both(_ptr(x), _dt(x), rows, cols, _ptr(rc), _ptr(rs), _ptr(cc),
                                         _ptr(cs), _stream(stream, x.device)), "mxfp4_quantize_both")
+    _wrote((*(along or ()), *(down or ())))
     return (rc, rs), (cc, cs)
 
 
@@ -722,6 +733,7 @@ def mxfp4_dequantize(codes, scales, rows, cols, axis=NVFP4_ROWS, out_dtype=NS_F3
                      stream=None):
     """The values of an MXFP4 tensor, in the original rows x cols orientation."""
     _need_cuda(codes, scales, out)
+    given = out
     if out is None:
         out = _empty((rows, cols), _out_dtype(out_dtype), codes.device, stream)
     r, c = (rows, cols) if axis == NVFP4_ROWS else (cols, rows)
@@ -730,6 +742,7 @@ def mxfp4_dequantize(codes, scales, rows, cols, axis=NVFP4_ROWS, out_dtype=NS_F3
     with _on(codes.device):
         _check(_lib.mxfp4_dequantize(_ptr(codes), _ptr(scales), rows, cols, axis, _ptr(out), _dt(out),
                                      _stream(stream, codes.device)), "mxfp4_dequantize")
+    _wrote((given,))
     return out
 
 
@@ -759,6 +772,7 @@ def mxfp4_gemm(p, q, M, N, K, alpha=1.0, beta=0.0, addend=None, out_dtype=NS_F32
     torch = _torch()
     (pc, ps), (qc, qs) = p, q
     dev = pc.device
+    given = out
     if out is None:
         out = _empty((M, N), _out_dtype(out_dtype), dev, stream)
     if workspace is not None or split:
@@ -773,6 +787,7 @@ def mxfp4_gemm(p, q, M, N, K, alpha=1.0, beta=0.0, addend=None, out_dtype=NS_F32
         _check(_lib.mxfp4_gemm(_ptr(pc), _ptr(ps), _ptr(qc), _ptr(qs), M, N, K, float(alpha),
                                float(beta), _ptr(addend), _ptr(out), _dt(out),
                                *_ws_args(workspace), _stream(stream, dev)), "mxfp4_gemm")
+    _wrote((given,))
     return out
 
 
@@ -794,6 +809,7 @@ def mxfp4_linear(x, w, N, out=None, keep=False, kept=None, workspace=None, strea
     _need_2d(x, "x")
     T, K = x.shape
     dev = x.device
+    given = (out, *(kept or ()))
     if out is None:
         out = _empty((T, N), x.dtype, dev, stream)
     kc, ks = _mx_buffers(K, T, *(kept or (None, None)), dev, stream) if keep or kept else (None, None)
@@ -807,6 +823,7 @@ def mxfp4_linear(x, w, N, out=None, keep=False, kept=None, workspace=None, strea
         _check(_lib.mxfp4_linear(_ptr(x), _dt(x), T, K, _ptr(wc), _ptr(ws_), N, _ptr(out), _dt(out),
                                  _ptr(kc), _ptr(ks), *_ws_args(workspace),
                                  _stream(stream, dev)), "mxfp4_linear")
+    _wrote(given)
     return (out, (kc, ks)) if kc is not None else out
 
 
@@ -821,6 +838,7 @@ def mxfp4_linear_backward(dy, wt, kept, K, dx=None, dw=None, need_dx=True, need_
     _need_2d(dy, "dy")
     T, N = dy.shape
     dev = dy.device
+    given = dx if need_dx else None, dw if need_dw else None
     if need_dx and dx is None:
         dx = _empty((T, K), dy.dtype, dev, stream)
     if need_dw and dw is None:
@@ -843,6 +861,7 @@ def mxfp4_linear_backward(dy, wt, kept, K, dx=None, dw=None, need_dx=True, need_
                                           _dt(dw) if need_dw else NS_F32, float(beta),
                                           *_ws_args(workspace), _stream(stream, dev)),
                "mxfp4_linear_backward")
+    _wrote(given)
     return dx, dw
 
 
@@ -875,6 +894,7 @@ def ns_orthogonalize_f16(G, coeffs, clip=float("inf"), out_dtype=NS_F32, out=Non
     _need_cuda(G, out)
     _need_2d(G, "G")
     m, n = G.shape
+    given = out
     if out is None:
         out = _empty((m, n), _out_dtype(out_dtype), G.device, stream)
     workspace = _mx_workspace(ns_f16_workspace_bytes([(m, n)]), workspace, G.device, stream)
@@ -884,6 +904,7 @@ def ns_orthogonalize_f16(G, coeffs, clip=float("inf"), out_dtype=NS_F32, out=Non
         _check(_lib.ns_orthogonalize_f16(_ptr(G), _dt(G), m, n, carr, k, float(clip), _ptr(out),
                                          _dt(out), *_ws_args(workspace),
                                          _stream(stream, G.device)), "ns_orthogonalize_f16")
+    _wrote((given,))
     return out
 
 
@@ -900,6 +921,7 @@ def ns_orthogonalize_f16_grouped(Gs, coeffs, clips=None, out_dtype=NS_F32, outs=
         _need_2d(g, f"Gs[{i}]")
     shapes = [tuple(g.shape) for g in Gs]
     dev = Gs[0].device
+    given = outs or ()
     if outs is None:
         outs = [_empty(s, _out_dtype(out_dtype), dev, stream) for s in shapes]
     workspace = _mx_workspace(ns_f16_workspace_bytes(shapes), workspace, dev, stream)
@@ -914,6 +936,7 @@ def ns_orthogonalize_f16_grouped(Gs, coeffs, clips=None, out_dtype=NS_F32, outs=
                                                  _pointers(outs), _dt(outs[0]),
                                                  *_ws_args(workspace), _stream(stream, dev)),
                "ns_orthogonalize_f16_grouped")
+    _wrote(given)
     return outs
 
 
@@ -924,7 +947,8 @@ def ns_muon_step(Ws, Ms, Gs, coeffs, lr, momentum=0.95, weight_decay=0.0, nester
     (nesterov) or M; W <- (1 - lr weight_decay) W - lr scale NS(U).
 
     NS runs on f16 operands, whatever the arrays' types, and is off by as much
-    as ns_orthogonalize_f16."""
+    as ns_orthogonalize_f16.  To autograd it is an update in place (without
+    no_grad), so a weight that a pending backward pass has saved is reported."""
     cnt = len(Ws)
     if cnt == 0 or len(Ms) != cnt or len(Gs) != cnt:
         raise ValueError("one momentum and one gradient per weight matrix, at least one")
@@ -951,4 +975,5 @@ def ns_muon_step(Ws, Ms, Gs, coeffs, lr, momentum=0.95, weight_decay=0.0, nester
                                  _pointers(Gs), _dt(Gs[0]), ms, ns_, carr, k, ctypes.byref(opt), sc,
                                  *_ws_args(workspace), _stream(stream, dev)),
                "ns_muon_step")
+    _wrote((*Ws, *Ms))
     return Ws
