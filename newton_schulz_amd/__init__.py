@@ -680,10 +680,18 @@ def _mx_buffers(rows, cols, codes, scales, dev, stream):
 
 
 def _need_mx(codes, scales, name, rows, cols):
+    """The row count is the pitch from panel to panel, so a larger operand's
+    panels would be read in the wrong places: the shape has to be the call's.
+    Other views need its size, flat buffers at least that."""
     torch = _torch()
     p = _mx_panels(cols)
-    _need(codes, f"{name} codes", (torch.uint8,), p * rows * 128)
-    _need(scales, f"{name} scales", (torch.uint8,), p * rows * 8)
+    for t, what, n in ((codes, "codes", 128), (scales, "scales", 8)):
+        what = f"{name} {what}"
+        _need(t, what, (torch.uint8,), p * rows * n)
+        if t is not None and t.dim() == 3:
+            _need_shape(t, what, (p, rows, n))
+        elif t is not None and t.dim() != 1 and t.numel() != p * rows * n:
+            raise ValueError(f"{what}: {t.numel()} elements, {p * rows * n} needed")
 
 
 def _need_2d(t, name):
