@@ -659,9 +659,9 @@ def _empty(shape, dtype, dev, stream):
 def _wrote(given):
     """Tells autograd of the caller's tensors that a call has written (None:
     not given), so that one saved for a backward pass is reported."""
-    given = [t for t in given if t is not None]
-    if given:
-        _torch().autograd.graph.increment_version(given)
+    for t in given:
+        if t is not None:
+            _torch().autograd.graph.increment_version(t)
 
 
 def _mx_panels(n):
@@ -686,11 +686,13 @@ def _need_mx(codes, scales, name, rows, cols):
     torch = _torch()
     p = _mx_panels(cols)
     for t, what, n in ((codes, "codes", 128), (scales, "scales", 8)):
+        if t is None or t.dtype == torch.uint8 and t.shape == (p, rows, n):
+            continue
         what = f"{name} {what}"
         _need(t, what, (torch.uint8,), p * rows * n)
-        if t is not None and t.dim() == 3:
+        if t.dim() == 3:
             _need_shape(t, what, (p, rows, n))
-        elif t is not None and t.dim() != 1 and t.numel() != p * rows * n:
+        elif t.dim() != 1 and t.numel() != p * rows * n:
             raise ValueError(f"{what}: {t.numel()} elements, {p * rows * n} needed")
 
 
