@@ -138,6 +138,8 @@ def _stream(stream, device=None):
     """The stream to enqueue on: `stream`, else the current stream of the
     tensors' device."""
     if stream is not None:
+        if device is not None and getattr(stream, "device", device) != device:
+            raise ValueError(f"a stream of {stream.device} for tensors on {device}")
         return ctypes.c_void_p(stream.cuda_stream)
     torch = _torch()
     if device is None or device.index is None:

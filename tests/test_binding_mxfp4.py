@@ -1,5 +1,8 @@
-"""What the binding asks of MXFP4 operands (CPU only): the row count of a call
-is the pitch of the panels that it reads."""
+"""What the binding asks of MXFP4 operands and of streams (CPU only): the row
+count of a call is the pitch of the panels that it reads, and a stream belongs
+to the tensors' device."""
+import types
+
 import pytest
 import torch
 
@@ -32,3 +35,13 @@ def test_operands_of_another_shape_are_refused(rows, cols):
         ns._need_mx(right[0].transpose(0, 1).contiguous(), right[1], "x", rows, cols)
     with pytest.raises(ValueError):
         ns._need_mx(codes.view(-1, 128), right[1], "x", rows, cols)
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Also where the caller gives every output and the workspace."""
+    dev = torch.device("cuda", 0)
+    here = types.SimpleNamespace(cuda_stream=64, device=dev)
+    assert ns._stream(here, dev).value == 64
+    assert ns._stream(types.SimpleNamespace(cuda_stream=64), dev).value == 64        # any holder of a handle
+    with pytest.raises(ValueError):
+        ns._stream(types.SimpleNamespace(cuda_stream=64, device=torch.device("cuda", 1)), dev)
