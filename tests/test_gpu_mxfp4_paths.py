@@ -88,3 +88,15 @@ def test_operands_of_other_shapes_are_refused():
                  lambda: ns.mxfp4_quantize(x, codes=torch.empty(3, 130, 128, dtype=torch.uint8, device=DEV))):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 100, 700), (300, 333, 1000), (1024, 1024, 256), (4096, 4096, 512)])
+def test_products_of_far_scales_are_exact(M, N, K):
+    """Powers of two on the operands are powers of two on the product, to the
+    bit, subnormal results included (their sums have bits to spare)."""
+    x, y = _x(M, K, 1), _x(N, K, 2)
+    base = ns.mxfp4_gemm(ns.mxfp4_quantize(x), ns.mxfp4_quantize(y), M, N, K).double()
+    for ex, ey in ((100, -100), (-60, -50), (60, 40), (110, -112), (-112, 110), (-90, -40)):
+        p, q = (ns.mxfp4_quantize(torch.ldexp(t, torch.tensor(e, device=DEV))) for t, e in ((x, ex), (y, ey)))
+        want = torch.ldexp(base, torch.tensor(ex + ey, device=DEV)).float()
+        assert torch.equal(ns.mxfp4_gemm(p, q, M, N, K), want), (ex, ey)
