@@ -42,10 +42,11 @@ struct PanelProblem {
   // is put back in FP32: Gram writes d = A_ii - f16(A_ii) to dout; Poly takes
   // it as din -- A^2 is A~^2 + (d_i + d_j) A~_ij to first order -- and writes
   // B_ii / f16(B_ii) to dout (1 where f16 holds B_ii as a subnormal number);
-  // Iter, Out and Step multiply their rows by din
-  // (columns when din_cols), which is B's diagonal put right as long as that
-  // dominates its rows.  Halves the error of five steps where singular values are
-  // of one size (a 92 x 868 gradient: 2.0e-3 -> 1.05e-3).  Arrays of M rounded up to 256 rows; null: none.
+  // Iter, Out and Step multiply their rows by din (columns when din_cols),
+  // which is B's diagonal put right as long as that dominates its rows.  Halves
+  // the error of five steps where singular values are of one size (a 92 x 868
+  // gradient: 2.0e-3 -> 1.05e-3).  Arrays of M rounded up to 256 rows; null:
+  // none.
   const float* din = nullptr;
   float* dout = nullptr;
   bool din_cols = false;
