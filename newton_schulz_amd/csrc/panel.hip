@@ -25,6 +25,7 @@
 // parts whose FP32 partials a second kernel sums in part order.
 #include <cstddef>
 
+#include "dma.hpp"
 #include "mxfp4_device.hpp"
 #include "panel.hpp"
 
@@ -186,38 +187,7 @@ __device__ __forceinline__ void place_of(const Args& a, int t, int& y, int& I, i
   J = __builtin_amdgcn_readfirstlane(j);
 }
 
-// The same value, which the compiler takes as new: what is computed from it
-// once a tile stays there, instead of waiting in registers through the tiles.
-__device__ __forceinline__ int renewed(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-
 // ---- loads -------------------------------------------------------------------
-// Global -> LDS DMA: lane l's bytes land at lds + 16 l (4 l).  Inline asm, so
-// that the compiler does not take the LDS write as pending before every later
-// LDS read; ordered by s_waitcnt vmcnt and the stage's barrier.  There are no
-// register results, and the address operands are read at issue.  The LDS base
-// comes from M0, which has to be written a wait state before (s_nop; the
-// compiler does not look inside the asm).
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
-}
-__device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
-}
-__device__ __forceinline__ void dma4(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory", "m0");
-}
-
-// s_barrier that no memory access moves across (the builtin alone does not
-// keep LDS reads behind it).
-__device__ __forceinline__ void all_waves() { asm volatile("s_barrier" ::: "memory"); }
-
-// Depends on r % 32 alone, so that a fragment's LDS address is one per-lane
-// offset for each step plus a constant for its 32-row block.
-__device__ __forceinline__ int swizzle(int r) { return (r ^ ((r & 31) >> 3)) & 7; }
-
 // Where a workgroup's loads stand: the next panel of the unit being loaded,
 // the wave's operand of it, and the byte offsets of a lane's loads inside a
 // panel.  Rows past the operand's end read its last row: they feed only
@@ -454,12 +424,6 @@ __device__ __forceinline__ void store_n(void* p, int64_t at, int n, const float 
         if (i < n) f[i] = (uint16_t)mx::pack_bf16(v[i], 0.0f);
     }
   }
-}
-
-// Orders a wave's own LDS writes before its reads of other lanes' values.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
 }
 
 // Factors on a tile's values: alpha, and per row or per column where an array
