@@ -520,6 +520,147 @@ ns_status ns_muon_step(int count, void* const* W, ns_dtype wt, void* const* M, n
                        const float* coeffs, int k, const ns_muon_options* opt, const float* scale,
                        void* ws, size_t ws_bytes, void* stream);
 
+/* ======================================================================
+ * Between two 4-bit linear layers: the root-mean-square norm with the
+ * residual's addition and dropout in front, activations in 8 bits, and
+ * products with 4-bit weights.
+ *
+ * MXFP8: a block is 32 consecutive elements along a row, E4M3FN codes and one
+ * E8M0 byte b, value = x_E4M3 * 2^(b - 127); b = 255 makes the block NaN.
+ *   b = max(floor(log2 max|x|) - 8 + 127, 0) (0 for an all-zero block),
+ *   code = RNE_E4M3(x / 2^(b - 127)), ties to the even code, magnitudes beyond
+ *   448 (up to 512 occur) becoming 448;
+ *   a block with a NaN or an infinity: b = 255, codes 0.
+ * Storage as MXFP4's, in panels of 256 elements: codes [panels][rows][256]
+ * bytes, scales [panels][rows][8]; all-zero blocks behind a row's end.
+ *
+ * Dropout: random bits come from Philox4x32-10 with `rng`, a DEVICE array of
+ * two 64-bit words, as seed and offset, read when the call runs (a captured
+ * call draws anew after the words change).  Element (t, c) takes half c % 2 of
+ * word c / 2 % 4 (low half first) of the counter (c / 8, t, offset low, offset
+ * high) under the key (seed low, seed high); it is kept where these 16 bits are
+ * at least P = floor(65536 p + 1/2), and what is kept is multiplied by
+ * 65536 / (65536 - P) (in FP32), so that means are kept exactly.  The mask is
+ * never stored: a backward pass draws the same bits again.  0 <= p < 1 with
+ * P < 65536; p = 0 keeps everything and draws nothing.
+ *
+ * Dimensions are 1 .. 2^24, of any parity, a matrix up to 2^36 elements.
+ * ====================================================================== */
+
+/*
+ * mx_dropout — out = k x / (1 - p), [rows][cols] FP32 or BF16; also its own
+ * gradient (of dy, with the same p and rng).  out may be x itself.
+ */
+ns_status mx_dropout(const void* x, ns_dtype xt, int64_t rows, int64_t cols, double p, const void* rng,
+                     void* out, void* stream);
+
+/*
+ * mx_rms_norm — h = residual + k x / (1 - p);  y = h / sqrt(mean(h^2) + eps) weight
+ * row by row.  h is rounded to its type first and normed as stored; the sum
+ * runs in FP64 and r = 1 / sqrt(..) is rounded to FP32 once, y is the FP32
+ * product (h r) weight, so that codes do not depend on how a row was split.
+ *   x        [T][C] FP32 or BF16 (xt).
+ *   residual [T][C] of type ht, or NULL: none.
+ *   weight   [C] FP32 or BF16 (wt).
+ *   h        out [T][C] FP32 or BF16 (ht), the new residual stream; may be
+ *            residual itself.  NULL without residual and dropout (then h is x,
+ *            and ht has to be xt).
+ *   rstd     out [T] FP32, r of each row for the backward pass; or NULL.
+ *   y        out [T][C] FP32 or BF16 (yt); or NULL.
+ *   codes8, scales8          out, y in MXFP8 (mxfp8_codes_bytes(T, C)); or NULL.
+ *   codes4, scales4          out, y in MXFP4 along the rows; or NULL.
+ *   kept_codes, kept_scales  out, y in MXFP4 along the tokens (NVFP4_COLS), as
+ *            mxfp4_linear_backward takes it for the weights' gradient; or NULL.
+ *            Needs rstd.
+ *   eps      > 0, finite.  drop, rng: as above; rng may be NULL when drop is 0.
+ * C is at most 32768.  At least one output is needed.  A NaN or infinity in h
+ * makes NaN of it (0 of its row's finite values beside an infinity), and of the
+ * blocks that hold one.
+ */
+typedef struct {
+  const void* x;
+  const void* residual;
+  const void* weight;
+  const void* rng;
+  void* h;
+  float* rstd;
+  void* y;
+  uint8_t *codes8, *scales8, *codes4, *scales4, *kept_codes, *kept_scales;
+  int64_t T, C;
+  double eps, drop;
+  ns_dtype xt, ht, wt, yt;
+} mx_norm_args;
+ns_status mx_rms_norm(const mx_norm_args* args, void* stream);
+
+/*
+ * mx_rms_norm_backward — the gradients of mx_rms_norm (a quantizer's derivative
+ * taken as 1), with u = h r as stored by the forward call:
+ *   dh = dh_in + r (weight dy - u mean(weight dy u))
+ *   dx = k dh / (1 - p), of dh before its rounding
+ *   dweight = beta dweight + sum over the rows of dy u
+ *   dy       [T][C] FP32 or BF16 (dyt), the gradient of y.
+ *   h        as written by the forward call (x where that had no h).
+ *   dh_in    [T][C] of ht, what reaches h by other ways (the residual stream);
+ *            or NULL: nothing.
+ *   dh       out [T][C] of ht, the gradient of h and of residual; may be dh_in.
+ *   dx       out [T][C] FP32 or BF16 (xt), the gradient of x; or NULL (without
+ *            dropout it is dh).
+ *   dweight  out [C] FP32; or NULL.  The sum's order is fixed.
+ *   ws       device scratch of mx_rms_norm_backward_workspace_bytes(); not
+ *            needed without dweight.
+ */
+typedef struct {
+  const void* dy;
+  const void* h;
+  const float* rstd;
+  const void* weight;
+  const void* dh_in;
+  const void* rng;
+  void* dh;
+  void* dx;
+  float* dweight;
+  int64_t T, C;
+  double drop;
+  float beta;
+  ns_dtype dyt, ht, wt, xt;
+} mx_norm_backward_args;
+size_t mx_rms_norm_backward_workspace_bytes(int64_t T, int64_t C);
+ns_status mx_rms_norm_backward(const mx_norm_backward_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/* mxfp8_quantize — a rows x cols matrix, FP32 or BF16 (xt), to MXFP8 along its
+ * rows; mxfp8_dequantize — the values, FP32 (exact) or BF16 (exact but for
+ * subnormals; ot). */
+size_t mxfp8_codes_bytes(int64_t rows, int64_t cols);
+size_t mxfp8_scales_bytes(int64_t rows, int64_t cols);
+ns_status mxfp8_quantize(const void* x, ns_dtype xt, int64_t rows, int64_t cols, uint8_t* codes,
+                         uint8_t* scales, void* stream);
+ns_status mxfp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                           void* out, ns_dtype ot, void* stream);
+
+/*
+ * mxfp8_gemm — out = beta * addend + alpha * P Q^T, P [M][K] in MXFP8
+ * (activations) and Q [N][K] in MXFP4 (weights), both along K; arguments as
+ * mxfp4_gemm.  Products are exact and accumulated in FP32.
+ *   ws       device scratch of mxfp8_gemm_workspace_bytes(), or NULL with
+ *            ws_bytes 0 (slower where a long K feeds few outputs).
+ */
+size_t mxfp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+ns_status mxfp8_gemm(const uint8_t* codes_p, const uint8_t* scales_p, const uint8_t* codes_q,
+                     const uint8_t* scales_q, int64_t M, int64_t N, int64_t K, float alpha, float beta,
+                     const float* addend, void* out, ns_dtype ot, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * nvfp4_linear — y = x W^T for T tokens, W [N][K] in NVFP4 along its rows
+ * (codes, scales and global scale as nvfp4_quantize writes them for
+ * NVFP4_ROWS), x [T][K] FP32 or BF16 as it is: the layer of a program that
+ * serves from NVFP4 weights, built for few tokens (the weights are read once
+ * for every 32).  K is a multiple of 16, N of any size.  Products are exact for
+ * BF16 x and within FP32's own rounding otherwise, sums in FP32.
+ */
+ns_status nvfp4_linear(const void* x, ns_dtype xt, int64_t T, int64_t K, const uint8_t* w_codes,
+                       const uint8_t* w_scales, const float* w_global_scale, int64_t N, void* y,
+                       ns_dtype yt, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

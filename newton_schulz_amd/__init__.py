@@ -14,8 +14,11 @@ Functions carry the C names:
     ns_orthogonalize_grouped_on,
     mxfp4_quantize, mxfp4_quantize_both, mxfp4_dequantize, mxfp4_gemm_workspace_bytes, mxfp4_gemm,
     mxfp4_linear, mxfp4_linear_backward,
-    ns_f16_workspace_bytes, ns_orthogonalize_f16, ns_orthogonalize_f16_grouped, ns_muon_step
+    ns_f16_workspace_bytes, ns_orthogonalize_f16, ns_orthogonalize_f16_grouped, ns_muon_step,
+    mx_dropout, mx_rms_norm, mx_rms_norm_backward, mxfp8_quantize, mxfp8_dequantize,
+    mxfp8_gemm_workspace_bytes, mxfp8_gemm, nvfp4_linear
 """
+import collections
 import contextlib
 import ctypes
 import os
@@ -55,6 +58,21 @@ class NsMuonOptions(ctypes.Structure):
     """ns_muon_options of the C ABI."""
     _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float),
                 ("weight_decay", ctypes.c_float), ("nesterov", ctypes.c_int)]
+
+
+class MxNormArgs(ctypes.Structure):
+    """mx_norm_args of the C ABI."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "residual", "weight", "rng", "h", "rstd", "y", "codes8",
+                                                "scales8", "codes4", "scales4", "kept_codes", "kept_scales")]
+                + [("T", ctypes.c_int64), ("C", ctypes.c_int64), ("eps", ctypes.c_double),
+                   ("drop", ctypes.c_double)] + [(n, ctypes.c_int) for n in ("xt", "ht", "wt", "yt")])
+
+
+class MxNormBackwardArgs(ctypes.Structure):
+    """mx_norm_backward_args of the C ABI."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("dy", "h", "rstd", "weight", "dh_in", "rng", "dh", "dx", "dweight")]
+                + [("T", ctypes.c_int64), ("C", ctypes.c_int64), ("drop", ctypes.c_double),
+                   ("beta", ctypes.c_float)] + [(n, ctypes.c_int) for n in ("dyt", "ht", "wt", "xt")])
 
 
 class NsWorkspaceMap(ctypes.Structure):
@@ -109,6 +127,17 @@ _SIGS = {
                                           _vp]),
     "ns_muon_step": (_i, [_i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _sz,
                           _vp]),
+    "mx_dropout": (_i, [_vp, _i, _i64, _i64, _d, _vp, _vp, _vp]),
+    "mx_rms_norm": (_i, [_vp, _vp]),
+    "mx_rms_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "mx_rms_norm_backward": (_i, [_vp, _vp, _sz, _vp]),
+    "mxfp8_codes_bytes": (_sz, [_i64, _i64]),
+    "mxfp8_scales_bytes": (_sz, [_i64, _i64]),
+    "mxfp8_quantize": (_i, [_vp, _i, _i64, _i64, _vp, _vp, _vp]),
+    "mxfp8_dequantize": (_i, [_vp, _vp, _i64, _i64, _vp, _i, _vp]),
+    "mxfp8_gemm_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "mxfp8_gemm": (_i, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _f, _f, _vp, _vp, _i, _vp, _sz, _vp]),
+    "nvfp4_linear": (_i, [_vp, _i, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -989,3 +1018,318 @@ def ns_muon_step(Ws, Ms, Gs, coeffs, lr, momentum=0.95, weight_decay=0.0, nester
                "ns_muon_step")
     _wrote((*Ws, *Ms))
     return Ws
+
+
+# ------------------------------------------- between 4-bit linear layers --
+
+def _need_rng(rng, drop):
+    """Seed and offset: two 64-bit words on the device."""
+    torch = _torch()
+    if rng is None:
+        raise ValueError("dropout needs rng: seed and offset as an int64 device tensor")
+    if rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2:
+        raise ValueError("rng: two 64-bit integers, seed and offset")
+
+
+def _blocks_buffers(given, rows, cols, width, dev, stream):
+    """(codes, scales) of an operand: the caller's pair, new ones (True), or none."""
+    if given is None or given is False:
+        return None
+    if given is not True:
+        return given
+    torch, p = _torch(), _mx_panels(cols)
+    return (_empty((p, rows, width), torch.uint8, dev, stream), _empty((p, rows, 8), torch.uint8, dev, stream))
+
+
+def _need_blocks(pair, name, rows, cols, width):
+    """As _need_mx, for codes of `width` bytes a panel's row."""
+    torch, p = _torch(), _mx_panels(cols)
+    for t, what, n in ((pair[0], "codes", width), (pair[1], "scales", 8)):
+        if t.dtype == torch.uint8 and t.shape == (p, rows, n):
+            continue
+        what = f"{name} {what}"
+        _need(t, what, (torch.uint8,), p * rows * n)
+        if t.dim() == 3:
+            _need_shape(t, what, (p, rows, n))
+        elif t.dim() != 1 and t.numel() != p * rows * n:
+            raise ValueError(f"{what}: {t.numel()} elements, {p * rows * n} needed")
+
+
+def _given(*wanted):
+    """The caller's own tensors among wanted outputs (True, None and False are none)."""
+    for w in wanted:
+        if isinstance(w, (tuple, list)):
+            yield from w
+        elif w is not None and not isinstance(w, bool):
+            yield w
+
+
+def mx_dropout(x, drop, rng, out=None, stream=None):
+    """k x / (1 - drop) for a float32/bfloat16 matrix, k drawn from the seed and
+    offset in `rng` (two 64-bit integers on the device); of a gradient, with the
+    same drop and rng, its own backward pass.  `out` may be x."""
+    _need_2d(x, "x")
+    rows, cols = x.shape
+    given = out
+    if out is None:
+        out = _empty((rows, cols), x.dtype, x.device, stream)
+    _need_rng(rng, drop)
+    _need_cuda(x, rng, out)
+    _need_shape(out, "out", (rows, cols))
+    _need(out, "out", (x.dtype,), rows * cols)
+    with _on(x.device):
+        _check(_lib.mx_dropout(x.data_ptr(), _dt(x), rows, cols, float(drop), rng.data_ptr(), out.data_ptr(),
+                               _stream(stream, x.device)), "mx_dropout")
+    _wrote((given,))
+    return out
+
+
+NormOut = collections.namedtuple("NormOut", "h rstd y mxfp8 mxfp4 kept")
+NormOut.__doc__ = """What mx_rms_norm returns: the residual stream, the rows' 1 / rms, and y in the
+wanted forms (None for the others); operands are (codes, scales)."""
+NormGrads = collections.namedtuple("NormGrads", "dh dx dw")
+
+
+def mx_rms_norm(x, weight, eps=1e-6, residual=None, drop=0.0, rng=None, y=None, mxfp8=None, mxfp4=None,
+                kept=None, rstd=None, h=None, stream=None):
+    """h = residual + dropout(x) and y = h / sqrt(mean(h^2) + eps) * weight, row by row.
+
+    x [T][C] and residual (or None) are float32/bfloat16, weight [C] too; h has
+    the residual's type (x's without one; it is x itself without residual and
+    dropout) and may be given, also as the residual itself.  y (x's type unless
+    given), mxfp8 (operand of mxfp8_gemm), mxfp4 (operand of mxfp4_gemm), kept
+    (MXFP4 along the tokens, for mxfp4_linear_backward) and rstd (for
+    mx_rms_norm_backward) are outputs: True for a new one, or the caller's
+    tensor or (codes, scales); y where none of the four is asked for."""
+    torch = _torch()
+    _need_2d(x, "x")
+    T, C = x.shape
+    dev = x.device
+    written = list(_given(h, y, mxfp8, mxfp4, kept, rstd))
+    if y is None and not (mxfp8 or mxfp4 or kept):
+        y = True
+    if residual is not None or drop:
+        if h is None:
+            h = _empty((T, C), x.dtype if residual is None else residual.dtype, dev, stream)
+    elif h is not None:
+        raise ValueError("h is x itself without residual and dropout")
+    if y is True:
+        y = _empty((T, C), x.dtype, dev, stream)
+    elif y is False:
+        y = None
+    if rstd is True or kept and (rstd is None or rstd is False):
+        rstd = _empty((T,), torch.float32, dev, stream)
+    elif rstd is False:
+        rstd = None
+    p8 = _blocks_buffers(mxfp8, T, C, 256, dev, stream)
+    p4 = _blocks_buffers(mxfp4, T, C, 128, dev, stream)
+    pk = _blocks_buffers(kept, C, T, 128, dev, stream)
+    _need_cuda(x, weight, residual, rng, h, y, rstd, *(p8 or ()), *(p4 or ()), *(pk or ()))
+    _need_shape(weight, "weight", (C,))
+    _need_shape(residual, "residual", (T, C))
+    _need_shape(h, "h", (T, C))
+    _need_shape(y, "y", (T, C))
+    if rstd is not None:
+        _need_shape(rstd, "rstd", (T,))
+        _need(rstd, "rstd", (torch.float32,), T)
+    if residual is not None and h.dtype != residual.dtype:
+        raise TypeError("h has the residual's dtype")
+    if p8:
+        _need_blocks(p8, "mxfp8", T, C, 256)
+    if p4:
+        _need_blocks(p4, "mxfp4", T, C, 128)
+    if pk:
+        _need_blocks(pk, "kept", C, T, 128)
+    if drop:
+        _need_rng(rng, drop)
+    a = MxNormArgs()
+    a.x, a.weight, a.T, a.C, a.eps, a.drop = x.data_ptr(), weight.data_ptr(), T, C, eps, drop
+    a.xt, a.wt = _dt(x), _dt(weight)
+    if residual is not None:
+        a.residual = residual.data_ptr()
+    if drop:
+        a.rng = rng.data_ptr()
+    if h is not None:
+        a.h, a.ht = h.data_ptr(), _dt(h)
+    else:
+        a.ht = a.xt
+    if rstd is not None:
+        a.rstd = rstd.data_ptr()
+    if y is not None:
+        a.y, a.yt = y.data_ptr(), _dt(y)
+    if p8:
+        a.codes8, a.scales8 = p8[0].data_ptr(), p8[1].data_ptr()
+    if p4:
+        a.codes4, a.scales4 = p4[0].data_ptr(), p4[1].data_ptr()
+    if pk:
+        a.kept_codes, a.kept_scales = pk[0].data_ptr(), pk[1].data_ptr()
+    with _on(dev):
+        _check(_lib.mx_rms_norm(ctypes.byref(a), _stream(stream, dev)), "mx_rms_norm")
+    if written:
+        _wrote(written)
+    return NormOut(x if h is None else h, rstd, y, p8, p4, pk)
+
+
+def mx_rms_norm_backward_workspace_bytes(T, C):
+    return int(_lib.mx_rms_norm_backward_workspace_bytes(T, C))
+
+
+def mx_rms_norm_backward(dy, h, rstd, weight, dh=None, drop=0.0, rng=None, out=None, dx=None, dw=None,
+                         need_dw=True, beta=0.0, x_dtype=None, workspace=None, stream=None):
+    """Gradients of mx_rms_norm for dy [T][C], the gradient of y: (dh, dx, dw).
+
+    h and rstd are the forward call's, dh what reaches h by other ways (the
+    residual stream's gradient, or None); `out` takes the sum (may be dh
+    itself).  dx is the gradient of x, through the same dropout, in x_dtype
+    (dy's unless given); where it equals the gradient of h (no dropout, one
+    type) it is that tensor.  dw = beta * dw + gradient is float32."""
+    torch = _torch()
+    _need_2d(dy, "dy")
+    T, C = dy.shape
+    dev = dy.device
+    written = [t for t in (out, dx, dw) if t is not None]
+    if out is None:
+        out = _empty((T, C), h.dtype, dev, stream)
+    if x_dtype is None:
+        x_dtype = dy.dtype if dx is None else dx.dtype
+    if dx is None and (drop or x_dtype != h.dtype):
+        dx = _empty((T, C), x_dtype, dev, stream)
+    if not need_dw:
+        dw = None
+    elif dw is None:
+        if float(beta) != 0.0:
+            raise ValueError("beta != 0 adds to a dw that is given")
+        dw = _empty((C,), torch.float32, dev, stream)
+    if dw is not None:
+        workspace = _mx_workspace(mx_rms_norm_backward_workspace_bytes(T, C), workspace, dev, stream)
+    _need_cuda(dy, h, rstd, weight, dh, rng, out, dx, dw, workspace)
+    _need_shape(h, "h", (T, C))
+    _need_shape(rstd, "rstd", (T,))
+    _need(rstd, "rstd", (torch.float32,), T)
+    _need_shape(weight, "weight", (C,))
+    for t, name in ((dh, "dh"), (out, "out")):
+        _need_shape(t, name, (T, C))
+        if t is not None and t.dtype != h.dtype:
+            raise TypeError(f"{name} has h's dtype")
+    _need_shape(dx, "dx", (T, C))
+    if dx is not None and dx.dtype != x_dtype:
+        raise TypeError("dx has x_dtype")
+    if dw is not None:
+        _need_shape(dw, "dw", (C,))
+        _need(dw, "dw", (torch.float32,), C)
+    if drop:
+        _need_rng(rng, drop)
+    a = MxNormBackwardArgs()
+    a.dy, a.h, a.rstd, a.weight, a.dh = (t.data_ptr() for t in (dy, h, rstd, weight, out))
+    a.T, a.C, a.drop, a.beta = T, C, drop, beta
+    a.dyt, a.ht, a.wt = _dt(dy), _dt(h), _dt(weight)
+    if dh is not None:
+        a.dh_in = dh.data_ptr()
+    if drop:
+        a.rng = rng.data_ptr()
+    if dx is not None:
+        a.dx, a.xt = dx.data_ptr(), _dt(dx)
+    if dw is not None:
+        a.dweight = dw.data_ptr()
+    with _on(dev):
+        _check(_lib.mx_rms_norm_backward(ctypes.byref(a), *_ws_args(workspace), _stream(stream, dev)),
+               "mx_rms_norm_backward")
+    if written:
+        _wrote(written)
+    return NormGrads(out, out if dx is None else dx, dw)
+
+
+def mxfp8_quantize(x, codes=None, scales=None, stream=None):
+    """MXFP8 quantization of a 2-D float32/bfloat16 device tensor along its rows:
+    (codes uint8 [panels][rows][256], scales uint8 [panels][rows][8])."""
+    torch = _torch()
+    _need_2d(x, "x")
+    rows, cols = x.shape
+    given, p = (codes, scales), _mx_panels(cols)
+    if codes is None:
+        codes = _empty((p, rows, 256), torch.uint8, x.device, stream)
+    if scales is None:
+        scales = _empty((p, rows, 8), torch.uint8, x.device, stream)
+    _need_cuda(x, codes, scales)
+    _need_blocks((codes, scales), "out", rows, cols, 256)
+    with _on(x.device):
+        _check(_lib.mxfp8_quantize(_ptr(x), _dt(x), rows, cols, _ptr(codes), _ptr(scales),
+                                   _stream(stream, x.device)), "mxfp8_quantize")
+    _wrote(given)
+    return codes, scales
+
+
+def mxfp8_dequantize(codes, scales, rows, cols, out_dtype=NS_F32, out=None, stream=None):
+    """The values of an MXFP8 tensor, rows x cols."""
+    given = out
+    if out is None:
+        out = _empty((rows, cols), _out_dtype(out_dtype), codes.device, stream)
+    _need_cuda(codes, scales, out)
+    _need_blocks((codes, scales), "in", rows, cols, 256)
+    _need(out, "out", _floats(), rows * cols)
+    with _on(codes.device):
+        _check(_lib.mxfp8_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(out), _dt(out),
+                                     _stream(stream, codes.device)), "mxfp8_dequantize")
+    _wrote((given,))
+    return out
+
+
+def mxfp8_gemm_workspace_bytes(M, N, K):
+    return int(_lib.mxfp8_gemm_workspace_bytes(M, N, K))
+
+
+def mxfp8_gemm(p, q, M, N, K, alpha=1.0, beta=0.0, addend=None, out_dtype=NS_F32, out=None, workspace=None,
+               split=True, stream=None):
+    """out = beta*addend + alpha*(P Q^T) for p = (codes, scales) in MXFP8 and q in
+    MXFP4, both along K: 8-bit activations by 4-bit weights.
+
+    With split=True (default) a workspace of mxfp8_gemm_workspace_bytes() is
+    allocated when none is given."""
+    torch = _torch()
+    (pc, ps), (qc, qs) = p, q
+    dev = pc.device
+    given = out
+    if out is None:
+        out = _empty((M, N), _out_dtype(out_dtype), dev, stream)
+    if workspace is not None or split:
+        workspace = _mx_workspace(_lib.mxfp8_gemm_workspace_bytes(M, N, K), workspace, dev, stream)
+    _need_cuda(pc, ps, qc, qs, addend, out, workspace)
+    _need_blocks(p, "p", M, K, 256)
+    _need_mx(qc, qs, "q", N, K)
+    _need(out, "out", _floats(), M * N)
+    if float(beta) != 0.0:
+        _need(addend, "addend", (torch.float32,), M * N)
+    with _on(dev):
+        _check(_lib.mxfp8_gemm(_ptr(pc), _ptr(ps), _ptr(qc), _ptr(qs), M, N, K, float(alpha), float(beta),
+                               _ptr(addend), _ptr(out), _dt(out), *_ws_args(workspace), _stream(stream, dev)),
+               "mxfp8_gemm")
+    if given is not None:
+        _wrote((given,))
+    return out
+
+
+def nvfp4_linear(x, w, N, out=None, stream=None):
+    """y = x W^T for x [T][K] (float32/bfloat16, not quantized) and NVFP4 weights
+    w = (codes, scales, global_scale) of [N][K] as nvfp4_quantize returns them;
+    y takes x's dtype unless `out` is given.  Built for few tokens."""
+    torch = _torch()
+    codes, scales, sg = w
+    _need_2d(x, "x")
+    T, K = x.shape
+    dev = x.device
+    given = out
+    if out is None:
+        out = _empty((T, N), x.dtype, dev, stream)
+    _need_cuda(x, codes, scales, sg, out)
+    if codes.numel() != N * K // 2 or scales.numel() != N * K // 16:
+        raise ValueError(f"w: codes and scales of {N} x {K} needed")
+    _need(codes, "codes", (torch.uint8,), 0)
+    _need(scales, "scales", (torch.uint8,), 0)
+    _need(sg, "global_scale", (torch.float32,), 1)
+    _need(out, "out", _floats(), T * N)
+    with _on(dev):
+        _check(_lib.nvfp4_linear(_ptr(x), _dt(x), T, K, _ptr(codes), _ptr(scales), _ptr(sg), N, _ptr(out), _dt(out),
+                                 _stream(stream, dev)), "nvfp4_linear")
+    if given is not None:
+        _wrote((given,))
+    return out
