@@ -1021,29 +1021,68 @@ def ns_muon_step(Ws, Ms, Gs, coeffs, lr, momentum=0.95, weight_decay=0.0, nester
 
 
 # ------------------------------------------- between 4-bit linear layers --
+# Calls of a few microseconds on the GPU: a tensor made here is not checked
+# again, and a stream or device object is not made where a number serves.
 
-def _need_rng(rng, drop):
+def _launch(fn, name, dev, stream, *args):
+    """fn(*args, stream) with the tensors' device the current one."""
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif getattr(stream, "device", dev) != dev:
+        raise ValueError(f"a stream of {stream.device} for tensors on {dev}")
+    else:
+        s = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev.index:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, s)
+    if status != NS_OK:
+        raise NSError(status, name)
+
+
+def _need_on(dev, *ts):
+    """Contiguous tensors (or None) of one device, a GPU."""
+    if dev.type != "cuda":
+        raise ValueError("tensors must be contiguous device tensors")
+    for t in ts:
+        if t is not None:
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous device tensors")
+            if t.device != dev:
+                raise ValueError("tensors must be on one device")
+
+
+_TYPES = {torch.float32: NS_F32, torch.bfloat16: NS_BF16}
+
+
+def _type_of(t):
+    d = _TYPES.get(t.dtype)
+    if d is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return d
+
+
+def _need_rng(rng, dev):
     """Seed and offset: two 64-bit words on the device."""
-    torch = _torch()
     if rng is None:
         raise ValueError("dropout needs rng: seed and offset as an int64 device tensor")
     if rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2:
         raise ValueError("rng: two 64-bit integers, seed and offset")
+    _need_on(dev, rng)
 
 
-def _blocks_buffers(given, rows, cols, width, dev, stream):
-    """(codes, scales) of an operand: the caller's pair, new ones (True), or none."""
-    if given is None or given is False:
-        return None
-    if given is not True:
-        return given
-    torch, p = _torch(), _mx_panels(cols)
-    return (_empty((p, rows, width), torch.uint8, dev, stream), _empty((p, rows, 8), torch.uint8, dev, stream))
+def _need_like(t, name, shape, dtypes):
+    """A caller's tensor of a shape and one of some types."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
 
 
 def _need_blocks(pair, name, rows, cols, width):
     """As _need_mx, for codes of `width` bytes a panel's row."""
-    torch, p = _torch(), _mx_panels(cols)
+    p = _mx_panels(cols)
     for t, what, n in ((pair[0], "codes", width), (pair[1], "scales", 8)):
         if t.dtype == torch.uint8 and t.shape == (p, rows, n):
             continue
@@ -1055,13 +1094,18 @@ def _need_blocks(pair, name, rows, cols, width):
             raise ValueError(f"{what}: {t.numel()} elements, {p * rows * n} needed")
 
 
-def _given(*wanted):
-    """The caller's own tensors among wanted outputs (True, None and False are none)."""
-    for w in wanted:
-        if isinstance(w, (tuple, list)):
-            yield from w
-        elif w is not None and not isinstance(w, bool):
-            yield w
+def _blocks(wanted, name, rows, cols, width, dev, stream, written):
+    """(codes, scales) of an output operand: new ones (True), the caller's pair,
+    noted in `written`, or None."""
+    if wanted is None or wanted is False:
+        return None
+    if wanted is True:
+        p = _mx_panels(cols)
+        return (_empty((p, rows, width), torch.uint8, dev, stream), _empty((p, rows, 8), torch.uint8, dev, stream))
+    _need_on(dev, *wanted)
+    _need_blocks(wanted, name, rows, cols, width)
+    written += wanted
+    return wanted
 
 
 def mx_dropout(x, drop, rng, out=None, stream=None):
@@ -1070,17 +1114,19 @@ def mx_dropout(x, drop, rng, out=None, stream=None):
     same drop and rng, its own backward pass.  `out` may be x."""
     _need_2d(x, "x")
     rows, cols = x.shape
+    dev, t = x.device, _type_of(x)
+    _need_on(dev, x)
+    _need_rng(rng, dev)
     given = out
     if out is None:
-        out = _empty((rows, cols), x.dtype, x.device, stream)
-    _need_rng(rng, drop)
-    _need_cuda(x, rng, out)
-    _need_shape(out, "out", (rows, cols))
-    _need(out, "out", (x.dtype,), rows * cols)
-    with _on(x.device):
-        _check(_lib.mx_dropout(x.data_ptr(), _dt(x), rows, cols, float(drop), rng.data_ptr(), out.data_ptr(),
-                               _stream(stream, x.device)), "mx_dropout")
-    _wrote((given,))
+        out = _empty((rows, cols), x.dtype, dev, stream)
+    else:
+        _need_on(dev, out)
+        _need_like(out, "out", x.shape, (x.dtype,))
+    _launch(_lib.mx_dropout, "mx_dropout", dev, stream, x.data_ptr(), t, rows, cols, drop, rng.data_ptr(),
+            out.data_ptr())
+    if given is not None:
+        _wrote((given,))
     return out
 
 
@@ -1101,70 +1147,65 @@ def mx_rms_norm(x, weight, eps=1e-6, residual=None, drop=0.0, rng=None, y=None, 
     (MXFP4 along the tokens, for mxfp4_linear_backward) and rstd (for
     mx_rms_norm_backward) are outputs: True for a new one, or the caller's
     tensor or (codes, scales); y where none of the four is asked for."""
-    torch = _torch()
     _need_2d(x, "x")
-    T, C = x.shape
+    T, C = shape = x.shape
     dev = x.device
-    written = list(_given(h, y, mxfp8, mxfp4, kept, rstd))
-    if y is None and not (mxfp8 or mxfp4 or kept):
-        y = True
-    if residual is not None or drop:
-        if h is None:
-            h = _empty((T, C), x.dtype if residual is None else residual.dtype, dev, stream)
-    elif h is not None:
-        raise ValueError("h is x itself without residual and dropout")
-    if y is True:
-        y = _empty((T, C), x.dtype, dev, stream)
-    elif y is False:
-        y = None
-    if rstd is True or kept and (rstd is None or rstd is False):
-        rstd = _empty((T,), torch.float32, dev, stream)
-    elif rstd is False:
-        rstd = None
-    p8 = _blocks_buffers(mxfp8, T, C, 256, dev, stream)
-    p4 = _blocks_buffers(mxfp4, T, C, 128, dev, stream)
-    pk = _blocks_buffers(kept, C, T, 128, dev, stream)
-    _need_cuda(x, weight, residual, rng, h, y, rstd, *(p8 or ()), *(p4 or ()), *(pk or ()))
-    _need_shape(weight, "weight", (C,))
-    _need_shape(residual, "residual", (T, C))
-    _need_shape(h, "h", (T, C))
-    _need_shape(y, "y", (T, C))
-    if rstd is not None:
-        _need_shape(rstd, "rstd", (T,))
-        _need(rstd, "rstd", (torch.float32,), T)
-    if residual is not None and h.dtype != residual.dtype:
-        raise TypeError("h has the residual's dtype")
-    if p8:
-        _need_blocks(p8, "mxfp8", T, C, 256)
-    if p4:
-        _need_blocks(p4, "mxfp4", T, C, 128)
-    if pk:
-        _need_blocks(pk, "kept", C, T, 128)
-    if drop:
-        _need_rng(rng, drop)
+    _need_on(dev, x, weight)
+    if weight.shape != (C,):
+        raise ValueError(f"weight: shape {tuple(weight.shape)}, expected {(C,)}")
     a = MxNormArgs()
     a.x, a.weight, a.T, a.C, a.eps, a.drop = x.data_ptr(), weight.data_ptr(), T, C, eps, drop
-    a.xt, a.wt = _dt(x), _dt(weight)
+    a.xt = a.ht = _type_of(x)
+    a.wt = _type_of(weight)
+    written = []
     if residual is not None:
+        _need_on(dev, residual)
+        _need_like(residual, "residual", shape, _floats())
         a.residual = residual.data_ptr()
     if drop:
+        _need_rng(rng, dev)
         a.rng = rng.data_ptr()
-    if h is not None:
-        a.h, a.ht = h.data_ptr(), _dt(h)
+    if residual is not None or drop:
+        kind = x.dtype if residual is None else residual.dtype
+        if h is None:
+            h = _empty(shape, kind, dev, stream)
+        else:
+            _need_on(dev, h)
+            _need_like(h, "h", shape, (kind,))
+            written.append(h)
+        a.h, a.ht = h.data_ptr(), _TYPES[kind]
+    elif h is not None:
+        raise ValueError("h is x itself without residual and dropout")
+    p8 = _blocks(mxfp8, "mxfp8", T, C, 256, dev, stream, written)
+    p4 = _blocks(mxfp4, "mxfp4", T, C, 128, dev, stream, written)
+    pk = _blocks(kept, "kept", C, T, 128, dev, stream, written)
+    if p8 is not None:
+        a.codes8, a.scales8 = p8[0].data_ptr(), p8[1].data_ptr()
+    if p4 is not None:
+        a.codes4, a.scales4 = p4[0].data_ptr(), p4[1].data_ptr()
+    if pk is not None:
+        a.kept_codes, a.kept_scales = pk[0].data_ptr(), pk[1].data_ptr()
+    if y is None and p8 is None and p4 is None and pk is None or y is True:
+        y = _empty(shape, x.dtype, dev, stream)
+    elif y is False:
+        y = None
+    elif y is not None:
+        _need_on(dev, y)
+        _need_like(y, "y", shape, _floats())
+        written.append(y)
+    if y is not None:
+        a.y, a.yt = y.data_ptr(), _TYPES[y.dtype]
+    if rstd is None or rstd is False:
+        rstd = None if pk is None else _empty((T,), torch.float32, dev, stream)
+    elif rstd is True:
+        rstd = _empty((T,), torch.float32, dev, stream)
     else:
-        a.ht = a.xt
+        _need_on(dev, rstd)
+        _need_like(rstd, "rstd", (T,), (torch.float32,))
+        written.append(rstd)
     if rstd is not None:
         a.rstd = rstd.data_ptr()
-    if y is not None:
-        a.y, a.yt = y.data_ptr(), _dt(y)
-    if p8:
-        a.codes8, a.scales8 = p8[0].data_ptr(), p8[1].data_ptr()
-    if p4:
-        a.codes4, a.scales4 = p4[0].data_ptr(), p4[1].data_ptr()
-    if pk:
-        a.kept_codes, a.kept_scales = pk[0].data_ptr(), pk[1].data_ptr()
-    with _on(dev):
-        _check(_lib.mx_rms_norm(ctypes.byref(a), _stream(stream, dev)), "mx_rms_norm")
+    _launch(_lib.mx_rms_norm, "mx_rms_norm", dev, stream, ctypes.byref(a))
     if written:
         _wrote(written)
     return NormOut(x if h is None else h, rstd, y, p8, p4, pk)
@@ -1183,57 +1224,60 @@ def mx_rms_norm_backward(dy, h, rstd, weight, dh=None, drop=0.0, rng=None, out=N
     itself).  dx is the gradient of x, through the same dropout, in x_dtype
     (dy's unless given); where it equals the gradient of h (no dropout, one
     type) it is that tensor.  dw = beta * dw + gradient is float32."""
-    torch = _torch()
     _need_2d(dy, "dy")
-    T, C = dy.shape
+    T, C = shape = dy.shape
     dev = dy.device
-    written = [t for t in (out, dx, dw) if t is not None]
-    if out is None:
-        out = _empty((T, C), h.dtype, dev, stream)
-    if x_dtype is None:
-        x_dtype = dy.dtype if dx is None else dx.dtype
-    if dx is None and (drop or x_dtype != h.dtype):
-        dx = _empty((T, C), x_dtype, dev, stream)
-    if not need_dw:
-        dw = None
-    elif dw is None:
-        if float(beta) != 0.0:
-            raise ValueError("beta != 0 adds to a dw that is given")
-        dw = _empty((C,), torch.float32, dev, stream)
-    if dw is not None:
-        workspace = _mx_workspace(mx_rms_norm_backward_workspace_bytes(T, C), workspace, dev, stream)
-    _need_cuda(dy, h, rstd, weight, dh, rng, out, dx, dw, workspace)
-    _need_shape(h, "h", (T, C))
-    _need_shape(rstd, "rstd", (T,))
-    _need(rstd, "rstd", (torch.float32,), T)
-    _need_shape(weight, "weight", (C,))
-    for t, name in ((dh, "dh"), (out, "out")):
-        _need_shape(t, name, (T, C))
-        if t is not None and t.dtype != h.dtype:
-            raise TypeError(f"{name} has h's dtype")
-    _need_shape(dx, "dx", (T, C))
-    if dx is not None and dx.dtype != x_dtype:
-        raise TypeError("dx has x_dtype")
-    if dw is not None:
-        _need_shape(dw, "dw", (C,))
-        _need(dw, "dw", (torch.float32,), C)
-    if drop:
-        _need_rng(rng, drop)
+    if dw is None and need_dw and float(beta) != 0.0:
+        raise ValueError("beta != 0 adds to a dw that is given")
+    _need_on(dev, dy, h, rstd, weight)
+    _need_like(h, "h", shape, _floats())
+    _need_like(rstd, "rstd", (T,), (torch.float32,))
+    _need_like(weight, "weight", (C,), _floats())
     a = MxNormBackwardArgs()
-    a.dy, a.h, a.rstd, a.weight, a.dh = (t.data_ptr() for t in (dy, h, rstd, weight, out))
     a.T, a.C, a.drop, a.beta = T, C, drop, beta
-    a.dyt, a.ht, a.wt = _dt(dy), _dt(h), _dt(weight)
+    a.dy, a.h, a.rstd, a.weight = dy.data_ptr(), h.data_ptr(), rstd.data_ptr(), weight.data_ptr()
+    a.dyt, a.ht, a.wt = _type_of(dy), _TYPES[h.dtype], _TYPES[weight.dtype]
+    written = []
     if dh is not None:
+        _need_on(dev, dh)
+        _need_like(dh, "dh", shape, (h.dtype,))
         a.dh_in = dh.data_ptr()
     if drop:
+        _need_rng(rng, dev)
         a.rng = rng.data_ptr()
+    if out is None:
+        out = _empty(shape, h.dtype, dev, stream)
+    else:
+        _need_on(dev, out)
+        _need_like(out, "out", shape, (h.dtype,))
+        written.append(out)
+    a.dh = out.data_ptr()
+    if x_dtype is None:
+        x_dtype = dy.dtype if dx is None else dx.dtype
     if dx is not None:
-        a.dx, a.xt = dx.data_ptr(), _dt(dx)
-    if dw is not None:
+        _need_on(dev, dx)
+        _need_like(dx, "dx", shape, (x_dtype,))
+        written.append(dx)
+    elif drop or x_dtype != h.dtype:
+        dx = _empty(shape, x_dtype, dev, stream)
+    if dx is not None:
+        a.dx, a.xt = dx.data_ptr(), _type_of(dx)
+    ws = (None, 0)
+    if not need_dw:
+        dw = None
+    else:
+        if dw is None:
+            dw = _empty((C,), torch.float32, dev, stream)
+        else:
+            _need_on(dev, dw)
+            _need_like(dw, "dw", (C,), (torch.float32,))
+            written.append(dw)
         a.dweight = dw.data_ptr()
-    with _on(dev):
-        _check(_lib.mx_rms_norm_backward(ctypes.byref(a), *_ws_args(workspace), _stream(stream, dev)),
-               "mx_rms_norm_backward")
+        workspace = _mx_workspace(_lib.mx_rms_norm_backward_workspace_bytes(T, C), workspace, dev, stream)
+        if workspace is not None:
+            _need_on(dev, workspace)
+            ws = workspace.data_ptr(), workspace.numel()
+    _launch(_lib.mx_rms_norm_backward, "mx_rms_norm_backward", dev, stream, ctypes.byref(a), *ws)
     if written:
         _wrote(written)
     return NormGrads(out, out if dx is None else dx, dw)
@@ -1242,35 +1286,37 @@ def mx_rms_norm_backward(dy, h, rstd, weight, dh=None, drop=0.0, rng=None, out=N
 def mxfp8_quantize(x, codes=None, scales=None, stream=None):
     """MXFP8 quantization of a 2-D float32/bfloat16 device tensor along its rows:
     (codes uint8 [panels][rows][256], scales uint8 [panels][rows][8])."""
-    torch = _torch()
     _need_2d(x, "x")
     rows, cols = x.shape
-    given, p = (codes, scales), _mx_panels(cols)
+    dev, t = x.device, _type_of(x)
+    p = _mx_panels(cols)
+    given = codes, scales
     if codes is None:
-        codes = _empty((p, rows, 256), torch.uint8, x.device, stream)
+        codes = _empty((p, rows, 256), torch.uint8, dev, stream)
     if scales is None:
-        scales = _empty((p, rows, 8), torch.uint8, x.device, stream)
-    _need_cuda(x, codes, scales)
+        scales = _empty((p, rows, 8), torch.uint8, dev, stream)
+    _need_on(dev, x, codes, scales)
     _need_blocks((codes, scales), "out", rows, cols, 256)
-    with _on(x.device):
-        _check(_lib.mxfp8_quantize(_ptr(x), _dt(x), rows, cols, _ptr(codes), _ptr(scales),
-                                   _stream(stream, x.device)), "mxfp8_quantize")
+    _launch(_lib.mxfp8_quantize, "mxfp8_quantize", dev, stream, x.data_ptr(), t, rows, cols, codes.data_ptr(),
+            scales.data_ptr())
     _wrote(given)
     return codes, scales
 
 
 def mxfp8_dequantize(codes, scales, rows, cols, out_dtype=NS_F32, out=None, stream=None):
     """The values of an MXFP8 tensor, rows x cols."""
+    dev = codes.device
+    _need_on(dev, codes, scales, out)
+    _need_blocks((codes, scales), "in", rows, cols, 256)
     given = out
     if out is None:
-        out = _empty((rows, cols), _out_dtype(out_dtype), codes.device, stream)
-    _need_cuda(codes, scales, out)
-    _need_blocks((codes, scales), "in", rows, cols, 256)
-    _need(out, "out", _floats(), rows * cols)
-    with _on(codes.device):
-        _check(_lib.mxfp8_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(out), _dt(out),
-                                     _stream(stream, codes.device)), "mxfp8_dequantize")
-    _wrote((given,))
+        out = _empty((rows, cols), _out_dtype(out_dtype), dev, stream)
+    else:
+        _need(out, "out", _floats(), rows * cols)
+    _launch(_lib.mxfp8_dequantize, "mxfp8_dequantize", dev, stream, codes.data_ptr(), scales.data_ptr(), rows, cols,
+            out.data_ptr(), _TYPES[out.dtype])
+    if given is not None:
+        _wrote((given,))
     return out
 
 
@@ -1285,24 +1331,27 @@ def mxfp8_gemm(p, q, M, N, K, alpha=1.0, beta=0.0, addend=None, out_dtype=NS_F32
 
     With split=True (default) a workspace of mxfp8_gemm_workspace_bytes() is
     allocated when none is given."""
-    torch = _torch()
     (pc, ps), (qc, qs) = p, q
     dev = pc.device
+    _need_on(dev, pc, ps, qc, qs, addend, out, workspace)
+    _need_blocks(p, "p", M, K, 256)
+    _need_mx(qc, qs, "q", N, K)
     given = out
     if out is None:
         out = _empty((M, N), _out_dtype(out_dtype), dev, stream)
+    else:
+        _need(out, "out", _floats(), M * N)
+    add = None
+    if beta:
+        _need(addend, "addend", (torch.float32,), M * N)
+        add = None if addend is None else addend.data_ptr()
+    ws = (None, 0)
     if workspace is not None or split:
         workspace = _mx_workspace(_lib.mxfp8_gemm_workspace_bytes(M, N, K), workspace, dev, stream)
-    _need_cuda(pc, ps, qc, qs, addend, out, workspace)
-    _need_blocks(p, "p", M, K, 256)
-    _need_mx(qc, qs, "q", N, K)
-    _need(out, "out", _floats(), M * N)
-    if float(beta) != 0.0:
-        _need(addend, "addend", (torch.float32,), M * N)
-    with _on(dev):
-        _check(_lib.mxfp8_gemm(_ptr(pc), _ptr(ps), _ptr(qc), _ptr(qs), M, N, K, float(alpha), float(beta),
-                               _ptr(addend), _ptr(out), _dt(out), *_ws_args(workspace), _stream(stream, dev)),
-               "mxfp8_gemm")
+        if workspace is not None:
+            ws = workspace.data_ptr(), workspace.numel()
+    _launch(_lib.mxfp8_gemm, "mxfp8_gemm", dev, stream, pc.data_ptr(), ps.data_ptr(), qc.data_ptr(), qs.data_ptr(),
+            M, N, K, alpha, beta, add, out.data_ptr(), _TYPES[out.dtype], *ws)
     if given is not None:
         _wrote((given,))
     return out
@@ -1312,24 +1361,23 @@ def nvfp4_linear(x, w, N, out=None, stream=None):
     """y = x W^T for x [T][K] (float32/bfloat16, not quantized) and NVFP4 weights
     w = (codes, scales, global_scale) of [N][K] as nvfp4_quantize returns them;
     y takes x's dtype unless `out` is given.  Built for few tokens."""
-    torch = _torch()
     codes, scales, sg = w
     _need_2d(x, "x")
     T, K = x.shape
-    dev = x.device
+    dev, t = x.device, _type_of(x)
+    _need_on(dev, x, codes, scales, sg, out)
+    if codes.numel() != N * K // 2 or scales.numel() != N * K // 16:
+        raise ValueError(f"w: codes and scales of {N} x {K} needed")
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise TypeError("w: codes and scales are uint8")
+    _need(sg, "global_scale", (torch.float32,), 1)
     given = out
     if out is None:
         out = _empty((T, N), x.dtype, dev, stream)
-    _need_cuda(x, codes, scales, sg, out)
-    if codes.numel() != N * K // 2 or scales.numel() != N * K // 16:
-        raise ValueError(f"w: codes and scales of {N} x {K} needed")
-    _need(codes, "codes", (torch.uint8,), 0)
-    _need(scales, "scales", (torch.uint8,), 0)
-    _need(sg, "global_scale", (torch.float32,), 1)
-    _need(out, "out", _floats(), T * N)
-    with _on(dev):
-        _check(_lib.nvfp4_linear(_ptr(x), _dt(x), T, K, _ptr(codes), _ptr(scales), _ptr(sg), N, _ptr(out), _dt(out),
-                                 _stream(stream, dev)), "nvfp4_linear")
+    else:
+        _need(out, "out", _floats(), T * N)
+    _launch(_lib.nvfp4_linear, "nvfp4_linear", dev, stream, x.data_ptr(), t, T, K, codes.data_ptr(),
+            scales.data_ptr(), sg.data_ptr(), N, out.data_ptr(), _TYPES[out.dtype])
     if given is not None:
         _wrote((given,))
     return out

@@ -18,6 +18,7 @@
 // that is less than their own rounding; FP32 outputs, and the product of few
 // rows, which waits for memory anyway, take P in two parts, codes from 2 on and
 // below: each spans 8 exponents, and 7 + 4 + 2 bits fit the window exactly.
+#include "dma.hpp"
 #include "layer.hpp"
 #include "mx8_device.hpp"
 
@@ -145,13 +146,340 @@ hipError_t few(const Product8& g, hipStream_t s) {
   return hipGetLastError();
 }
 
+
+// ---- tiles ----------------------------------------------------------------------
+// A stage is one panel (256 of K) of the tile's rows in lines of 128 bytes: the
+// first halves of P's rows, their second halves, Q's rows; behind them the
+// scales, eight bytes a row.  Chunk c of row r lies at position c ^ swizzle(r) of
+// its line, so that 32 lanes reading one chunk of 32 rows hit distinct banks.
+// Step s of four multiplies blocks s and 4 + s of every row: of a row of Q a
+// lane of half h takes block 4 h + s (chunk 4 h + s), of a row of P sixteen bytes
+// of either block (chunk 2 s + h of both lines), and the scales are byte s of
+// word h.
+//
+// Workgroups stay for as many tiles as there are per slot, and the stages of
+// their tiles form one stream through the buffers, so that a tile's first panel
+// loads while the tile before leaves.
+template <int BM_, int BN_, int WM_, int WN_, int NST_, int BLOCKS_>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_, kBlocks = BLOCKS_;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int FM = BM / (32 * WM), FN = BN / (32 * WN);
+  static constexpr int kLines = 2 * BM + BN, kCodeBytes = kLines * 128;
+  static constexpr int kCodeLoads = kLines / 8 / kWaves;           // DMA instructions a wave and stage
+  static constexpr int kScaleGroups = (BM + BN) / 32;              // 256 bytes each
+  static constexpr int kScaleLoads = (kScaleGroups + kWaves - 1) / kWaves;
+  static constexpr int kStage = kCodeBytes + kScaleGroups * 256;
+  static constexpr int kScratch = 2304;                            // of a wave's epilogue: 16 rows of 36 floats
+  static constexpr int kLds = NST * kStage + kWaves * kScratch;
+  static_assert(kCodeLoads * 8 * kWaves == kLines && BM % 8 == 0, "uneven loads");
+};
+
+struct Args {
+  Product8 g;
+  int panels, TM, TN, tiles, slots;       // slots: workgroups per XCD
+};
+
+constexpr int kXcds = 8, kCusPerXcd = 32, kStrip = 4;
+
+// Strips of kStrip tile rows, column by column within a strip.
+__device__ __forceinline__ void place_of(const Args& a, int t, int& I, int& J) {
+  const int s = t / (kStrip * a.TN) * kStrip, w = a.TM - s < kStrip ? a.TM - s : kStrip;
+  t -= s * a.TN;
+  I = __builtin_amdgcn_readfirstlane(s + t % w);
+  J = __builtin_amdgcn_readfirstlane(t / w);
+}
+
+// Where a workgroup's loads stand: tile and next panel, and the byte offsets of
+// a lane's loads from the tile's first row.  Rows past an operand's end read its
+// last row: they feed only values that are not written.
+template <class C>
+struct Loads {
+  static constexpr int kLoads = C::kCodeLoads + C::kScaleLoads;
+  int t, g;
+  const uint8_t *p, *q, *ps, *qs;         // the tile's first rows in panel g
+  uint32_t code[C::kCodeLoads], scale[C::kScaleLoads];
+
+  static __device__ __forceinline__ int scale_group(int wave, int k) {
+    const int n = wave * C::kScaleLoads + k;              // the last groups twice where they do not divide
+    return n < C::kScaleGroups ? n : C::kScaleGroups - 1;
+  }
+  __device__ __forceinline__ void start(const Args& a, int tile, int wave, int lane) {
+    int I, J;
+    place_of(a, tile, I, J);
+    t = tile;
+    g = 0;
+    const int64_t m0 = (int64_t)I * C::BM, n0 = (int64_t)J * C::BN;
+    p = a.g.p + m0 * kPanelBytes8;
+    q = a.g.q + n0 * kPanelBytes;
+    ps = a.g.p_scales + m0 * kPanelScales;
+    qs = a.g.q_scales + n0 * kPanelScales;
+    const int pm = (int)(a.g.M - m0 < C::BM ? a.g.M - m0 : C::BM) - 1, qm = (int)(a.g.N - n0 < C::BN ? a.g.N - n0 : C::BN) - 1;
+#pragma unroll
+    for (int k = 0; k < C::kCodeLoads; ++k) {
+      const int line = 8 * (wave * C::kCodeLoads + k);
+      const bool isP = line < 2 * C::BM;
+      const int r = (isP ? line % C::BM : line - 2 * C::BM) + (lane >> 3), last = isP ? pm : qm;
+      const uint32_t row = (uint32_t)(r < last ? r : last);
+      code[k] = (isP ? row * kPanelBytes8 + (line >= C::BM ? 128u : 0u) : row * kPanelBytes) +
+                16u * (uint32_t)((lane & 7) ^ swizzle(r));
+    }
+#pragma unroll
+    for (int k = 0; k < C::kScaleLoads; ++k) {
+      const int n = 32 * scale_group(wave, k), r = (n < C::BM ? n : n - C::BM) + (lane >> 1), last = n < C::BM ? pm : qm;
+      scale[k] = (uint32_t)(r < last ? r : last) * kPanelScales + 4u * (uint32_t)(lane & 1);
+    }
+  }
+  // Load number k of the wave's share into the stage at LDS address `stage`.
+  __device__ __forceinline__ void load(uint32_t stage, int wave, int k) const {
+    if (k < C::kCodeLoads) {
+      const int n = wave * C::kCodeLoads + k;
+      dma16(8 * n < 2 * C::BM ? p : q, code[k], stage + (uint32_t)n * 1024u);
+    } else {
+      const int n = scale_group(wave, k - C::kCodeLoads);
+      dma4(32 * n < C::BM ? ps : qs, scale[k - C::kCodeLoads], stage + (uint32_t)(C::kCodeBytes + 256 * n));
+    }
+  }
+  // To the next panel: of this tile, of the workgroup's next one, or, behind
+  // the last, the same again (into a buffer that nothing reads).
+  __device__ __forceinline__ void advance(const Args& a, int end, int wave, int lane) {
+    if (g + 1 < a.panels) {
+      ++g;
+      p += a.g.M * kPanelBytes8;
+      q += a.g.N * kPanelBytes;
+      ps += a.g.M * kPanelScales;
+      qs += a.g.N * kPanelScales;
+    } else if (t + a.slots < end) {
+      start(a, t + a.slots, wave, renewed(lane));
+    }
+  }
+};
+
+template <class C>
+struct Frags {
+  intx4 q[C::FN];
+  intx4 p[C::FM][2];
+};
+template <class C>
+struct Scales {
+  uint32_t q[C::FN], p[C::FM];
+};
+
+// Read number k of a step: Q's fragments, then the halves of P's.
+template <class C>
+__device__ __forceinline__ void read_frag(const uint8_t* st, uint32_t qo, uint32_t po, int wm, int wn, int k, Frags<C>& f) {
+  if (k < C::FN) {
+    f.q[k] = *reinterpret_cast<const intx4*>(st + qo + (2 * C::BM + (wn * C::FN + k) * 32) * 128);
+  } else {
+    const int i = (k - C::FN) >> 1, half = (k - C::FN) & 1;
+    f.p[i][half] = *reinterpret_cast<const intx4*>(st + po + (half * C::BM + (wm * C::FM + i) * 32) * 128);
+  }
+}
+template <class C>
+__device__ __forceinline__ void read_scale(const uint8_t* st, uint32_t off, int wm, int wn, int k, Scales<C>& f) {
+  st += C::kCodeBytes;
+  if (k < C::FN) f.q[k] = *reinterpret_cast<const uint32_t*>(st + off + (C::BM + (wn * C::FN + k) * 32) * 8);
+  else if (k < C::FN + C::FM) f.p[k - C::FN] = *reinterpret_cast<const uint32_t*>(st + off + (wm * C::FM + k - C::FN) * 32 * 8);
+}
+
+__device__ __forceinline__ constexpr int share(int total, int k, int n) { return total * k / n; }
+
+// One step's matrix instructions; `between(k)` puts memory operations behind
+// the k-th block's, and the compiler keeps this order.
+template <class C, bool EXACT, int S, class F>
+__device__ __forceinline__ void step(const Frags<C>& f, const Scales<C>& sc, floatx16 (&acc)[C::FM][C::FN], F&& between) {
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) {
+    const intx8 x = __builtin_shufflevector(f.p[i][0], f.p[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+    intx8 high, low;
+    if constexpr (EXACT) two_parts(x, high, low);
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+      if constexpr (EXACT) {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(high, four_bits(f.q[j]), acc[i][j], 0, 4, S, (int)sc.p[i], S, (int)sc.q[j]);
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(low, four_bits(f.q[j]), acc[i][j], 0, 4, S, (int)sc.p[i], S, (int)sc.q[j]);
+      } else {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, four_bits(f.q[j]), acc[i][j], 0, 4, S, (int)sc.p[i], S, (int)sc.q[j]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      between(i * C::FN + j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+// acc[i][j][4 q + t] of a lane is row (wm FM + i) 32 + 8 q + 4 (lane / 32) + t,
+// column (wn FN + j) 32 + lane % 32 of the tile.  Sixteen rows of a block at a
+// time pass through the wave's own LDS, from where a lane takes eight neighbours
+// of a row.
+template <class C, Dt OT>
+__device__ __forceinline__ void epilogue(const Product8& g, const floatx16 (&acc)[C::FM][C::FN], int64_t m0, int64_t n0, int wm,
+                                         int wn, int lane, uint8_t* lds) {
+  constexpr int kPitch = 36;
+  float* t = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int el = renewed(lane), h = el >> 5, c = el & 31, r = el >> 2, c8 = (el & 3) * 8;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) t[(8 * q + 4 * h + s) * kPitch + c] = acc[i][j][8 * half + 4 * q + s];
+        wave_sync();
+        float v[8];
+        const float4 lo = *reinterpret_cast<const float4*>(t + r * kPitch + c8);
+        const float4 hi = *reinterpret_cast<const float4*>(t + r * kPitch + c8 + 4);
+        v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+        v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+        const int64_t row = m0 + (wm * C::FM + i) * 32 + 16 * half + r, col = n0 + (wn * C::FN + j) * 32 + c8;
+        if (row < g.M && col < g.N) {
+          const int64_t at = row * g.N + col;
+          const int n = g.N - col < 8 ? (int)(g.N - col) : 8;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] *= g.alpha;
+          if (g.addend) {
+            Raw8<float> o;
+            o.load(g.addend + at, n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(g.beta, o.get(e), v[e]);
+          }
+          if constexpr (OT == Dt::F32) store8u(static_cast<float*>(g.out) + at, n, v);
+          else store8u(static_cast<uint16_t*>(g.out) + at, n, v);
+        }
+        wave_sync();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+}
+
+template <class C, Dt OT>
+__global__ __launch_bounds__(C::kThreads, C::kBlocks * C::kWaves / 4) void tile8_kernel(const Args a) {
+  constexpr bool kExact = OT == Dt::F32;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[C::kLds];
+  // one contiguous run of tiles an XCD
+  const int x = (int)blockIdx.x % kXcds;
+  const int end = (int)((int64_t)(x + 1) * a.tiles / kXcds);
+  int tile = (int)((int64_t)x * a.tiles / kXcds) + (int)blockIdx.x / kXcds;
+  if (tile >= end) return;
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  uint8_t* scratch = smem + C::NST * C::kStage + wave * C::kScratch;
+
+  floatx16 acc[C::FM][C::FN];
+  Loads<C> next;
+  next.start(a, tile, wave, lane);
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+  constexpr int kLoads = Loads<C>::kLoads, kReads = C::FN + 2 * C::FM, kMul = C::FM * C::FN;
+  uint32_t qo[4], po[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    qo[s] = (uint32_t)(r * 128 + 16 * ((4 * h + s) ^ swizzle(r)));
+    po[s] = (uint32_t)(r * 128 + 16 * ((2 * s + h) ^ swizzle(r)));
+  }
+  const uint32_t so = (uint32_t)(r * 8 + 4 * h);
+  Frags<C> f0, f1;
+  Scales<C> sc;
+  // all but the newest NST - 2 stages' loads of this wave have landed
+  auto wait_loads = [&] { asm volatile("s_waitcnt vmcnt(%0)" ::"n"((C::NST - 2) * kLoads) : "memory"); };
+
+  // NST - 1 stages in flight before the first is read, then always NST
+#pragma unroll 1
+  for (int s = 0; s < C::NST - 1; ++s) {
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) next.load(lds0 + s * C::kStage, wave, k);
+    next.advance(a, end, wave, lane);
+  }
+  wait_loads();
+  all_waves();
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) next.load(lds0 + (C::NST - 1) * C::kStage, wave, k);
+#pragma unroll
+  for (int k = 0; k < kReads; ++k) {
+    read_scale<C>(smem, so, wm, wn, k, sc);
+    read_frag<C>(smem, qo[0], po[0], wm, wn, k, f0);
+  }
+
+  int cur = 0;
+  for (; tile < end; tile += a.slots) {
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    for (int g = 0; g < a.panels; ++g) {
+      // here, not behind the loads: a branch behind the matrix instructions
+      // would let the compiler sink them past it
+      next.advance(a, end, wave, lane);
+      const uint8_t* st = smem + cur * C::kStage;
+      auto ahead = [&](int s, Frags<C>& f) {
+        return [&, s](int k) {
+#pragma unroll
+          for (int n = share(kReads, k, kMul); n < share(kReads, k + 1, kMul); ++n)
+            read_frag<C>(st, qo[s], po[s], wm, wn, n, f);
+        };
+      };
+      step<C, kExact, 0>(f0, sc, acc, ahead(1, f1));
+      step<C, kExact, 1>(f1, sc, acc, ahead(2, f0));
+      step<C, kExact, 2>(f0, sc, acc, ahead(3, f1));
+      // every read of this stage has returned: its buffer is free once all
+      // waves are here, and the next stage's loads have landed
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      wait_loads();
+      all_waves();
+      const uint32_t freed = lds0 + cur * C::kStage;
+      cur = cur + 1 == C::NST ? 0 : cur + 1;
+      const uint8_t* nst = smem + cur * C::kStage;
+      Scales<C> nsc;
+      step<C, kExact, 3>(f1, sc, acc, [&](int k) {
+#pragma unroll
+        for (int n = share(kReads, k, kMul); n < share(kReads, k + 1, kMul); ++n) {
+          read_scale<C>(nst, so, wm, wn, n, nsc);
+          read_frag<C>(nst, qo[0], po[0], wm, wn, n, f0);
+        }
+#pragma unroll
+        for (int n = share(kLoads, k, kMul); n < share(kLoads, k + 1, kMul); ++n) next.load(freed, wave, n);
+      });
+      sc = nsc;
+    }
+    int I, J;
+    place_of(a, tile, I, J);
+    epilogue<C, OT>(a.g, acc, (int64_t)I * C::BM, (int64_t)J * C::BN, wm, wn, renewed(lane), scratch);
+  }
+  // the loads behind the last stage write LDS until they land
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+using Large = Tile<128, 256, 4, 2, 2, 1>;
+using Small = Tile<64, 64, 2, 2, 3, 1>;
+
+template <class C, Dt OT>
+hipError_t tiled(const Product8& g, hipStream_t s) {
+  Args a{g, (int)((g.K + kPanel - 1) / kPanel), (int)((g.M + C::BM - 1) / C::BM), (int)((g.N + C::BN - 1) / C::BN), 0, 0};
+  a.tiles = a.TM * a.TN;
+  a.slots = C::kBlocks * kCusPerXcd;
+  const int most = (a.tiles + kXcds - 1) / kXcds;
+  tile8_kernel<C, OT><<<dim3((unsigned)(most < a.slots ? most : a.slots) * kXcds), C::kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <Dt OT>
+hipError_t product(const Product8& g, hipStream_t s) {
+  if (g.M <= 16) return few<1, OT>(g, s);
+  if (g.M <= 32) return few<2, OT>(g, s);
+  const int64_t large = ((g.M + 127) / 128) * ((g.N + 255) / 256);
+  return large >= 192 ? tiled<Large, OT>(g, s) : tiled<Small, OT>(g, s);
+}
+
 }  // namespace
 
 size_t mx8_workspace(int64_t, int64_t, int64_t) { return 0; }
 
 hipError_t launch_mx8_product(const Product8& g, void*, hipStream_t s) {
-  if (g.M <= 16) return g.ot == Dt::F32 ? few<1, Dt::F32>(g, s) : few<1, Dt::BF16>(g, s);
-  return g.ot == Dt::F32 ? few<2, Dt::F32>(g, s) : few<2, Dt::BF16>(g, s);
+  return g.ot == Dt::F32 ? product<Dt::F32>(g, s) : product<Dt::BF16>(g, s);
 }
 
 }  // namespace nvfp4

@@ -171,25 +171,20 @@ __device__ __forceinline__ void encode_block(const float (&v)[32], uint4& c, uin
 }
 
 template <bool VEC>
-__device__ __forceinline__ void load_two(const float* p, int n, float& a, float& b) {
-  if constexpr (VEC) {
-    const float2 v = *reinterpret_cast<const float2*>(p);
-    a = v.x;
-    b = v.y;
-  } else {
-    a = p[0];
-    b = n > 1 ? p[1] : 0.0f;
-  }
+__device__ __forceinline__ float2 load_two(const float* p, int n) {
+  if constexpr (VEC) return *reinterpret_cast<const float2*>(p);
+  else return make_float2(p[0], n > 1 ? p[1] : 0.0f);
 }
 template <bool VEC>
-__device__ __forceinline__ void load_two(const uint16_t* p, int n, float& a, float& b) {
-  const uint32_t v = VEC ? *reinterpret_cast<const uint32_t*>(p) : (uint32_t)p[0] | (n > 1 ? (uint32_t)p[1] << 16 : 0u);
-  a = bf16_lo(v);
-  b = bf16_hi(v);
+__device__ __forceinline__ float2 load_two(const uint16_t* p, int n) {
+  uint32_t v;
+  if constexpr (VEC) v = *reinterpret_cast<const uint32_t*>(p);
+  else v = (uint32_t)p[0] | (n > 1 ? (uint32_t)p[1] << 16 : 0u);
+  return make_float2(bf16_lo(v), bf16_hi(v));
 }
 
 template <class H, bool VEC>
-__global__ __launch_bounds__(512) void norm_cols_kernel(const H* h, const float* rstd, const void* w, Dt wt, int64_t T,
+__global__ __launch_bounds__(512) void norm_cols_kernel(const H* h, const float* rstd, const void* weight, Dt wt, int64_t T,
                                                         int64_t C, uint32_t tiles, uint8_t* codes, uint8_t* scales) {
   __shared__ __attribute__((aligned(16))) uint8_t lc[kTileCols * 128];
   __shared__ __attribute__((aligned(16))) uint8_t ls[kTileCols * 8];
@@ -199,23 +194,18 @@ __global__ __launch_bounds__(512) void norm_cols_kernel(const H* h, const float*
   const int64_t t0 = g * kPanel + 32 * wave;
   const int64_t c = c0 + 2 * lane;
   const int n = c < C ? (C - c < 2 ? 1 : 2) : 0;
+  float2 w = make_float2(0.0f, 0.0f);
+  if (n) w = wt == Dt::F32 ? load_two<false>(static_cast<const float*>(weight) + c, n) : load_two<false>(static_cast<const uint16_t*>(weight) + c, n);
+  float2 u[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) u[i] = t0 + i < T && n ? load_two<VEC>(h + (t0 + i) * C + c, n) : make_float2(0.0f, 0.0f);
   float v0[32], v1[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    v0[i] = v1[i] = 0.0f;
-    if (t0 + i < T && n) load_two<VEC>(h + (t0 + i) * C + c, n, v0[i], v1[i]);
-  }
-  float w0 = 0.0f, w1 = 0.0f;
-  if (n) {
-    if (wt == Dt::F32) load_two<false>(static_cast<const float*>(w) + c, n, w0, w1);
-    else load_two<false>(static_cast<const uint16_t*>(w) + c, n, w0, w1);
-  }
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    if (t0 + i >= T) continue;                   // zeros behind the last token
-    const float r = rstd[t0 + i];
-    v0[i] = v0[i] * r * w0;
-    v1[i] = v1[i] * r * w1;
+    // behind the last token 0
+    const float r = t0 + i < T ? rstd[t0 + i] : 0.0f;
+    v0[i] = u[i].x * r * w.x;
+    v1[i] = u[i].y * r * w.y;
   }
   uint4 k0, k1;
   uint32_t b0, b1;

@@ -1,15 +1,19 @@
 // y = x W^T with W in NVFP4 (16-element blocks with E4M3 scales, one FP32 scale
 // s_g) and x as it is: the linear layer of few tokens, whose time is the
-// weights' way from memory.
+// weights' way from memory as long as decoding them (two or three vector
+// instructions a pair) stays below it.
 //
-// A weight's value without s_g, E2M1 times E4M3, has at most six significant
-// bits and is exact in BF16, so BF16 rows of x multiply it on
-// v_mfma_f32_16x16x32_bf16 without a rounding before the FP32 sum; FP32 rows do
-// so in three BF16 parts of eight bits each, which hold all 24.
+// x enters as BF16 operands that sum to it: BF16 rows as they are, FP32 rows in
+// three parts of eight bits each, which hold all 24.  E2M1 codes, and codes
+// times their E4M3 scale (at most six significant bits), are exact in BF16 too,
+// so every product is exact and sums are FP32.
 //
-// A workgroup takes 16 rows of W, its waves divide K; of 128 elements a lane
-// has 32 of one row (16 bytes of codes, two scales), eight a matrix
-// instruction.  The waves' sums meet in LDS, in wave order.
+// One or two tokens (gemv_kernel): a wave takes rows of W whole, 32 codes a
+// lane, x in LDS; v_dot2_f32_bf16 adds a block's sixteen products without its
+// scale, which one fused multiply-add a block applies.
+// More (nv_kernel): a workgroup takes 16 rows of W, its waves divide K; codes
+// times scales feed v_mfma_f32_16x16x32_bf16.
+#include "dma.hpp"
 #include "layer.hpp"
 #include "mx8_device.hpp"
 
@@ -19,19 +23,194 @@ using namespace mx;
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef uint16_t u16_any __attribute__((aligned(1)));   // two neighbouring scales, K / 16 of any parity
 typedef uint32_t wordx4 __attribute__((ext_vector_type(4)));
-typedef uint32_t word4_8 __attribute__((ext_vector_type(4), aligned(8)));
 
 struct Nv {
   const void* x;
   const uint8_t *codes, *scales;
   const float* sg;
   void* y;
-  int T, N, groups;      // groups: of 16 rows of W
+  int T, N, groups;      // groups: workgroups along N
   int64_t K;
 };
 
+// Eight neighbours of a row of x, and the BF16 operands that sum to them.
+template <class X> struct Parts;
+template <> struct Parts<uint16_t> {
+  static constexpr int kParts = 1;
+  wordx4 w;
+  __device__ __forceinline__ void load(const uint16_t* p) { w = *reinterpret_cast<const wordx4*>(p); }
+  __device__ __forceinline__ void clear() { w = wordx4{0, 0, 0, 0}; }
+  __device__ __forceinline__ void split(wordx4 (&parts)[1]) const { parts[0] = w; }
+};
+template <> struct Parts<float> {
+  static constexpr int kParts = 3;
+  floatx4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const floatx4*>(p);
+    b = *reinterpret_cast<const floatx4*>(p + 4);
+  }
+  __device__ __forceinline__ void clear() { a = b = floatx4{0, 0, 0, 0}; }
+  // The leading bits, cut off, the leading bits of what is left, and the rest.
+  // Infinities and NaN go whole into the first (their lanes are looked for, not
+  // waited for: the whole wave takes the short way where there are none).
+  __device__ __forceinline__ void split(wordx4 (&parts)[3]) const {
+    float v[8];
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = i < 4 ? a[i & 3] : b[i & 3];
+      most = umax(most, mag_bits(v[i]));
+    }
+    const bool odd = __any(most >= 0x7F800000u);
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        parts[p][i] = __builtin_amdgcn_perm(__float_as_uint(v[2 * i + 1]), __float_as_uint(v[2 * i]), 0x07060302u);
+      if (p == 2) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] -= __uint_as_float(__float_as_uint(v[i]) & 0xFFFF0000u);
+      if (p == 0 && odd) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float f = i < 4 ? a[i & 3] : b[i & 3];
+          if (fabsf(f) < __builtin_inff()) continue;
+          v[i] = 0.0f;
+          if (f != f) parts[0][i >> 1] |= i & 1 ? 0x7FC00000u : 0x7FC0u;
+        }
+      }
+    }
+  }
+};
+
+template <Dt OT>
+__device__ __forceinline__ void put1(void* y, int64_t at, float v) {
+  if constexpr (OT == Dt::F32) static_cast<float*>(y)[at] = v;
+  else static_cast<uint16_t*>(y)[at] = (uint16_t)pack_bf16(v, 0.0f);
+}
+
+// ---- one or two tokens --------------------------------------------------------
+constexpr int kStep = 64 * 32;            // elements of a row that a wave takes at a time
+constexpr int kGemvWaves = 8, kGemvRows = 2;   // rows of W a wave
+constexpr int kGemvLds = 65536;           // bytes of x a workgroup holds at most
+
+// The sum over a wave's lanes, in every lane.
+__device__ __forceinline__ float lane_sum(float v) {
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, true));    // lane ^ 1
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, true));    // lane ^ 2
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, true));   // mirrored in eight
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, true));   // mirrored in sixteen
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// Two codes in byte SEL of w, as BF16.
+template <int SEL>
+__device__ __forceinline__ bf16x2 pair_of(uint32_t w) {
+  return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, SEL);
+}
+__device__ __forceinline__ float dot8(uint32_t c, wordx4 x, float sum) {
+  union { uint32_t u; bf16x2 v; } x0{x[0]}, x1{x[1]}, x2{x[2]}, x3{x[3]};
+  sum = __builtin_amdgcn_fdot2_f32_bf16(pair_of<0>(c), x0.v, sum, false);
+  sum = __builtin_amdgcn_fdot2_f32_bf16(pair_of<1>(c), x1.v, sum, false);
+  sum = __builtin_amdgcn_fdot2_f32_bf16(pair_of<2>(c), x2.v, sum, false);
+  return __builtin_amdgcn_fdot2_f32_bf16(pair_of<3>(c), x3.v, sum, false);
+}
+
+// span: elements of K in LDS at a time, a multiple of kStep.  K is a multiple
+// of 32.  A part of a row of x lies in LDS in chunks of eight elements; chunk
+// 4 l + j, which lane l reads as its j-th, at 4 l + (j ^ l / 4 % 4), so that eight
+// lanes reading their j-th hit distinct banks.
+template <class X, int T, Dt OT>
+__global__ __launch_bounds__(64 * kGemvWaves) void gemv_kernel(const Nv a, int span) {
+  constexpr int P = Parts<X>::kParts, R = kGemvRows;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  wordx4* xs = reinterpret_cast<wordx4*>(lds);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = ((int)blockIdx.x * kGemvWaves + wave) * R;
+  const uint8_t *codes[R], *scales[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t n = n0 + r < a.N ? n0 + r : a.N - 1;      // rows behind W's end: not written
+    codes[r] = a.codes + n * (a.K / 2);
+    scales[r] = a.scales + n * (a.K / 16);
+  }
+  float acc[R][T];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < T; ++t) acc[r][t] = 0.0f;
+  const int chunks = span / 8;            // of a part in LDS
+  wordx4 c[R];
+  uint32_t sc[R];
+  // the lane's codes of the step at k; behind a row's end its last ones, with
+  // scales of zero
+  auto fetch = [&](int64_t k) {
+    const int64_t kl = k + 32 * lane, kc = kl < a.K ? kl : a.K - 32;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      c[r] = *reinterpret_cast<const wordx4*>(codes[r] + kc / 2);
+      sc[r] = *reinterpret_cast<const uint16_t*>(scales[r] + kc / 16);
+    }
+  };
+  fetch(0);
+  for (int64_t k0 = 0; k0 < a.K; k0 += span) {
+    if (k0) __syncthreads();              // all waves are through with the span before
+    const int64_t left = a.K - k0;
+    for (int i = threadIdx.x; i < T * chunks; i += 64 * kGemvWaves) {
+      const int t = T == 1 ? 0 : i >= chunks, ch = i - t * chunks;
+      Parts<X> v;
+      v.clear();
+      if (8 * (int64_t)ch < left) v.load(static_cast<const X*>(a.x) + t * a.K + k0 + 8 * ch);
+      const int l = ch >> 2, at = 4 * l + ((ch ^ (l >> 2)) & 3);
+      wordx4 parts[P];
+      v.split(parts);
+#pragma unroll
+      for (int p = 0; p < P; ++p) xs[(t * P + p) * chunks + at] = parts[p];
+    }
+    __syncthreads();
+    const int64_t k1 = k0 + span < a.K ? k0 + span : a.K;
+    for (int64_t k = k0; k < k1; k += kStep) {
+      wordx4 u[R];
+      float s[R][2];
+      const bool in = k + 32 * lane < a.K;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        u[r] = c[r];
+        const uint32_t b = in ? sc[r] : 0u;
+        s[r][0] = __builtin_amdgcn_cvt_f32_fp8((int)b, 0);
+        s[r][1] = __builtin_amdgcn_cvt_f32_fp8((int)b, 1);
+      }
+      fetch(k + kStep < a.K ? k + kStep : k);
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const wordx4* x = xs + (t * P + p) * chunks + (int)(k - k0) / 8 + 4 * lane;
+          wordx4 v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = x[j ^ ((lane >> 2) & 3)];
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            acc[r][t] = fmaf(s[r][0], dot8(u[r][1], v[1], dot8(u[r][0], v[0], 0.0f)), acc[r][t]);
+            acc[r][t] = fmaf(s[r][1], dot8(u[r][3], v[3], dot8(u[r][2], v[2], 0.0f)), acc[r][t]);
+          }
+        }
+    }
+  }
+  const float sg = *a.sg;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const float v = lane_sum(acc[r][t]) * sg;
+      if (lane == r * T + t && n0 + r < a.N) put1<OT>(a.y, (int64_t)t * a.N + n0 + r, v);
+    }
+}
+
+// ---- more tokens ------------------------------------------------------------------
 // Eight weights: codes times their block's scale.
 __device__ __forceinline__ bf16x8 weights8(uint32_t w, float s) {
   const floatx2 a = decode2<0>(w, 1.0f), b = decode2<1>(w, 1.0f), c = decode2<2>(w, 1.0f), d = decode2<3>(w, 1.0f);
@@ -43,117 +222,106 @@ __device__ __forceinline__ bf16x8 weights8(uint32_t w, float s) {
   return r.v;
 }
 
-// Eight values of x as BF16 operands that sum to them: one, or three for FP32.
-template <class X> struct Parts;
-template <> struct Parts<uint16_t> {
-  static constexpr int kParts = 1;
-  wordx4 w;
-  __device__ __forceinline__ void load(const uint16_t* p, bool in) {
-    w = in ? *reinterpret_cast<const wordx4*>(p) : wordx4{0, 0, 0, 0};
-  }
-  __device__ __forceinline__ bf16x8 part(int) const {
-    union { wordx4 u; bf16x8 v; } r{w};
-    return r.v;
-  }
-};
-template <> struct Parts<float> {
-  static constexpr int kParts = 3;
-  floatx4 a, b;
-  __device__ __forceinline__ void load(const float* p, bool in) {
-    a = in ? *reinterpret_cast<const floatx4*>(p) : floatx4{0, 0, 0, 0};
-    b = in ? *reinterpret_cast<const floatx4*>(p + 4) : floatx4{0, 0, 0, 0};
-  }
-  // The next part: the leading bits, cut off; what is left stays.  Infinities
-  // and NaN go whole into the first.
-  static __device__ __forceinline__ uint32_t take(float& v) {
-    const uint32_t bits = __float_as_uint(v);
-    if (!(fabsf(v) < __builtin_inff())) {
-      const uint32_t top = v != v ? 0x7FC00000u : bits;
-      v = 0.0f;
-      return top;
-    }
-    const uint32_t top = bits & 0xFFFF0000u;
-    v -= __uint_as_float(top);
-    return top;
-  }
-  __device__ __forceinline__ bf16x8 part(int) {
-    union { uint32_t u[4]; bf16x8 v; } r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float lo = i < 2 ? a[2 * i] : b[2 * i - 4], hi = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
-      const uint32_t l = take(lo), h = take(hi);
-      r.u[i] = l >> 16 | h;
-      if (i < 2) {
-        a[2 * i] = lo;
-        a[2 * i + 1] = hi;
-      } else {
-        b[2 * i - 4] = lo;
-        b[2 * i - 3] = hi;
-      }
-    }
-    return r.v;
-  }
-};
-
-template <class X, int TG, Dt OT, int WAVES>
+// Of a step of 128 elements lane (q, r) = (l / 16, l % 16) multiplies row r's
+// elements 32 q .. + 31, eight an instruction.  Its codes are 16 bytes of W's row;
+// x comes in whole lines (four rows an instruction) and turns in LDS of the
+// wave's own: chunk c (eight elements) of row r at position c ^ r.
+// Everything that DEEP steps read goes out before the first is used, from
+// clamped places instead of behind branches, which would wait for each other;
+// the places are 32-bit offsets from scalar bases.
+// K32: K is a multiple of 32, a lane's 32 elements all in or all behind the end.
+template <class X, int TG, Dt OT, int WAVES, int DEEP, bool K32>
 __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
-  constexpr int kDeep = 4;                                  // steps of 128 in flight
+  constexpr int P = Parts<X>::kParts;
+  __shared__ wordx4 turn[WAVES][P * TG][16][16];
   __shared__ floatx4 sums[WAVES][TG][64];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = (int)(blockIdx.x % (unsigned)a.groups) * 16, t0 = (int)(blockIdx.x / (unsigned)a.groups) * 16 * TG;
+  const int64_t K = a.K;
+  const int steps = (int)((K + 127) / 128), last = (int)(K - 128 * (int64_t)(steps - 1));   // elements of the last step
+  const int s0 = (int)((int64_t)steps * wave / WAVES), s1 = (int)((int64_t)steps * (wave + 1) / WAVES);
   // rows behind an operand's end: its last row, into values that are not written
-  const int64_t row = n0 + r < a.N ? n0 + r : a.N - 1;
-  const uint8_t* codes = a.codes + row * (a.K / 2);
-  const uint8_t* scales = a.scales + row * (a.K / 16);
-  const X* x[TG];
+  const uint32_t row = (uint32_t)(n0 + r < a.N ? r : a.N - 1 - n0);
+  const uint8_t* codes = a.codes + (int64_t)n0 * (K / 2);
+  const uint8_t* scales = a.scales + (int64_t)n0 * (K / 16);
+  const X* x = static_cast<const X*>(a.x) + (int64_t)t0 * K;
+  const uint32_t crow = row * (uint32_t)(K / 2), srow = row * (uint32_t)(K / 16);
+  uint32_t xrow[TG][4];
 #pragma unroll
-  for (int g = 0; g < TG; ++g) {
-    const int t = t0 + 16 * g + r;
-    x[g] = static_cast<const X*>(a.x) + (int64_t)(t < a.T ? t : a.T - 1) * a.K;
-  }
-  const int64_t steps = (a.K + 127) / 128;
-  const int64_t s0 = steps * wave / WAVES, s1 = steps * (wave + 1) / WAVES;
+  for (int g = 0; g < TG; ++g)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 16 * g + 4 * i + q;
+      xrow[g][i] = (uint32_t)(t0 + t < a.T ? t : a.T - 1 - t0) * (uint32_t)K;
+    }
   floatx4 acc[TG];
 #pragma unroll
   for (int g = 0; g < TG; ++g) acc[g] = floatx4{0, 0, 0, 0};
-  for (int64_t s = s0; s < s1; s += kDeep) {
-    wordx4 c[kDeep];
-    uint32_t sc[kDeep];
+  for (int s = s0; s < s1; s += DEEP) {
+    wordx4 c[DEEP];
+    uint32_t sc[DEEP];
+    Parts<X> v[DEEP][TG][4];
 #pragma unroll
-    for (int i = 0; i < kDeep; ++i) {
-      // K is a multiple of 16: of a lane's 32 elements all, the first half or none
-      const int64_t k = 128 * (s + i) + 32 * q;
-      c[i] = wordx4{0, 0, 0, 0};
-      sc[i] = 0;
-      if (s + i < s1) {
-        if (k + 32 <= a.K) {
-          c[i] = *reinterpret_cast<const word4_8*>(codes + k / 2);
-          sc[i] = *reinterpret_cast<const u16_any*>(scales + k / 16);
-        } else if (k < a.K) {
-          const uint2 h = *reinterpret_cast<const uint2*>(codes + k / 2);
-          c[i] = wordx4{h.x, h.y, 0, 0};
-          sc[i] = scales[k / 16];
+    for (int i = 0; i < DEEP; ++i) {
+      const int at = s + i < s1 ? s + i : s1 - 1;             // the last again: not multiplied
+      const int end = at == steps - 1 ? last : 128;           // elements of this step
+      const uint8_t* cs = codes + (int64_t)at * 64;
+      const uint8_t* ss = scales + (int64_t)at * 8;
+      if constexpr (K32) {
+        const uint32_t e = 32 * q < end ? 32u * q : 0u;
+        c[i] = *reinterpret_cast<const wordx4*>(cs + (crow + e / 2));
+        sc[i] = *reinterpret_cast<const uint16_t*>(ss + (srow + e / 16));
+      } else {
+        const uint32_t e0 = 32 * q < end ? 32u * q : 0u, e1 = 32 * q + 16 < end ? 32u * q + 16 : 0u;
+        const uint2 lo = *reinterpret_cast<const uint2*>(cs + (crow + e0 / 2)), hi = *reinterpret_cast<const uint2*>(cs + (crow + e1 / 2));
+        c[i] = wordx4{lo.x, lo.y, hi.x, hi.y};
+        sc[i] = ss[srow + e0 / 16] | (uint32_t)ss[srow + e1 / 16] << 8;
+      }
+      const X* xc = x + (int64_t)at * 128;
+      const uint32_t e = 8 * r < end ? 8u * r : 0u;
+#pragma unroll
+      for (int g = 0; g < TG; ++g)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][g][j].load(xc + (xrow[g][j] + e));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < DEEP; ++i) {
+      if (s + i >= s1) break;
+      if (s + i == steps - 1 && last < 128) {                 // nothing behind K
+        sc[i] = 32 * q + 32 <= last ? sc[i] : 32 * q < last ? sc[i] & 0xFFu : 0u;
+        if (8 * r >= last) {
+#pragma unroll
+          for (int g = 0; g < TG; ++g)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][g][j].clear();
         }
       }
-    }
+      // row 4 j + q, chunk r
 #pragma unroll
-    for (int i = 0; i < kDeep; ++i) {
-      if (s + i >= s1) break;
-      const int64_t k = 128 * (s + i) + 32 * q;
+      for (int g = 0; g < TG; ++g)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          wordx4 parts[P];
+          v[i][g][j].split(parts);
+#pragma unroll
+          for (int p = 0; p < P; ++p) turn[wave][g * P + p][4 * j + q][r ^ (4 * j + q)] = parts[p];
+        }
+      wave_sync();
       const float f[2] = {__builtin_amdgcn_cvt_f32_fp8((int)sc[i], 0), __builtin_amdgcn_cvt_f32_fp8((int)sc[i], 1)};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const bf16x8 w = weights8(c[i][j], f[j >> 1]);
 #pragma unroll
-        for (int g = 0; g < TG; ++g) {
-          Parts<X> v;
-          v.load(x[g] + k + 8 * j, k + 8 * j < a.K);
+        for (int g = 0; g < TG; ++g)
 #pragma unroll
-          for (int p = 0; p < Parts<X>::kParts; ++p)
-            acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, v.part(p), acc[g], 0, 0, 0);
-        }
+          for (int p = 0; p < P; ++p) {
+            union { wordx4 u; bf16x8 v; } b{turn[wave][g * P + p][r][(4 * q + j) ^ r]};
+            acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, b.v, acc[g], 0, 0, 0);
+          }
       }
+      wave_sync();
     }
   }
 #pragma unroll
@@ -173,25 +341,46 @@ __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (n + e < a.N) {
-        if constexpr (OT == Dt::F32) static_cast<float*>(a.y)[at + e] = v[e];
-        else static_cast<uint16_t*>(a.y)[at + e] = (uint16_t)pack_bf16(v[e], 0.0f);
-      }
+      if (n + e < a.N) put1<OT>(a.y, at + e, v[e]);
   }
 }
 
-template <class X, int TG, Dt OT>
-hipError_t launch(const Nv& a, hipStream_t s) {
-  const unsigned grid = (unsigned)a.groups * (unsigned)((a.T + 16 * TG - 1) / (16 * TG));
-  // enough waves to cover the chip several times, none without a step
-  if (grid < 512 && a.K >= 2048) nv_kernel<X, TG, OT, 16><<<grid, 1024, 0, s>>>(a);
-  else nv_kernel<X, TG, OT, 4><<<grid, 256, 0, s>>>(a);
+template <class X, int T, Dt OT>
+hipError_t gemv(Nv a, hipStream_t s) {
+  constexpr int kBytes = 2 * T * Parts<X>::kParts;           // of LDS an element of K
+  const int64_t most = kGemvLds / kBytes / kStep * kStep, all = (a.K + kStep - 1) / kStep * kStep;
+  const int span = (int)(all < most ? all : most);
+  a.groups = (a.N + kGemvWaves * kGemvRows - 1) / (kGemvWaves * kGemvRows);
+  gemv_kernel<X, T, OT><<<dim3((unsigned)a.groups), 64 * kGemvWaves, (size_t)span * kBytes, s>>>(a, span);
   return hipGetLastError();
 }
-template <class X>
-hipError_t by_shape(const Nv& a, Dt ot, hipStream_t s) {
-  if (a.T <= 16) return ot == Dt::F32 ? launch<X, 1, Dt::F32>(a, s) : launch<X, 1, Dt::BF16>(a, s);
-  return ot == Dt::F32 ? launch<X, 2, Dt::F32>(a, s) : launch<X, 2, Dt::BF16>(a, s);
+
+template <class X, int TG, Dt OT, bool K32>
+hipError_t launch(const Nv& a, hipStream_t s) {
+  const unsigned grid = (unsigned)a.groups * (unsigned)((a.T + 16 * TG - 1) / (16 * TG));
+  constexpr int kDeep = sizeof(X) == 2 && TG == 1 ? 2 : 1;
+  // FP32's parts take 13 KB of LDS a wave: with more than one workgroup a CU
+  // four waves each leave room for three of them (8 tokens, 11008 x 4096: 21 us
+  // against 26 with eight; 5 tokens, 777 x 1504: 6.2 against 5.9)
+  if constexpr (sizeof(X) == 4)
+    if (grid > 256) {
+      nv_kernel<X, TG, OT, 4, kDeep, K32><<<grid, 256, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  nv_kernel<X, TG, OT, 8, kDeep, K32><<<grid, 512, 0, s>>>(a);
+  return hipGetLastError();
+}
+template <class X, int TG, Dt OT>
+hipError_t by_width(const Nv& a, hipStream_t s) {
+  return a.K % 32 == 0 ? launch<X, TG, OT, true>(a, s) : launch<X, TG, OT, false>(a, s);
+}
+template <class X, Dt OT>
+hipError_t by_tokens(const Nv& a, hipStream_t s) {
+  if (a.K % 32 == 0 && a.T == 1) return gemv<X, 1, OT>(a, s);
+  if (a.K % 32 == 0 && a.T == 2) return gemv<X, 2, OT>(a, s);
+  if constexpr (sizeof(X) == 2)
+    if (a.T > 16) return by_width<X, 2, OT>(a, s);
+  return by_width<X, 1, OT>(a, s);
 }
 
 }  // namespace
@@ -199,7 +388,8 @@ hipError_t by_shape(const Nv& a, Dt ot, hipStream_t s) {
 hipError_t launch_nv_linear(const void* x, Dt xt, int64_t T, int64_t K, const uint8_t* codes, const uint8_t* scales,
                             const float* sg, int64_t N, void* y, Dt yt, hipStream_t s) {
   const Nv a{x, codes, scales, sg, y, (int)T, (int)N, (int)((N + 15) / 16), K};
-  return xt == Dt::F32 ? by_shape<float>(a, yt, s) : by_shape<uint16_t>(a, yt, s);
+  if (xt == Dt::F32) return yt == Dt::F32 ? by_tokens<float, Dt::F32>(a, s) : by_tokens<float, Dt::BF16>(a, s);
+  return yt == Dt::F32 ? by_tokens<uint16_t, Dt::F32>(a, s) : by_tokens<uint16_t, Dt::BF16>(a, s);
 }
 
 }  // namespace nvfp4

@@ -138,11 +138,11 @@ def test_nvfp4_linear():
 def test_binding():
     """What only the binding can see: shapes, types and generators."""
     with pytest.raises(ValueError):
-        ns._need_rng(None, 0.5)
+        ns._need_rng(None, torch.device("cuda", 0))
     with pytest.raises(ValueError):
-        ns._need_rng(torch.zeros(2), 0.5)
+        ns._need_rng(torch.zeros(2), torch.device("cuda", 0))
     with pytest.raises(ValueError):
-        ns._need_rng(torch.zeros(3, dtype=torch.int64), 0.5)
+        ns._need_rng(torch.zeros(3, dtype=torch.int64), torch.device("cuda", 0))
     ok = torch.zeros(2, 7, 256, dtype=torch.uint8), torch.zeros(2, 7, 8, dtype=torch.uint8)
     ns._need_blocks(ok, "p", 7, 300, 256)
     for rows, cols, width in ((6, 300, 256), (8, 300, 256), (7, 200, 256), (7, 600, 256), (7, 300, 128)):
