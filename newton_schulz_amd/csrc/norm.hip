@@ -235,6 +235,21 @@ __global__ __launch_bounds__(512) void norm_cols_kernel(const H* h, const float*
 // A workgroup takes every gridDim-th group of rows and keeps its columns' share
 // of dw in registers; the shares are summed by norm_weight_kernel in a fixed
 // order, so that the result is the same every time.
+// dh and, through the dropout, dx of eight columns of row t.
+template <class H>
+__device__ __forceinline__ void put_gradients(const NormBackward& a, int64_t t, int c, uint64_t seed, uint64_t offset,
+                                              float (&d)[8]) {
+  const int64_t at = t * a.C + c;
+  store8u(static_cast<H*>(a.dh) + at, a.C - c, d);
+  if (!a.dx) return;
+  if (a.drop.rng) {
+    const Mask8 mask((uint32_t)(c >> 3), (uint32_t)t, seed, offset);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = mask.keeps(i, a.drop.cut) ? d[i] * a.drop.scale : 0.0f;
+  }
+  store_as(a.dx, a.xt, at, a.C - c, d);
+}
+
 template <class D, class H, int LPR, int NV>
 __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_backward_kernel(const NormBackward a) {
   constexpr int kThreads = LPR < 256 ? 256 : LPR, kRows = kThreads / LPR, kWaves = LPR / 64;
@@ -305,23 +320,108 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_backward_kernel(co
         const float v = r * (dy[k].get(i) * w[i] - h[k].get(i) * r * m);
         d[i] = a.dh_in ? in[k].get(i) + v : v;
       }
-      store8u(static_cast<H*>(a.dh) + at + c, C - c, d);
-      if (a.dx) {
-        if (a.drop.rng) {
-          const Mask8 mask((uint32_t)(c >> 3), (uint32_t)t, seed, offset);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] = mask.keeps(i, a.drop.cut) ? d[i] * a.drop.scale : 0.0f;
-        }
-        store_as(a.dx, a.xt, at + c, C - c, d);
-      }
+      put_gradients<H>(a, t, c, seed, offset, d);
     }
   }
   if (!a.dw) return;
-  float* part = a.partials + ((int64_t)blockIdx.x * kRows + sub) * C;
+  if constexpr (kRows > 1) {
+    // the rows' shares meet first
+    __shared__ float shares[kRows][8][NV * LPR];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) shares[sub][i][k * LPR + lane] = dw[k][i];
+    __syncthreads();
+    if (sub) return;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int y = 1; y < kRows; ++y) dw[k][i] += shares[y][i][k * LPR + lane];
+  }
+  float* part = a.partials + (int64_t)blockIdx.x * C;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = 8 * (k * LPR + lane);
     if (c < C) store8u(part + c, C - c, dw[k]);
+  }
+}
+
+// The same for rows of more than 8192 columns, for which a lane's registers
+// would not do: 1024 lanes walk a row twice, the second time from the caches, and
+// hold its columns' share of dw in LDS.
+template <class D, class H, int V>
+__global__ __launch_bounds__(1024) void norm_backward_wide_kernel(const NormBackward a) {
+  __shared__ float share[V * 8 * 1024];
+  __shared__ float sums[2][16];
+  const int lane = threadIdx.x, C = a.C;
+  const float inv = 1.0f / (float)C;
+  for (int k = 0; k < 8 * V; ++k) share[k * 1024 + lane] = 0.0f;
+  uint64_t seed = 0, offset = 0;
+  if (a.drop.rng) {
+    seed = a.drop.rng[0];
+    offset = a.drop.rng[1];
+  }
+  int buf = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const int64_t at = t * C;
+    const float r = a.rstd[t];
+    float m = 0.0f;
+#pragma unroll 1
+    for (int k = 0; k < V; ++k) {
+      const int c = 8 * (k * 1024 + lane);
+      if (c >= C) break;
+      Raw8<D> dy;
+      Raw8<H> h;
+      dy.load(static_cast<const D*>(a.dy) + at + c, C - c);
+      h.load(static_cast<const H*>(a.h) + at + c, C - c);
+      float w[8];
+      load_weights(a.w, a.wt, c, C - c, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (c + i >= C) break;
+        const float p = dy.get(i) * (h.get(i) * r);
+        m = fmaf(p, w[i], m);
+        share[(8 * k + i) * 1024 + lane] += p;
+      }
+    }
+    m = wave_sum(m);
+    if ((lane & 63) == 0) sums[buf][lane >> 6] = m;
+    __syncthreads();
+    m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m += sums[buf][i];
+    buf ^= 1;
+    m *= inv;
+#pragma unroll 1
+    for (int k = 0; k < V; ++k) {
+      const int c = 8 * (k * 1024 + lane);
+      if (c >= C) break;
+      Raw8<D> dy;
+      Raw8<H> h, in;
+      dy.load(static_cast<const D*>(a.dy) + at + c, C - c);
+      h.load(static_cast<const H*>(a.h) + at + c, C - c);
+      if (a.dh_in) in.load(static_cast<const H*>(a.dh_in) + at + c, C - c);
+      float w[8], d[8];
+      load_weights(a.w, a.wt, c, C - c, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = r * (dy.get(i) * w[i] - h.get(i) * r * m);
+        d[i] = a.dh_in ? in.get(i) + v : v;
+      }
+      put_gradients<H>(a, t, c, seed, offset, d);
+    }
+  }
+  if (!a.dw) return;
+  float* part = a.partials + (int64_t)blockIdx.x * C;
+  for (int k = 0; k < V; ++k) {
+    const int c = 8 * (k * 1024 + lane);
+    if (c >= C) break;
+    float d[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = share[(8 * k + i) * 1024 + lane];
+    store8u(part + c, C - c, d);
   }
 }
 
@@ -412,20 +512,10 @@ hipError_t forward_by_width(const NormForward& a, hipStream_t s) {
   return forward<X, H, 1024, 4>(a, s);
 }
 
-struct BackwardShape {
-  int lpr, nv;
-};
-BackwardShape backward_shape(int64_t C) {
-  if (C <= 512) return {64, 1};
-  if (C <= 1024) return {64, 2};
-  if (C <= 2048) return {256, 1};
-  if (C <= 4096) return {256, 2};
-  if (C <= 8192) return {256, 4};
-  return {1024, C <= 16384 ? 2 : 4};
-}
-constexpr int64_t kBackwardGroups = 1024;    // workgroups at most
+constexpr int64_t kBackwardGroups = 768;     // workgroups at most, three a CU
 int64_t backward_groups(int64_t T, int64_t C) {
-  const int rows = backward_shape(C).lpr == 64 ? 4 : 1;
+  if (C > 8192) return T < 256 ? T : 256;    // of 1024 lanes, one a CU
+  const int rows = C <= 1024 ? 4 : 1;
   const int64_t n = (T + rows - 1) / rows;
   return n < kBackwardGroups ? n : kBackwardGroups;
 }
@@ -437,11 +527,15 @@ hipError_t backward(const NormBackward& a, hipStream_t s) {
 }
 template <class D, class H>
 hipError_t backward_by_width(const NormBackward& a, hipStream_t s) {
-  const BackwardShape b = backward_shape(a.C);
-  if (b.lpr == 64) return b.nv == 1 ? backward<D, H, 64, 1>(a, s) : backward<D, H, 64, 2>(a, s);
-  if (b.lpr == 256)
-    return b.nv == 1 ? backward<D, H, 256, 1>(a, s) : b.nv == 2 ? backward<D, H, 256, 2>(a, s) : backward<D, H, 256, 4>(a, s);
-  return b.nv == 2 ? backward<D, H, 1024, 2>(a, s) : backward<D, H, 1024, 4>(a, s);
+  if (a.C <= 512) return backward<D, H, 64, 1>(a, s);
+  if (a.C <= 1024) return backward<D, H, 64, 2>(a, s);
+  if (a.C <= 2048) return backward<D, H, 256, 1>(a, s);
+  if (a.C <= 4096) return backward<D, H, 256, 2>(a, s);
+  if (a.C <= 8192) return backward<D, H, 256, 4>(a, s);
+  const dim3 grid((unsigned)backward_groups(a.T, a.C));
+  if (a.C <= 16384) norm_backward_wide_kernel<D, H, 2><<<grid, 1024, 0, s>>>(a);
+  else norm_backward_wide_kernel<D, H, 4><<<grid, 1024, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -471,9 +565,7 @@ hipError_t launch_norm_cols(const void* h, Dt ht, const float* rstd, const void*
   return hipGetLastError();
 }
 
-int64_t norm_partials(int64_t T, int64_t C) {
-  return backward_groups(T, C) * (backward_shape(C).lpr == 64 ? 4 : 1);
-}
+int64_t norm_partials(int64_t T, int64_t C) { return backward_groups(T, C); }
 
 hipError_t launch_norm_backward(const NormBackward& n, hipStream_t s) {
   if (n.C < 1 || n.C > kNormMaxCols) return hipErrorInvalidValue;
