@@ -18,6 +18,8 @@
 // that is less than their own rounding; FP32 outputs, and the product of few
 // rows, which waits for memory anyway, take P in two parts, codes from 2 on and
 // below: each spans 8 exponents, and 7 + 4 + 2 bits fit the window exactly.
+#include <algorithm>
+
 #include "dma.hpp"
 #include "layer.hpp"
 #include "mx8_device.hpp"
@@ -68,29 +70,24 @@ __device__ __forceinline__ void put4(const Product8& g, int64_t at, int n, bool 
   }
 }
 
-// Sixteen rows of Q a workgroup, 16 TG rows of P; the waves divide the panels
-// of K and have DEEP of them in flight; their sums meet in LDS, in wave order.
-template <int TG, Dt OT, int WAVES, int DEEP>
+// Sixteen rows of Q a workgroup, up to 16 rows of P; the waves divide the
+// panels of K and have DEEP of them in flight; their sums meet in LDS, in wave
+// order.
+template <Dt OT, int WAVES, int DEEP>
 __global__ __launch_bounds__(64 * WAVES) void few8_kernel(const Product8 g, int panels) {
-  __shared__ floatx4 sums[WAVES][TG][64];
+  __shared__ floatx4 sums[WAVES][64];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = (int)blockIdx.x * 16, t0 = (int)blockIdx.y * 16 * TG;
+  const int n0 = (int)blockIdx.x * 16;
   const int M = (int)g.M, N = (int)g.N;
   // rows behind an operand's end read its last row: not written
-  const int64_t row = n0 + r < N ? n0 + r : N - 1;
-  int64_t prow[TG];
-#pragma unroll
-  for (int i = 0; i < TG; ++i) prow[i] = t0 + 16 * i + r < M ? t0 + 16 * i + r : M - 1;
+  const int64_t row = n0 + r < N ? n0 + r : N - 1, prow = r < M ? r : M - 1;
   const int p0 = panels * wave / WAVES, p1 = panels * (wave + 1) / WAVES;
-  floatx4 acc[TG];
-#pragma unroll
-  for (int i = 0; i < TG; ++i) acc[i] = floatx4{0, 0, 0, 0};
+  floatx4 acc = floatx4{0, 0, 0, 0};
   for (int p = p0; p < p1; p += DEEP) {
     intx4 wc[DEEP][2];
-    uint2 ws[DEEP];
-    intx8 xc[DEEP][2][TG];
-    uint2 xs[DEEP][TG];
+    uint2 ws[DEEP], xs[DEEP];
+    intx8 xc[DEEP][2];
 #pragma unroll
     for (int i = 0; i < DEEP; ++i) {
       const int64_t pi = p + i < p1 ? p + i : p1 - 1;       // the last again: not multiplied
@@ -98,54 +95,47 @@ __global__ __launch_bounds__(64 * WAVES) void few8_kernel(const Product8 g, int 
       wc[i][0] = *reinterpret_cast<const intx4*>(c);
       wc[i][1] = *reinterpret_cast<const intx4*>(c + 64);
       ws[i] = *reinterpret_cast<const uint2*>(g.q_scales + (pi * N + row) * kPanelScales);
+      const uint8_t* x = g.p + (pi * M + prow) * kPanelBytes8 + 16 * q;
 #pragma unroll
-      for (int k = 0; k < TG; ++k) {
-        const uint8_t* x = g.p + (pi * M + prow[k]) * kPanelBytes8 + 16 * q;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const intx4 lo = *reinterpret_cast<const intx4*>(x + 128 * u), hi = *reinterpret_cast<const intx4*>(x + 128 * u + 64);
-          xc[i][u][k] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
-        xs[i][k] = *reinterpret_cast<const uint2*>(g.p_scales + (pi * M + prow[k]) * kPanelScales);
+      for (int u = 0; u < 2; ++u) {
+        const intx4 lo = *reinterpret_cast<const intx4*>(x + 128 * u), hi = *reinterpret_cast<const intx4*>(x + 128 * u + 64);
+        xc[i][u] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
       }
+      xs[i] = *reinterpret_cast<const uint2*>(g.p_scales + (pi * M + prow) * kPanelScales);
     }
 #pragma unroll
     for (int i = 0; i < DEEP; ++i) {
       if (p + i >= p1) break;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int k = 0; k < TG; ++k) {
-          intx8 high, low;
-          two_parts(xc[i][u][k], high, low);
-          const int sw = (int)((u ? ws[i].y : ws[i].x) >> (8 * q)), sx = (int)((u ? xs[i][k].y : xs[i][k].x) >> (8 * q));
-          acc[k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(four_bits(wc[i][u]), high, acc[k], 4, 0, 0, sw, 0, sx);
-          acc[k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(four_bits(wc[i][u]), low, acc[k], 4, 0, 0, sw, 0, sx);
-        }
+      for (int u = 0; u < 2; ++u) {
+        intx8 high, low;
+        two_parts(xc[i][u], high, low);
+        const int sw = (int)((u ? ws[i].y : ws[i].x) >> (8 * q)), sx = (int)((u ? xs[i].y : xs[i].x) >> (8 * q));
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(four_bits(wc[i][u]), high, acc, 4, 0, 0, sw, 0, sx);
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(four_bits(wc[i][u]), low, acc, 4, 0, 0, sw, 0, sx);
+      }
     }
   }
-#pragma unroll
-  for (int i = 0; i < TG; ++i) sums[wave][i][lane] = acc[i];
+  sums[wave][lane] = acc;
   __syncthreads();
-  // lane: rows n0 + 4 q .. + 3 of Q, row r of P's group `wave`
-  if (wave >= TG) return;
-  const int t = t0 + 16 * wave + r, n = n0 + 4 * q;
-  if (t >= M || n >= N) return;
-  floatx4 v = sums[0][wave][lane];
-  for (int w = 1; w < WAVES; ++w) v += sums[w][wave][lane];
-  put4<OT>(g, (int64_t)t * N + n, N - n, N % 4 == 0, v);
+  // lane: rows n0 + 4 q .. + 3 of Q, row r of P
+  if (wave) return;
+  const int n = n0 + 4 * q;
+  if (r >= M || n >= N) return;
+  floatx4 v = sums[0][lane];
+  for (int w = 1; w < WAVES; ++w) v += sums[w][lane];
+  put4<OT>(g, (int64_t)r * N + n, N - n, N % 4 == 0, v);
 }
 
-template <int TG, Dt OT>
+template <Dt OT>
 hipError_t few(const Product8& g, hipStream_t s) {
   const int panels = (int)((g.K + kPanel - 1) / kPanel);
-  const dim3 grid((unsigned)((g.N + 15) / 16), (unsigned)((g.M + 16 * TG - 1) / (16 * TG)));
+  const dim3 grid((unsigned)((g.N + 15) / 16));
   // enough waves to cover the chip several times, none without a panel
-  if (grid.x * grid.y < 512 && panels >= 16) few8_kernel<TG, OT, 16, 1><<<grid, 1024, 0, s>>>(g, panels);
-  else few8_kernel<TG, OT, 4, TG == 1 ? 4 : 2><<<grid, 256, 0, s>>>(g, panels);
+  if (grid.x < 512 && panels >= 16) few8_kernel<OT, 16, 1><<<grid, 1024, 0, s>>>(g, panels);
+  else few8_kernel<OT, 4, 4><<<grid, 256, 0, s>>>(g, panels);
   return hipGetLastError();
 }
-
 
 // ---- tiles ----------------------------------------------------------------------
 // A stage is one panel (256 of K) of the tile's rows in lines of 128 bytes: the
@@ -160,9 +150,9 @@ hipError_t few(const Product8& g, hipStream_t s) {
 // Workgroups stay for as many tiles as there are per slot, and the stages of
 // their tiles form one stream through the buffers, so that a tile's first panel
 // loads while the tile before leaves.
-template <int BM_, int BN_, int WM_, int WN_, int NST_, int BLOCKS_>
+template <int BM_, int BN_, int WM_, int WN_, int NST_>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_, kBlocks = BLOCKS_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NST = NST_;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int FM = BM / (32 * WM), FN = BN / (32 * WN);
   static constexpr int kLines = 2 * BM + BN, kCodeBytes = kLines * 128;
@@ -175,15 +165,27 @@ struct Tile {
   static_assert(kCodeLoads * 8 * kWaves == kLines && BM % 8 == 0, "uneven loads");
 };
 
+// A unit is K-part `u / tiles` of tile u % tiles, `per` panels of it.
 struct Args {
   Product8 g;
-  int panels, TM, TN, tiles, slots;       // slots: workgroups per XCD
+  int panels, per, TM, TN, tiles, units, slots;       // slots: workgroups per XCD
+  float* partials;                                    // [parts][M][N], with more than one part
 };
 
 constexpr int kXcds = 8, kCusPerXcd = 32, kStrip = 4;
 
+// The kernel's arguments read again: what the epilogue needs of them would
+// otherwise wait in scalar registers through the whole product, and spill.
+__device__ __forceinline__ const Product8& product_again() {
+  uint64_t at = (uint64_t)(uintptr_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(at));
+  return *(const Product8*)(const __attribute__((address_space(4))) Product8*)at;
+}
+
 // Strips of kStrip tile rows, column by column within a strip.
-__device__ __forceinline__ void place_of(const Args& a, int t, int& I, int& J) {
+__device__ __forceinline__ void place_of(const Args& a, int u, int& I, int& J, int& part) {
+  part = __builtin_amdgcn_readfirstlane(u / a.tiles);
+  int t = u - part * a.tiles;
   const int s = t / (kStrip * a.TN) * kStrip, w = a.TM - s < kStrip ? a.TM - s : kStrip;
   t -= s * a.TN;
   I = __builtin_amdgcn_readfirstlane(s + t % w);
@@ -196,7 +198,9 @@ __device__ __forceinline__ void place_of(const Args& a, int t, int& I, int& J) {
 template <class C>
 struct Loads {
   static constexpr int kLoads = C::kCodeLoads + C::kScaleLoads;
-  int t, g;
+  // whether every wave's loads are of one operand: then `p` and `ps` stand for it
+  static constexpr bool kOne = C::BM % (8 * C::kCodeLoads) == 0 && C::BM / 32 % C::kScaleLoads == 0;
+  int u, g, end;                          // unit, next panel and the unit's last + 1
   const uint8_t *p, *q, *ps, *qs;         // the tile's first rows in panel g
   uint32_t code[C::kCodeLoads], scale[C::kScaleLoads];
 
@@ -204,25 +208,41 @@ struct Loads {
     const int n = wave * C::kScaleLoads + k;              // the last groups twice where they do not divide
     return n < C::kScaleGroups ? n : C::kScaleGroups - 1;
   }
-  __device__ __forceinline__ void start(const Args& a, int tile, int wave, int lane) {
-    int I, J;
-    place_of(a, tile, I, J);
-    t = tile;
-    g = 0;
+  __device__ __forceinline__ void start(const Args& a, int unit, int wave, int lane) {
+    int I, J, part;
+    place_of(a, unit, I, J, part);
+    u = unit;
+    g = part * a.per;
+    end = g + a.per < a.panels ? g + a.per : a.panels;
     const int64_t m0 = (int64_t)I * C::BM, n0 = (int64_t)J * C::BN;
-    p = a.g.p + m0 * kPanelBytes8;
-    q = a.g.q + n0 * kPanelBytes;
-    ps = a.g.p_scales + m0 * kPanelScales;
-    qs = a.g.q_scales + n0 * kPanelScales;
+    p = a.g.p + (g * a.g.M + m0) * kPanelBytes8;
+    q = a.g.q + (g * a.g.N + n0) * kPanelBytes;
+    ps = a.g.p_scales + (g * a.g.M + m0) * kPanelScales;
+    qs = a.g.q_scales + (g * a.g.N + n0) * kPanelScales;
+    if constexpr (kOne) {
+      if (8 * wave * C::kCodeLoads >= 2 * C::BM) p = q;
+      if (32 * wave * C::kScaleLoads >= C::BM) ps = qs;
+    }
     const int pm = (int)(a.g.M - m0 < C::BM ? a.g.M - m0 : C::BM) - 1, qm = (int)(a.g.N - n0 < C::BN ? a.g.N - n0 : C::BN) - 1;
-#pragma unroll
-    for (int k = 0; k < C::kCodeLoads; ++k) {
-      const int line = 8 * (wave * C::kCodeLoads + k);
-      const bool isP = line < 2 * C::BM;
-      const int r = (isP ? line % C::BM : line - 2 * C::BM) + (lane >> 3), last = isP ? pm : qm;
+    auto place = [&](int k, bool isP, int first, int half) {
+      const int r = first + (lane >> 3), last = isP ? pm : qm;
       const uint32_t row = (uint32_t)(r < last ? r : last);
-      code[k] = (isP ? row * kPanelBytes8 + (line >= C::BM ? 128u : 0u) : row * kPanelBytes) +
-                16u * (uint32_t)((lane & 7) ^ swizzle(r));
+      code[k] = (isP ? row * kPanelBytes8 + 128u * half : row * kPanelBytes) + 16u * (uint32_t)((lane & 7) ^ swizzle(r));
+    };
+    const int line0 = 8 * wave * C::kCodeLoads;
+    if constexpr (kOne) {
+      // one operand, and of P one half of its rows
+      const bool isP = line0 < 2 * C::BM;
+      const int half = isP && line0 >= C::BM, first = isP ? line0 - half * C::BM : line0 - 2 * C::BM;
+#pragma unroll
+      for (int k = 0; k < C::kCodeLoads; ++k) place(k, isP, first + 8 * k, half);
+    } else {
+#pragma unroll
+      for (int k = 0; k < C::kCodeLoads; ++k) {
+        const int line = line0 + 8 * k;
+        const bool isP = line < 2 * C::BM;
+        place(k, isP, isP ? line % C::BM : line - 2 * C::BM, line >= C::BM);
+      }
     }
 #pragma unroll
     for (int k = 0; k < C::kScaleLoads; ++k) {
@@ -234,23 +254,28 @@ struct Loads {
   __device__ __forceinline__ void load(uint32_t stage, int wave, int k) const {
     if (k < C::kCodeLoads) {
       const int n = wave * C::kCodeLoads + k;
-      dma16(8 * n < 2 * C::BM ? p : q, code[k], stage + (uint32_t)n * 1024u);
+      dma16(kOne || 8 * n < 2 * C::BM ? p : q, code[k], stage + (uint32_t)n * 1024u);
     } else {
       const int n = scale_group(wave, k - C::kCodeLoads);
-      dma4(32 * n < C::BM ? ps : qs, scale[k - C::kCodeLoads], stage + (uint32_t)(C::kCodeBytes + 256 * n));
+      dma4(kOne || 32 * n < C::BM ? ps : qs, scale[k - C::kCodeLoads], stage + (uint32_t)(C::kCodeBytes + 256 * n));
     }
   }
-  // To the next panel: of this tile, of the workgroup's next one, or, behind
+  // To the next panel: of this unit, of the workgroup's next one, or, behind
   // the last, the same again (into a buffer that nothing reads).
-  __device__ __forceinline__ void advance(const Args& a, int end, int wave, int lane) {
-    if (g + 1 < a.panels) {
+  __device__ __forceinline__ void advance(const Args& a, int units, int wave, int lane) {
+    if (g + 1 < end) {
       ++g;
-      p += a.g.M * kPanelBytes8;
-      q += a.g.N * kPanelBytes;
-      ps += a.g.M * kPanelScales;
-      qs += a.g.N * kPanelScales;
-    } else if (t + a.slots < end) {
-      start(a, t + a.slots, wave, renewed(lane));
+      if constexpr (kOne) {
+        p += 8 * wave * C::kCodeLoads < 2 * C::BM ? a.g.M * kPanelBytes8 : a.g.N * kPanelBytes;
+        ps += (32 * wave * C::kScaleLoads < C::BM ? a.g.M : a.g.N) * kPanelScales;
+      } else {
+        p += a.g.M * kPanelBytes8;
+        q += a.g.N * kPanelBytes;
+        ps += a.g.M * kPanelScales;
+        qs += a.g.N * kPanelScales;
+      }
+    } else if (u + a.slots < units) {
+      start(a, u + a.slots, wave, renewed(lane));
     }
   }
 };
@@ -308,12 +333,28 @@ __device__ __forceinline__ void step(const Frags<C>& f, const Scales<C>& sc, flo
   }
 }
 
+// beta addend + alpha v of eight neighbours, or the first n, rounded once.
+template <Dt OT>
+__device__ __forceinline__ void put8(const Product8& g, int64_t at, int n, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= g.alpha;
+  if (g.addend) {
+    Raw8<float> o;
+    o.load(g.addend + at, n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = fmaf(g.beta, o.get(e), v[e]);
+  }
+  if constexpr (OT == Dt::F32) store8u(static_cast<float*>(g.out) + at, n, v);
+  else store8u(static_cast<uint16_t*>(g.out) + at, n, v);
+}
+
 // acc[i][j][4 q + t] of a lane is row (wm FM + i) 32 + 8 q + 4 (lane / 32) + t,
 // column (wn FN + j) 32 + lane % 32 of the tile.  Sixteen rows of a block at a
 // time pass through the wave's own LDS, from where a lane takes eight neighbours
 // of a row.
-template <class C, Dt OT>
-__device__ __forceinline__ void epilogue(const Product8& g, const floatx16 (&acc)[C::FM][C::FN], int64_t m0, int64_t n0, int wm,
+// PART: as they are, to a part's own [M][N].
+template <class C, Dt OT, bool PART>
+__device__ __forceinline__ void epilogue(const Product8& g, float* part, const floatx16 (&acc)[C::FM][C::FN], int64_t m0, int64_t n0, int wm,
                                          int wn, int lane, uint8_t* lds) {
   constexpr int kPitch = 36;
   float* t = reinterpret_cast<float*>(lds);
@@ -338,31 +379,23 @@ __device__ __forceinline__ void epilogue(const Product8& g, const floatx16 (&acc
         if (row < g.M && col < g.N) {
           const int64_t at = row * g.N + col;
           const int n = g.N - col < 8 ? (int)(g.N - col) : 8;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= g.alpha;
-          if (g.addend) {
-            Raw8<float> o;
-            o.load(g.addend + at, n);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(g.beta, o.get(e), v[e]);
-          }
-          if constexpr (OT == Dt::F32) store8u(static_cast<float*>(g.out) + at, n, v);
-          else store8u(static_cast<uint16_t*>(g.out) + at, n, v);
+          if constexpr (PART) store8u(part + at, n, v);
+          else put8<OT>(g, at, n, v);
         }
         wave_sync();
         __builtin_amdgcn_sched_barrier(0);
       }
 }
 
-template <class C, Dt OT>
-__global__ __launch_bounds__(C::kThreads, C::kBlocks * C::kWaves / 4) void tile8_kernel(const Args a) {
+template <class C, Dt OT, bool PART>
+__global__ __launch_bounds__(C::kThreads, C::kWaves / 4) void tile8_kernel(const Args a) {
   constexpr bool kExact = OT == Dt::F32;
   __shared__ __attribute__((aligned(16))) uint8_t smem[C::kLds];
-  // one contiguous run of tiles an XCD
+  // one contiguous run of units an XCD
   const int x = (int)blockIdx.x % kXcds;
-  const int end = (int)((int64_t)(x + 1) * a.tiles / kXcds);
-  int tile = (int)((int64_t)x * a.tiles / kXcds) + (int)blockIdx.x / kXcds;
-  if (tile >= end) return;
+  const int end = (int)((int64_t)(x + 1) * a.units / kXcds);
+  int unit = (int)((int64_t)x * a.units / kXcds) + (int)blockIdx.x / kXcds;
+  if (unit >= end) return;
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
@@ -370,7 +403,7 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks * C::kWaves / 4) void tile8
 
   floatx16 acc[C::FM][C::FN];
   Loads<C> next;
-  next.start(a, tile, wave, lane);
+  next.start(a, unit, wave, lane);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
   constexpr int kLoads = Loads<C>::kLoads, kReads = C::FN + 2 * C::FM, kMul = C::FM * C::FN;
   uint32_t qo[4], po[4];
@@ -403,14 +436,17 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks * C::kWaves / 4) void tile8
   }
 
   int cur = 0;
-  for (; tile < end; tile += a.slots) {
+  for (; unit < end; unit += a.slots) {
+    int I, J, part;
+    place_of(a, unit, I, J, part);
+    const int n = a.panels - part * a.per < a.per ? a.panels - part * a.per : a.per;
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int j = 0; j < C::FN; ++j)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    for (int g = 0; g < a.panels; ++g) {
+    for (int g = 0; g < n; ++g) {
       // here, not behind the loads: a branch behind the matrix instructions
       // would let the compiler sink them past it
       next.advance(a, end, wave, lane);
@@ -445,41 +481,127 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks * C::kWaves / 4) void tile8
       });
       sc = nsc;
     }
-    int I, J;
-    place_of(a, tile, I, J);
-    epilogue<C, OT>(a.g, acc, (int64_t)I * C::BM, (int64_t)J * C::BN, wm, wn, renewed(lane), scratch);
+    const Product8& p = product_again();
+    epilogue<C, OT, PART>(p, PART ? a.partials + part * p.M * p.N : nullptr, acc, (int64_t)I * C::BM, (int64_t)J * C::BN, wm,
+                          wn, renewed(lane), scratch);
   }
   // the loads behind the last stage write LDS until they land
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-using Large = Tile<128, 256, 4, 2, 2, 1>;
-using Small = Tile<64, 64, 2, 2, 3, 1>;
+// The parts of a product's sums, in part order.
+template <Dt OT>
+__global__ __launch_bounds__(256) void parts_kernel(const Product8 g, const float* partials, int parts) {
+  const int64_t count = g.M * g.N, at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (at >= count) return;
+  const int n = count - at < 8 ? (int)(count - at) : 8;
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    Raw8<float> o;
+    o.load(partials + p * count + at, n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += o.get(e);
+  }
+  put8<OT>(g, at, n, v);
+}
+
+// Microseconds that tiles of one shape take, from measured BF16 products (K 4096
+// unless stated): a round of 256 workgroups and 1.2 a round, and a panel's
+// time, which grows from `low` to `high` with the CUs at work.
+//   M x N              64x64  64x128  128x128  128x256
+//   64 x 4096           10.6   11.7    16.4     24.8
+//   256 x 4096          11.5   12.8    17.2     26.0
+//   512 x 4096          19.5   14.0    17.6     26.5
+//   1024 x 4096         34.6   24.5    21.0     27.6
+//   2048 x 4096         65.7   43.6    36.5     33.3
+//   256 x 11008         26.7   21.9    17.9     26.7
+//   4096 x 300, K 1000   8.8    6.8     8.3     11.9
+// K in parts (few tiles, long K) adds their FP32 values' way and a launch.
+struct Shape {
+  int BM, BN;
+  double low, high;
+};
+constexpr Shape kShapes[] = {{64, 64, 0.53, 0.60}, {64, 128, 0.60, 0.75}, {128, 128, 0.95, 1.15}, {128, 256, 1.45, 1.90}};
+using Tile0 = Tile<64, 64, 2, 2, 3>;
+using Tile1 = Tile<64, 128, 2, 4, 3>;
+using Tile2 = Tile<128, 128, 4, 2, 2>;
+using Tile3 = Tile<128, 256, 4, 2, 2>;
+
+struct Plan {
+  int shape, parts, per;
+};
+// exact: FP32 outputs, whose P goes in two parts.
+Plan plan(int64_t M, int64_t N, int64_t K, bool exact, bool split) {
+  const int panels = (int)((K + kPanel - 1) / kPanel);
+  Plan best{0, 1, panels};
+  double least = 0.0;
+  for (int i = 0; i < 4; ++i) {
+    const Shape& h = kShapes[i];
+    const int64_t tiles = ((M + h.BM - 1) / h.BM) * ((N + h.BN - 1) / h.BN);
+    for (int wanted : {1, 2, 4, 8}) {
+      if (wanted > 1 && (!split || tiles * wanted > 256 || panels < 2 * wanted)) break;
+      const int per = (panels + wanted - 1) / wanted, parts = (panels + per - 1) / per;
+      const int64_t units = tiles * parts, rounds = (units + 255) / 256;
+      const double t = (exact ? 1.8 : 1.0) * (h.low + (h.high - h.low) * (units < 256 ? units / 256.0 : 1.0));
+      double us = rounds * (1.2 + per * t);
+      if (parts > 1) us += 3.0 + parts * 2e-6 * (double)(M * N);
+      if (least == 0.0 || us < least) {
+        least = us;
+        best = Plan{i, parts, per};
+      }
+    }
+  }
+  return best;
+}
 
 template <class C, Dt OT>
-hipError_t tiled(const Product8& g, hipStream_t s) {
-  Args a{g, (int)((g.K + kPanel - 1) / kPanel), (int)((g.M + C::BM - 1) / C::BM), (int)((g.N + C::BN - 1) / C::BN), 0, 0};
+hipError_t tiled(const Product8& g, const Plan& p, float* ws, hipStream_t s) {
+  Args a{g, (int)((g.K + kPanel - 1) / kPanel), p.per, (int)((g.M + C::BM - 1) / C::BM), (int)((g.N + C::BN - 1) / C::BN), 0, 0, kCusPerXcd, ws};
   a.tiles = a.TM * a.TN;
-  a.slots = C::kBlocks * kCusPerXcd;
-  const int most = (a.tiles + kXcds - 1) / kXcds;
-  tile8_kernel<C, OT><<<dim3((unsigned)(most < a.slots ? most : a.slots) * kXcds), C::kThreads, 0, s>>>(a);
+  a.units = a.tiles * p.parts;
+  const int most = (a.units + kXcds - 1) / kXcds;
+  const dim3 grid((unsigned)(most < a.slots ? most : a.slots) * kXcds);
+  if (p.parts == 1) {
+    tile8_kernel<C, OT, false><<<grid, C::kThreads, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  tile8_kernel<C, OT, true><<<grid, C::kThreads, 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  parts_kernel<OT><<<dim3((unsigned)((g.M * g.N + 2047) / 2048)), 256, 0, s>>>(g, ws, p.parts);
   return hipGetLastError();
 }
 
+// Up to 16 rows of P wait for Q alone (1 x 11008 x 4096 8.0 us; in two groups of
+// 16 rows, 32 of them take 17.5, on tiles 11.0).
+constexpr int64_t kFewRows = 16;
+
 template <Dt OT>
-hipError_t product(const Product8& g, hipStream_t s) {
-  if (g.M <= 16) return few<1, OT>(g, s);
-  if (g.M <= 32) return few<2, OT>(g, s);
-  const int64_t large = ((g.M + 127) / 128) * ((g.N + 255) / 256);
-  return large >= 192 ? tiled<Large, OT>(g, s) : tiled<Small, OT>(g, s);
+hipError_t product(const Product8& g, float* ws, hipStream_t s) {
+  if (g.M <= kFewRows) return few<OT>(g, s);
+  const Plan p = plan(g.M, g.N, g.K, OT == Dt::F32, ws != nullptr);
+  switch (p.shape) {
+    case 0: return tiled<Tile0, OT>(g, p, ws, s);
+    case 1: return tiled<Tile1, OT>(g, p, ws, s);
+    case 2: return tiled<Tile2, OT>(g, p, ws, s);
+    default: return tiled<Tile3, OT>(g, p, ws, s);
+  }
 }
 
 }  // namespace
 
-size_t mx8_workspace(int64_t, int64_t, int64_t) { return 0; }
+size_t mx8_workspace(int64_t M, int64_t N, int64_t K) {
+  if (M <= kFewRows) return 0;
+  const int parts = std::max(plan(M, N, K, false, true).parts, plan(M, N, K, true, true).parts);
+  return parts > 1 ? (size_t)parts * (size_t)(M * N) * sizeof(float) : 0;
+}
 
-hipError_t launch_mx8_product(const Product8& g, void*, hipStream_t s) {
-  return g.ot == Dt::F32 ? product<Dt::F32>(g, s) : product<Dt::BF16>(g, s);
+hipError_t launch_mx8_product(const Product8& g, void* ws, hipStream_t s) {
+  float* w = static_cast<float*>(ws);
+  return g.ot == Dt::F32 ? product<Dt::F32>(g, w, s) : product<Dt::BF16>(g, w, s);
 }
 
 }  // namespace nvfp4
