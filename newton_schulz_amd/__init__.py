@@ -1024,6 +1024,21 @@ def ns_muon_step(Ws, Ms, Gs, coeffs, lr, momentum=0.95, weight_decay=0.0, nester
 # Calls of a few microseconds on the GPU: a tensor made here is not checked
 # again, and a stream or device object is not made where a number serves.
 
+def _new(shape, dtype, dev, stream):
+    """As _empty; strides given, for a call that takes half the time."""
+    stride, strides = 1, []
+    for n in reversed(shape):
+        strides.append(stride)
+        stride *= n
+    strides.reverse()
+    if stream is None:
+        return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
+    if stream.device != dev:
+        raise ValueError(f"a stream of {stream.device} for tensors on {dev}")
+    with torch.cuda.stream(stream):
+        return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
+
+
 def _launch(fn, name, dev, stream, *args):
     """fn(*args, stream) with the tensors' device the current one."""
     if stream is None:
@@ -1046,14 +1061,21 @@ def _need_on(dev, *ts):
     if dev.type != "cuda":
         raise ValueError("tensors must be contiguous device tensors")
     for t in ts:
-        if t is not None:
-            if not t.is_contiguous():
-                raise ValueError("tensors must be contiguous device tensors")
-            if t.device != dev:
-                raise ValueError("tensors must be on one device")
+        if t is not None and not (t.is_contiguous() and t.device == dev):
+            raise ValueError("tensors must be contiguous device tensors, on one device")
+
+
+def _scratch(need, workspace, dev, stream):
+    """The given workspace, or a new one where the call needs any."""
+    if workspace is None:
+        return _new((need,), torch.uint8, dev, stream) if need else None
+    _need(workspace, "workspace", (torch.uint8,), 0)
+    _need_on(dev, workspace)
+    return workspace
 
 
 _TYPES = {torch.float32: NS_F32, torch.bfloat16: NS_BF16}
+_KINDS = tuple(_TYPES)
 
 
 def _type_of(t):
@@ -1101,7 +1123,7 @@ def _blocks(wanted, name, rows, cols, width, dev, stream, written):
         return None
     if wanted is True:
         p = _mx_panels(cols)
-        return (_empty((p, rows, width), torch.uint8, dev, stream), _empty((p, rows, 8), torch.uint8, dev, stream))
+        return (_new((p, rows, width), torch.uint8, dev, stream), _new((p, rows, 8), torch.uint8, dev, stream))
     _need_on(dev, *wanted)
     _need_blocks(wanted, name, rows, cols, width)
     written += wanted
@@ -1119,7 +1141,7 @@ def mx_dropout(x, drop, rng, out=None, stream=None):
     _need_rng(rng, dev)
     given = out
     if out is None:
-        out = _empty((rows, cols), x.dtype, dev, stream)
+        out = _new((rows, cols), x.dtype, dev, stream)
     else:
         _need_on(dev, out)
         _need_like(out, "out", x.shape, (x.dtype,))
@@ -1160,7 +1182,7 @@ def mx_rms_norm(x, weight, eps=1e-6, residual=None, drop=0.0, rng=None, y=None, 
     written = []
     if residual is not None:
         _need_on(dev, residual)
-        _need_like(residual, "residual", shape, _floats())
+        _need_like(residual, "residual", shape, _KINDS)
         a.residual = residual.data_ptr()
     if drop:
         _need_rng(rng, dev)
@@ -1168,7 +1190,7 @@ def mx_rms_norm(x, weight, eps=1e-6, residual=None, drop=0.0, rng=None, y=None, 
     if residual is not None or drop:
         kind = x.dtype if residual is None else residual.dtype
         if h is None:
-            h = _empty(shape, kind, dev, stream)
+            h = _new(shape, kind, dev, stream)
         else:
             _need_on(dev, h)
             _need_like(h, "h", shape, (kind,))
@@ -1186,19 +1208,19 @@ def mx_rms_norm(x, weight, eps=1e-6, residual=None, drop=0.0, rng=None, y=None, 
     if pk is not None:
         a.kept_codes, a.kept_scales = pk[0].data_ptr(), pk[1].data_ptr()
     if y is None and p8 is None and p4 is None and pk is None or y is True:
-        y = _empty(shape, x.dtype, dev, stream)
+        y = _new(shape, x.dtype, dev, stream)
     elif y is False:
         y = None
     elif y is not None:
         _need_on(dev, y)
-        _need_like(y, "y", shape, _floats())
+        _need_like(y, "y", shape, _KINDS)
         written.append(y)
     if y is not None:
         a.y, a.yt = y.data_ptr(), _TYPES[y.dtype]
     if rstd is None or rstd is False:
-        rstd = None if pk is None else _empty((T,), torch.float32, dev, stream)
+        rstd = None if pk is None else _new((T,), torch.float32, dev, stream)
     elif rstd is True:
-        rstd = _empty((T,), torch.float32, dev, stream)
+        rstd = _new((T,), torch.float32, dev, stream)
     else:
         _need_on(dev, rstd)
         _need_like(rstd, "rstd", (T,), (torch.float32,))
@@ -1230,9 +1252,9 @@ def mx_rms_norm_backward(dy, h, rstd, weight, dh=None, drop=0.0, rng=None, out=N
     if dw is None and need_dw and float(beta) != 0.0:
         raise ValueError("beta != 0 adds to a dw that is given")
     _need_on(dev, dy, h, rstd, weight)
-    _need_like(h, "h", shape, _floats())
+    _need_like(h, "h", shape, _KINDS)
     _need_like(rstd, "rstd", (T,), (torch.float32,))
-    _need_like(weight, "weight", (C,), _floats())
+    _need_like(weight, "weight", (C,), _KINDS)
     a = MxNormBackwardArgs()
     a.T, a.C, a.drop, a.beta = T, C, drop, beta
     a.dy, a.h, a.rstd, a.weight = dy.data_ptr(), h.data_ptr(), rstd.data_ptr(), weight.data_ptr()
@@ -1246,7 +1268,7 @@ def mx_rms_norm_backward(dy, h, rstd, weight, dh=None, drop=0.0, rng=None, out=N
         _need_rng(rng, dev)
         a.rng = rng.data_ptr()
     if out is None:
-        out = _empty(shape, h.dtype, dev, stream)
+        out = _new(shape, h.dtype, dev, stream)
     else:
         _need_on(dev, out)
         _need_like(out, "out", shape, (h.dtype,))
@@ -1259,25 +1281,22 @@ def mx_rms_norm_backward(dy, h, rstd, weight, dh=None, drop=0.0, rng=None, out=N
         _need_like(dx, "dx", shape, (x_dtype,))
         written.append(dx)
     elif drop or x_dtype != h.dtype:
-        dx = _empty(shape, x_dtype, dev, stream)
+        dx = _new(shape, x_dtype, dev, stream)
     if dx is not None:
         a.dx, a.xt = dx.data_ptr(), _type_of(dx)
-    ws = (None, 0)
     if not need_dw:
-        dw = None
+        dw = workspace = None
     else:
         if dw is None:
-            dw = _empty((C,), torch.float32, dev, stream)
+            dw = _new((C,), torch.float32, dev, stream)
         else:
             _need_on(dev, dw)
             _need_like(dw, "dw", (C,), (torch.float32,))
             written.append(dw)
         a.dweight = dw.data_ptr()
-        workspace = _mx_workspace(_lib.mx_rms_norm_backward_workspace_bytes(T, C), workspace, dev, stream)
-        if workspace is not None:
-            _need_on(dev, workspace)
-            ws = workspace.data_ptr(), workspace.numel()
-    _launch(_lib.mx_rms_norm_backward, "mx_rms_norm_backward", dev, stream, ctypes.byref(a), *ws)
+        workspace = _scratch(_lib.mx_rms_norm_backward_workspace_bytes(T, C), workspace, dev, stream)
+    _launch(_lib.mx_rms_norm_backward, "mx_rms_norm_backward", dev, stream, ctypes.byref(a),
+            *_ws_args(workspace))
     if written:
         _wrote(written)
     return NormGrads(out, out if dx is None else dx, dw)
@@ -1292,9 +1311,9 @@ def mxfp8_quantize(x, codes=None, scales=None, stream=None):
     p = _mx_panels(cols)
     given = codes, scales
     if codes is None:
-        codes = _empty((p, rows, 256), torch.uint8, dev, stream)
+        codes = _new((p, rows, 256), torch.uint8, dev, stream)
     if scales is None:
-        scales = _empty((p, rows, 8), torch.uint8, dev, stream)
+        scales = _new((p, rows, 8), torch.uint8, dev, stream)
     _need_on(dev, x, codes, scales)
     _need_blocks((codes, scales), "out", rows, cols, 256)
     _launch(_lib.mxfp8_quantize, "mxfp8_quantize", dev, stream, x.data_ptr(), t, rows, cols, codes.data_ptr(),
@@ -1310,9 +1329,9 @@ def mxfp8_dequantize(codes, scales, rows, cols, out_dtype=NS_F32, out=None, stre
     _need_blocks((codes, scales), "in", rows, cols, 256)
     given = out
     if out is None:
-        out = _empty((rows, cols), _out_dtype(out_dtype), dev, stream)
+        out = _new((rows, cols), _out_dtype(out_dtype), dev, stream)
     else:
-        _need(out, "out", _floats(), rows * cols)
+        _need(out, "out", _KINDS, rows * cols)
     _launch(_lib.mxfp8_dequantize, "mxfp8_dequantize", dev, stream, codes.data_ptr(), scales.data_ptr(), rows, cols,
             out.data_ptr(), _TYPES[out.dtype])
     if given is not None:
@@ -1333,25 +1352,22 @@ def mxfp8_gemm(p, q, M, N, K, alpha=1.0, beta=0.0, addend=None, out_dtype=NS_F32
     allocated when none is given."""
     (pc, ps), (qc, qs) = p, q
     dev = pc.device
-    _need_on(dev, pc, ps, qc, qs, addend, out, workspace)
+    _need_on(dev, pc, ps, qc, qs, addend, out)
     _need_blocks(p, "p", M, K, 256)
     _need_mx(qc, qs, "q", N, K)
     given = out
     if out is None:
-        out = _empty((M, N), _out_dtype(out_dtype), dev, stream)
+        out = _new((M, N), _out_dtype(out_dtype), dev, stream)
     else:
-        _need(out, "out", _floats(), M * N)
+        _need(out, "out", _KINDS, M * N)
     add = None
     if beta:
         _need(addend, "addend", (torch.float32,), M * N)
         add = None if addend is None else addend.data_ptr()
-    ws = (None, 0)
     if workspace is not None or split:
-        workspace = _mx_workspace(_lib.mxfp8_gemm_workspace_bytes(M, N, K), workspace, dev, stream)
-        if workspace is not None:
-            ws = workspace.data_ptr(), workspace.numel()
+        workspace = _scratch(_lib.mxfp8_gemm_workspace_bytes(M, N, K), workspace, dev, stream)
     _launch(_lib.mxfp8_gemm, "mxfp8_gemm", dev, stream, pc.data_ptr(), ps.data_ptr(), qc.data_ptr(), qs.data_ptr(),
-            M, N, K, alpha, beta, add, out.data_ptr(), _TYPES[out.dtype], *ws)
+            M, N, K, alpha, beta, add, out.data_ptr(), _TYPES[out.dtype], *_ws_args(workspace))
     if given is not None:
         _wrote((given,))
     return out
@@ -1373,9 +1389,9 @@ def nvfp4_linear(x, w, N, out=None, stream=None):
     _need(sg, "global_scale", (torch.float32,), 1)
     given = out
     if out is None:
-        out = _empty((T, N), x.dtype, dev, stream)
+        out = _new((T, N), x.dtype, dev, stream)
     else:
-        _need(out, "out", _floats(), T * N)
+        _need(out, "out", _KINDS, T * N)
     _launch(_lib.nvfp4_linear, "nvfp4_linear", dev, stream, x.data_ptr(), t, T, K, codes.data_ptr(),
             scales.data_ptr(), sg.data_ptr(), N, out.data_ptr(), _TYPES[out.dtype])
     if given is not None:
