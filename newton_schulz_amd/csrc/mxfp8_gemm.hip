@@ -489,6 +489,224 @@ __global__ __launch_bounds__(C::kThreads, C::kWaves / 4) void tile8_kernel(const
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
+// ---- large tiles ----------------------------------------------------------------
+// 256 x 256 a workgroup, eight waves of 64 x 128: two thirds of the bytes from
+// LDS an instruction that the tiles above read, and three quarters of the bytes
+// into it.  LDS holds two panels of Q's rows and scales, and of P's rows two
+// halves of a panel (blocks 4 u to 4 u + 3, a line of 128 bytes a row), which
+// follow each other: while half u is multiplied, the other half lands.  Step s
+// of a half multiplies blocks 4 u + 2 s (slot 0) and 4 u + 2 s + 1 (slot 1).
+namespace wide {
+constexpr int B = 256, kWaves = 8, WN = 2, FM = 2, FN = 4;
+constexpr int kHalf = B * 128, kQ = 2 * kHalf, kPanelQ = B * 128, kScales = kQ + 2 * kPanelQ, kPanelS = 2 * B * 8;
+constexpr int kScratch = 2304, kLds = kScales + 2 * kPanelS + kWaves * kScratch;
+constexpr int kLoads = 4, kScaleLoads = 2;       // a wave's of a half of P or a panel of Q, and of a panel's scales
+
+// The next panel of a workgroup's stream of tiles: of P's rows, or of Q's rows and
+// both operands' scales.  Behind the last panel the same again.
+template <bool P>
+struct Cursor {
+  int t, g;
+  const uint8_t *data, *s;
+  uint32_t code[kLoads], scale[P ? 1 : kScaleLoads];
+
+  __device__ __forceinline__ void start(const Args& a, int tile, int wave, int lane) {
+    int I, J, part;
+    place_of(a, tile, I, J, part);
+    t = tile;
+    g = 0;
+    const int64_t m0 = (int64_t)I * B, n0 = (int64_t)J * B;
+    // rows past an operand's end: its last row, into values that are not written
+    const int pm = (int)(a.g.M - m0 < B ? a.g.M - m0 : B) - 1, qm = (int)(a.g.N - n0 < B ? a.g.N - n0 : B) - 1;
+    data = P ? a.g.p + m0 * kPanelBytes8 : a.g.q + n0 * kPanelBytes;
+    const int last = P ? pm : qm;
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const int r = 8 * (wave * kLoads + k) + (lane >> 3);
+      code[k] = (uint32_t)(r < last ? r : last) * (P ? kPanelBytes8 : kPanelBytes) + 16u * (uint32_t)((lane & 7) ^ swizzle(r));
+    }
+    if constexpr (!P) {
+      // groups of 32 rows: P's eight, then Q's
+      const int slast = wave < 4 ? pm : qm;
+      s = wave < 4 ? a.g.p_scales + m0 * kPanelScales : a.g.q_scales + n0 * kPanelScales;
+#pragma unroll
+      for (int k = 0; k < kScaleLoads; ++k) {
+        const int r = 32 * ((wave & 3) * kScaleLoads + k) + (lane >> 1);
+        scale[k] = (uint32_t)(r < slast ? r : slast) * kPanelScales + 4u * (uint32_t)(lane & 1);
+      }
+    }
+  }
+  __device__ __forceinline__ void advance(const Args& a, int end, int wave, int lane) {
+    if (g + 1 < a.panels) {
+      ++g;
+      data += P ? a.g.M * kPanelBytes8 : a.g.N * kPanelBytes;
+      if constexpr (!P) s += (wave < 4 ? a.g.M : a.g.N) * kPanelScales;
+    } else if (t + a.slots < end) {
+      start(a, t + a.slots, wave, renewed(lane));
+    }
+  }
+  // Load number k of half u of P, or of Q's panel and the scales into buffer b.
+  __device__ __forceinline__ void load(uint32_t lds0, int ub, int wave, int k) const {
+    if constexpr (P) dma16(data + 128 * ub, code[k], lds0 + (uint32_t)(ub * kHalf + (wave * kLoads + k) * 1024));
+    else if (k < kLoads) dma16(data, code[k], lds0 + (uint32_t)(kQ + ub * kPanelQ + (wave * kLoads + k) * 1024));
+    else dma4(s, scale[k - kLoads], lds0 + (uint32_t)(kScales + ub * kPanelS + (wave * kScaleLoads + k - kLoads) * 256));
+  }
+};
+
+struct Blocks {                          // of a wave, for the epilogue
+  static constexpr int FM = wide::FM, FN = wide::FN;
+};
+struct Frags {
+  intx4 q[FN], p[FM][2];
+};
+
+template <bool EXACT, int S, class F>
+__device__ __forceinline__ void step(const Frags& f, const uint32_t (&sc)[FN + FM], floatx16 (&acc)[FM][FN], F&& between) {
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const intx8 x = __builtin_shufflevector(f.p[i][0], f.p[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+    intx8 high, low;
+    if constexpr (EXACT) two_parts(x, high, low);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      if constexpr (EXACT) {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(high, four_bits(f.q[j]), acc[i][j], 0, 4, 2 * S, (int)sc[FN + i], 2 * S, (int)sc[j]);
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(low, four_bits(f.q[j]), acc[i][j], 0, 4, 2 * S, (int)sc[FN + i], 2 * S, (int)sc[j]);
+      } else {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, four_bits(f.q[j]), acc[i][j], 0, 4, 2 * S, (int)sc[FN + i], 2 * S, (int)sc[j]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      between(i * FN + j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+template <Dt OT>
+__global__ __launch_bounds__(64 * kWaves, 2) void wide8_kernel(const Args a) {
+  constexpr bool kExact = OT == Dt::F32;
+  constexpr int kReads = FN + 2 * FM, kMul = FM * FN;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
+  const int x = (int)blockIdx.x % kXcds;
+  const int end = (int)((int64_t)(x + 1) * a.units / kXcds);
+  int tile = (int)((int64_t)x * a.units / kXcds) + (int)blockIdx.x / kXcds;
+  if (tile >= end) return;
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+  floatx16 acc[FM][FN];
+  Frags f0, f1;
+  uint32_t sc[FN + FM];
+  // a lane's chunks: of Q 4 u + 2 s + h; of P 4 s + h (slot 0) and 4 s + 2 + h
+  const uint32_t line = (uint32_t)(r * 128), sw = (uint32_t)swizzle(r);
+  auto read_frag = [&](int u, int s, int b, int k, Frags& f) {
+    if (k < FN) {
+      f.q[k] = *reinterpret_cast<const intx4*>(smem + kQ + b * kPanelQ + (wn * FN + k) * 4096 + line + 16 * ((4 * u + 2 * s + h) ^ sw));
+    } else {
+      const int i = (k - FN) >> 1, slot = (k - FN) & 1;
+      f.p[i][slot] = *reinterpret_cast<const intx4*>(smem + u * kHalf + (wm * FM + i) * 4096 + line + 16 * ((4 * s + 2 * slot + h) ^ sw));
+    }
+  };
+  // bytes 2 s of what a lane gets are its slot's scales in step s of half u
+  auto read_scale = [&](int u, int b, int k) {
+    const int row = (k < FN ? B + (wn * FN + k) * 32 : (wm * FM + k - FN) * 32) + r;
+    return *reinterpret_cast<const uint32_t*>(smem + kScales + b * kPanelS + row * 8 + 4 * u) >> (8 * h);
+  };
+  Cursor<true> np;
+  Cursor<false> nq;
+  np.start(a, tile, wave, lane);
+  nq.start(a, tile, wave, lane);
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) np.load(lds0, 0, wave, k);
+#pragma unroll
+  for (int k = 0; k < kLoads + kScaleLoads; ++k) nq.load(lds0, 0, wave, k);
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) np.load(lds0, 1, wave, k);
+  nq.advance(a, end, wave, lane);
+#pragma unroll
+  for (int k = 0; k < kLoads + kScaleLoads; ++k) nq.load(lds0, 1, wave, k);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads + kScaleLoads) : "memory");
+  all_waves();
+#pragma unroll
+  for (int k = 0; k < kReads; ++k) {
+    if (k < FN + FM) sc[k] = read_scale(0, 0, k);
+    read_frag(0, 0, 0, k, f0);
+  }
+  int b = 0;                              // buffer of this panel's Q and scales
+  for (; tile < end; tile += a.slots) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    for (int g = 0; g < a.panels; ++g) {
+      np.advance(a, end, wave, lane);     // to the next panel
+      nq.advance(a, end, wave, lane);     // to the one behind it
+      uint32_t nsc[FN + FM];
+      step<kExact, 0>(f0, sc, acc, [&](int k) {
+#pragma unroll
+        for (int n = share(kReads, k, kMul); n < share(kReads, k + 1, kMul); ++n) read_frag(0, 1, b, n, f1);
+      });
+      // every read of P's first half has returned, in all waves, and its second
+      // half has landed (behind it only the next panel's Q and scales are under way)
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads + kScaleLoads) : "memory");
+      all_waves();
+      step<kExact, 1>(f1, sc, acc, [&](int k) {
+#pragma unroll
+        for (int n = share(kReads, k, kMul); n < share(kReads, k + 1, kMul); ++n) {
+          if (n < FN + FM) nsc[n] = read_scale(1, b, n);
+          read_frag(1, 0, b, n, f0);
+        }
+#pragma unroll
+        for (int n = share(kLoads, k, kMul); n < share(kLoads, k + 1, kMul); ++n) np.load(lds0, 0, wave, n);
+      });
+      step<kExact, 0>(f0, nsc, acc, [&](int k) {
+#pragma unroll
+        for (int n = share(kReads, k, kMul); n < share(kReads, k + 1, kMul); ++n) read_frag(1, 1, b, n, f1);
+      });
+      // every read of this panel has returned, and the next one's first half of
+      // P, its Q and its scales have landed
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      all_waves();
+      step<kExact, 1>(f1, nsc, acc, [&](int k) {
+#pragma unroll
+        for (int n = share(kReads, k, kMul); n < share(kReads, k + 1, kMul); ++n) {
+          if (n < FN + FM) sc[n] = read_scale(0, b ^ 1, n);
+          read_frag(0, 0, b ^ 1, n, f0);
+        }
+        constexpr int kAll = 2 * kLoads + kScaleLoads;
+#pragma unroll
+        for (int n = share(kAll, k, kMul); n < share(kAll, k + 1, kMul); ++n) {
+          if (n < kLoads) np.load(lds0, 1, wave, n);
+          else nq.load(lds0, b, wave, n - kLoads);
+        }
+      });
+      b ^= 1;
+    }
+    int I, J, part;
+    place_of(a, tile, I, J, part);
+    epilogue<Blocks, OT, false>(product_again(), nullptr, acc, (int64_t)I * B, (int64_t)J * B, wm, wn, renewed(lane),
+                               smem + kScales + 2 * kPanelS + wave * kScratch);
+  }
+  // the loads behind the last panel write LDS until they land
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+template <Dt OT>
+hipError_t launch(const Product8& g, hipStream_t s) {
+  const int panels = (int)((g.K + kPanel - 1) / kPanel);
+  Args a{g, panels, panels, (int)((g.M + B - 1) / B), (int)((g.N + B - 1) / B), 0, 0, kCusPerXcd, nullptr};
+  a.tiles = a.units = a.TM * a.TN;
+  const int most = (a.units + kXcds - 1) / kXcds;
+  wide8_kernel<OT><<<dim3((unsigned)(most < a.slots ? most : a.slots) * kXcds), 64 * kWaves, 0, s>>>(a);
+  return hipGetLastError();
+}
+}  // namespace wide
+
 // The parts of a product's sums, in part order.
 template <Dt OT>
 __global__ __launch_bounds__(256) void parts_kernel(const Product8 g, const float* partials, int parts) {
@@ -511,42 +729,48 @@ __global__ __launch_bounds__(256) void parts_kernel(const Product8 g, const floa
 // Microseconds that tiles of one shape take, from measured BF16 products (K 4096
 // unless stated): a round of 256 workgroups and 1.2 a round, and a panel's
 // time, which grows from `low` to `high` with the CUs at work.
-//   M x N              64x64  64x128  128x128  128x256
+//   M x N              64x64  64x128  128x128  128x256  256x256
 //   64 x 4096           10.6   11.7    16.4     24.8
 //   256 x 4096          11.5   12.8    17.2     26.0
 //   512 x 4096          19.5   14.0    17.6     26.5
 //   1024 x 4096         34.6   24.5    21.0     27.6
-//   2048 x 4096         65.7   43.6    36.5     33.3
+//   2048 x 4096         65.7   43.6    36.5     31.5     42.8
 //   256 x 11008         26.7   21.9    17.9     26.7
 //   4096 x 300, K 1000   8.8    6.8     8.3     11.9
+//   4096 x 4096                                 59.0     52.2
+//   8192 x 4096                                114       98.8
 // K in parts (few tiles, long K) adds their FP32 values' way and a launch.
+// FP32 outputs, whose P goes in two parts, take 1.8 times as long a panel.
 struct Shape {
   int BM, BN;
   double low, high;
 };
-constexpr Shape kShapes[] = {{64, 64, 0.53, 0.60}, {64, 128, 0.60, 0.75}, {128, 128, 0.95, 1.15}, {128, 256, 1.45, 1.90}};
+constexpr int kWide = 4;
+constexpr Shape kShapes[] = {{64, 64, 0.53, 0.60}, {64, 128, 0.60, 0.75}, {128, 128, 0.95, 1.15}, {128, 256, 1.45, 1.90}, {256, 256, 2.40, 3.05}};
 using Tile0 = Tile<64, 64, 2, 2, 3>;
 using Tile1 = Tile<64, 128, 2, 4, 3>;
 using Tile2 = Tile<128, 128, 4, 2, 2>;
 using Tile3 = Tile<128, 256, 4, 2, 2>;
 
+double rounds_cost(const Shape& h, int64_t units, int per, bool exact) {
+  const double t = (exact ? 1.8 : 1.0) * (h.low + (h.high - h.low) * (units < 256 ? units / 256.0 : 1.0));
+  return ((units + 255) / 256) * (1.2 + per * t);
+}
+
 struct Plan {
   int shape, parts, per;
 };
-// exact: FP32 outputs, whose P goes in two parts.
 Plan plan(int64_t M, int64_t N, int64_t K, bool exact, bool split) {
   const int panels = (int)((K + kPanel - 1) / kPanel);
   Plan best{0, 1, panels};
   double least = 0.0;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i <= kWide; ++i) {
     const Shape& h = kShapes[i];
     const int64_t tiles = ((M + h.BM - 1) / h.BM) * ((N + h.BN - 1) / h.BN);
     for (int wanted : {1, 2, 4, 8}) {
-      if (wanted > 1 && (!split || tiles * wanted > 256 || panels < 2 * wanted)) break;
+      if (wanted > 1 && (!split || i == kWide || tiles * wanted > 256 || panels < 2 * wanted)) break;
       const int per = (panels + wanted - 1) / wanted, parts = (panels + per - 1) / per;
-      const int64_t units = tiles * parts, rounds = (units + 255) / 256;
-      const double t = (exact ? 1.8 : 1.0) * (h.low + (h.high - h.low) * (units < 256 ? units / 256.0 : 1.0));
-      double us = rounds * (1.2 + per * t);
+      double us = rounds_cost(h, tiles * parts, per, exact);
       if (parts > 1) us += 3.0 + parts * 2e-6 * (double)(M * N);
       if (least == 0.0 || us < least) {
         least = us;
@@ -574,7 +798,6 @@ hipError_t tiled(const Product8& g, const Plan& p, float* ws, hipStream_t s) {
   parts_kernel<OT><<<dim3((unsigned)((g.M * g.N + 2047) / 2048)), 256, 0, s>>>(g, ws, p.parts);
   return hipGetLastError();
 }
-
 // Up to 16 rows of P wait for Q alone (1 x 11008 x 4096 8.0 us; in two groups of
 // 16 rows, 32 of them take 17.5, on tiles 11.0).
 constexpr int64_t kFewRows = 16;
@@ -587,7 +810,8 @@ hipError_t product(const Product8& g, float* ws, hipStream_t s) {
     case 0: return tiled<Tile0, OT>(g, p, ws, s);
     case 1: return tiled<Tile1, OT>(g, p, ws, s);
     case 2: return tiled<Tile2, OT>(g, p, ws, s);
-    default: return tiled<Tile3, OT>(g, p, ws, s);
+    case 3: return tiled<Tile3, OT>(g, p, ws, s);
+    default: return wide::launch<OT>(g, s);
   }
 }
 
