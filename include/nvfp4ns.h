@@ -542,7 +542,7 @@ ns_status ns_muon_step(int count, void* const* W, ns_dtype wt, void* const* M, n
  * at least P = floor(65536 p + 1/2), and what is kept is multiplied by
  * 65536 / (65536 - P) (in FP32), so that means are kept exactly.  The mask is
  * never stored: a backward pass draws the same bits again.  0 <= p < 1 with
- * P < 65536; p = 0 keeps everything and draws nothing.
+ * P < 65536; p = 0 keeps everything.
  *
  * Dimensions are 1 .. 2^24, of any parity, a matrix up to 2^36 elements.
  * ====================================================================== */
@@ -640,7 +640,11 @@ ns_status mxfp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t 
 /*
  * mxfp8_gemm — out = beta * addend + alpha * P Q^T, P [M][K] in MXFP8
  * (activations) and Q [N][K] in MXFP4 (weights), both along K; arguments as
- * mxfp4_gemm.  Products are exact and accumulated in FP32.
+ * mxfp4_gemm.  FP32 outputs, and all of up to 16 rows: products are exact and
+ * accumulated in FP32.  BF16 outputs of more rows: the matrix instruction adds
+ * the products of eight neighbours of K in a window that ends 2^13 below the
+ * largest one's leading bit, so that each of the others loses up to 2^-13 of
+ * that; sums of these are FP32.
  *   ws       device scratch of mxfp8_gemm_workspace_bytes(), or NULL with
  *            ws_bytes 0 (slower where a long K feeds few outputs).
  */

@@ -1346,7 +1346,9 @@ def mxfp8_gemm_workspace_bytes(M, N, K):
 def mxfp8_gemm(p, q, M, N, K, alpha=1.0, beta=0.0, addend=None, out_dtype=NS_F32, out=None, workspace=None,
                split=True, stream=None):
     """out = beta*addend + alpha*(P Q^T) for p = (codes, scales) in MXFP8 and q in
-    MXFP4, both along K: 8-bit activations by 4-bit weights.
+    MXFP4, both along K: 8-bit activations by 4-bit weights.  float32 results
+    keep every bit up to their FP32 sum; in bfloat16 ones a product loses up to
+    2^-13 of the largest among its eight neighbours along K.
 
     With split=True (default) a workspace of mxfp8_gemm_workspace_bytes() is
     allocated when none is given."""

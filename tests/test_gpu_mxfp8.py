@@ -135,14 +135,44 @@ def test_blocks_of_far_scales():
     check_product(ns.mxfp8_gemm(p, q, M, N, K), P, Q, K)
 
 
-def test_nan_blocks():
-    M, N, K = 40, 50, 300
+@pytest.mark.parametrize("M,N,K", [(40, 50, 300), (5, 50, 300), (300, 700, 300), (4352, 4352, 300)])
+def test_nan_blocks(M, N, K):
     x, w = heavy(7, M, K), heavy(8, N, K)
     x[3, 290], w[11, 5] = np.nan, np.inf
     got = host(ns.mxfp8_gemm(ns.mxfp8_quantize(torch.from_numpy(x).to(DEV)), ns.mxfp4_quantize(torch.from_numpy(w).to(DEV)), M, N, K))
     bad = np.zeros((M, N), bool)
     bad[3], bad[:, 11] = True, True
     assert np.array_equal(np.isnan(got), bad)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_parts_in_graphs_and_streams(dtype):
+    """Products that pass through a workspace: the same on several streams at
+    once, in two graphs replayed in turn, and without one within the bounds."""
+    M, N, K = 64, 320, 8192
+    assert ns.mxfp8_gemm_workspace_bytes(M, N, K) > 0
+    ot = ns.NS_F32 if dtype == "f32" else ns.NS_BF16
+    ops = [operands(s, M, N, K) for s in (1, 2, 3)]
+    want = [ns.mxfp8_gemm(p, q, M, N, K, out_dtype=ot) for p, q, _, _ in ops]
+    for w, (p, q, P, Q) in zip(want, ops):
+        check_product(w, P, Q, K, dtype=TYPES[dtype])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ops]
+    for _ in range(3):
+        got = [ns.mxfp8_gemm(p, q, M, N, K, out_dtype=ot, stream=s) for (p, q, _, _), s in zip(ops, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs, outs = [], []
+    for p, q, _, _ in ops[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(ns.mxfp8_gemm(p, q, M, N, K, out_dtype=ot))
+        graphs.append(g)
+    for k in range(4):
+        graphs[k % 2].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[k % 2], want[k % 2])
+        check_product(ns.mxfp8_gemm(*ops[2][:2], M, N, K, out_dtype=ot), ops[2][2], ops[2][3], K, dtype=TYPES[dtype])
 
 
 def test_large_products_sampled():
@@ -161,6 +191,27 @@ def test_large_products_sampled():
     # the window's share of a sum, and the output's half step
     lost = 7 * 2.0 ** -13 * sum((P[:, k:k + 8].abs().amax(1)[:, None] * Q[:, k:k + 8].abs().amax(1) for k in range(0, K, 8)))
     assert bool(((b.double() - P @ Q.T.contiguous()).abs() <= bound + lost + 2.0 ** -8 * b.double().abs()).all())
+
+
+@pytest.mark.parametrize("M,N,K,dtype", [(4352, 4352, 256, "bf16"), (4100, 4203, 300, "f32"), (16400, 2300, 130, "bf16"),
+                                         (8192, 4097, 520, "bf16"), (3000, 5003, 770, "f32")])
+def test_large_ragged_products(M, N, K, dtype):
+    """More large tiles than CUs, odd pitches, one panel a tile, an addend; every
+    value is written, within the bounds of check_product."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(M + N)
+    p = ns.mxfp8_quantize(torch.randn(M, K, generator=g, device=DEV))
+    q = ns.mxfp4_quantize(torch.randn(N, K, generator=g, device=DEV))
+    add = torch.randn(M, N, generator=g, device=DEV)
+    P, Q = ns.mxfp8_dequantize(*p, M, K).double(), ns.mxfp4_dequantize(*q, N, K).double()
+    out = torch.full((M, N), float("nan"), dtype=TYPES[dtype], device=DEV)
+    got = ns.mxfp8_gemm(p, q, M, N, K, alpha=0.5, beta=2.0, addend=add, out=out).double()
+    want = 0.5 * (P @ Q.T.contiguous()) + 2.0 * add.double()
+    bound = (K + 2) * U * (0.5 * (P.abs() @ Q.abs().T.contiguous()) + 2.0 * add.double().abs())
+    if dtype == "bf16":       # the window's share, and the output's half step
+        lost = sum(P[:, k:k + 8].abs().amax(1)[:, None] * Q[:, k:k + 8].abs().amax(1) for k in range(0, K, 8))
+        bound = bound + 0.5 * 7 * 2.0 ** -13 * lost + 2.0 ** -8 * (want.abs() + bound)
+    assert bool(((got - want).abs() <= bound + U * want.abs()).all())
 
 
 def test_small_neighbours_of_large_values():

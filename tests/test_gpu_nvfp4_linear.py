@@ -51,6 +51,48 @@ def test_linear(T, N, K, dtype):
     check(out, x, w, other)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N,K", [(1, 21, 70016), (2, 35, 40032), (2, 18, 2080), (3, 20, 33000 // 16 * 16)])
+def test_long_rows(T, N, K, dtype):
+    """More of K than LDS holds at a time, steps that end inside a wave."""
+    op, w = weights(N + K, N, K)
+    x = torch.from_numpy(np.random.default_rng(T).standard_t(3, (T, K)).astype(np.float32)).to(TYPES[dtype]).to(DEV)
+    check(ns.nvfp4_linear(x, op, N), x, w, x.dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_two_tokens_element_by_element(dtype):
+    N, K = 18, 4128
+    op, w = weights(5, N, K)
+    for k in list(range(0, 66)) + list(range(2040, 2060)) + list(range(4090, K)):
+        x = torch.zeros(2, K, device=DEV)
+        x[0, k], x[1, K - 1 - k] = 3.0, -0.25
+        y = host(ns.nvfp4_linear(x.to(TYPES[dtype]), op, N, out=torch.empty(2, N, device=DEV)))
+        want = host(x).astype(np.float64) @ w.T
+        assert np.all(np.abs(y - want) <= 3 * U * np.abs(want))
+
+
+def test_graph_and_streams():
+    op, _ = weights(7, 100, 512)
+    xs = [torch.randn(T, 512, device=DEV).bfloat16() for T in (1, 2, 5, 40)]
+    want = [ns.nvfp4_linear(x, op, 100) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [ns.nvfp4_linear(x, op, 100, stream=s) for x, s in zip(xs, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [ns.nvfp4_linear(x, op, 100) for x in xs]
+    for _ in range(3):
+        for x in xs:
+            x.normal_()
+        want = [ns.nvfp4_linear(x, op, 100) for x in xs]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
 def test_weights_of_the_quantizer():
     W = torch.randn(64, 320, device=DEV)
     op = ns.nvfp4_quantize(W)
