@@ -154,34 +154,26 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_kernel(const NormF
 // each column's 128-byte line leaves whole.
 constexpr int kTileCols = 128;
 
-__device__ __forceinline__ void encode_block(const float (&v)[32], uint4& c, uint32_t& byte) {
-  uint32_t a = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) a = umax(a, mag_bits(v[i]));
-  byte = scale_byte(a);
-  uint32_t w[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = v[8 * q + i];
-    w[q] = encode8(e, byte);
+// Two neighbouring columns of a row, as they lie in memory.
+template <class H> struct Two;
+template <> struct Two<float> {
+  float2 v;
+  template <bool VEC> __device__ __forceinline__ void load(const float* p, int n) {
+    if constexpr (VEC) v = *reinterpret_cast<const float2*>(p);
+    else v = make_float2(p[0], n > 1 ? p[1] : 0.0f);
   }
-  c = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-template <bool VEC>
-__device__ __forceinline__ float2 load_two(const float* p, int n) {
-  if constexpr (VEC) return *reinterpret_cast<const float2*>(p);
-  else return make_float2(p[0], n > 1 ? p[1] : 0.0f);
-}
-template <bool VEC>
-__device__ __forceinline__ float2 load_two(const uint16_t* p, int n) {
+  __device__ __forceinline__ void clear() { v = make_float2(0.0f, 0.0f); }
+  __device__ __forceinline__ float get(int j) const { return j ? v.y : v.x; }
+};
+template <> struct Two<uint16_t> {
   uint32_t v;
-  if constexpr (VEC) v = *reinterpret_cast<const uint32_t*>(p);
-  else v = (uint32_t)p[0] | (n > 1 ? (uint32_t)p[1] << 16 : 0u);
-  return make_float2(bf16_lo(v), bf16_hi(v));
-}
+  template <bool VEC> __device__ __forceinline__ void load(const uint16_t* p, int n) {
+    if constexpr (VEC) v = *reinterpret_cast<const uint32_t*>(p);
+    else v = (uint32_t)p[0] | (n > 1 ? (uint32_t)p[1] << 16 : 0u);
+  }
+  __device__ __forceinline__ void clear() { v = 0; }
+  __device__ __forceinline__ float get(int j) const { return j ? bf16_hi(v) : bf16_lo(v); }
+};
 
 template <class H, bool VEC>
 __global__ __launch_bounds__(512) void norm_cols_kernel(const H* h, const float* rstd, const void* weight, Dt wt, int64_t T,
@@ -194,33 +186,62 @@ __global__ __launch_bounds__(512) void norm_cols_kernel(const H* h, const float*
   const int64_t t0 = g * kPanel + 32 * wave;
   const int64_t c = c0 + 2 * lane;
   const int n = c < C ? (C - c < 2 ? 1 : 2) : 0;
-  float2 w = make_float2(0.0f, 0.0f);
-  if (n) w = wt == Dt::F32 ? load_two<false>(static_cast<const float*>(weight) + c, n) : load_two<false>(static_cast<const uint16_t*>(weight) + c, n);
-  float2 u[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) u[i] = t0 + i < T && n ? load_two<VEC>(h + (t0 + i) * C + c, n) : make_float2(0.0f, 0.0f);
-  float v0[32], v1[32];
+  float w[2] = {0.0f, 0.0f};
+  if (n) {
+    if (wt == Dt::F32) {
+      Two<float> t;
+      t.template load<false>(static_cast<const float*>(weight) + c, n);
+      w[0] = t.get(0);
+      w[1] = t.get(1);
+    } else {
+      Two<uint16_t> t;
+      t.template load<false>(static_cast<const uint16_t*>(weight) + c, n);
+      w[0] = t.get(0);
+      w[1] = t.get(1);
+    }
+  }
+  Two<H> u[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    // behind the last token 0
-    const float r = t0 + i < T ? rstd[t0 + i] : 0.0f;
-    v0[i] = u[i].x * r * w.x;
-    v1[i] = u[i].y * r * w.y;
+    if (t0 + i < T && n) u[i].template load<VEC>(h + (t0 + i) * C + c, n);
+    else u[i].clear();
   }
-  uint4 k0, k1;
-  uint32_t b0, b1;
-  encode_block(v0, k0, b0);
-  encode_block(v1, k1, b1);
+  float r[32];                                   // the tokens' rstd, 0 behind the last
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = t0 + i < T ? rstd[t0 + i] : 0.0f;
+  // y is computed for its maximum and again for its codes: kept in between, its
+  // 64 values a lane cost more than 128 products do (8192 x 4096 BF16: 28.7 us
+  // kept, 18 so)
+  uint4 k[2];
+  uint32_t b[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) top = umax(top, mag_bits(u[i].get(j) * r[i] * w[j]));
+    b[j] = scale_byte(top);
+    uint32_t q[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      float e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = u[8 * s + i].get(j) * r[8 * s + i] * w[j];
+      q[s] = encode8(e, b[j]);
+    }
+    k[j] = make_uint4(q[0], q[1], q[2], q[3]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   // column j's line: chunk `wave` at position wave ^ (j / 2 % 8), so that the
   // 64 lanes' 16-byte writes spread over the banks
   const int pos = 16 * (wave ^ (lane & 7));
-  *reinterpret_cast<uint4*>(lc + (2 * lane) * 128 + pos) = k0;
-  *reinterpret_cast<uint4*>(lc + (2 * lane + 1) * 128 + pos) = k1;
-  ls[(2 * lane) * 8 + wave] = (uint8_t)b0;
-  ls[(2 * lane + 1) * 8 + wave] = (uint8_t)b1;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    *reinterpret_cast<uint4*>(lc + (2 * lane + j) * 128 + pos) = k[j];
+    ls[(2 * lane + j) * 8 + wave] = (uint8_t)b[j];
+  }
   __syncthreads();
-  for (int k = tid; k < kTileCols * 8; k += 512) {
-    const int j = k >> 3, p = k & 7;             // column, 16-byte position
+  for (int i = tid; i < kTileCols * 8; i += 512) {
+    const int j = i >> 3, p = i & 7;             // column, 16-byte position
     if (c0 + j < C)
       *reinterpret_cast<uint4*>(codes + (g * C + c0 + j) * kPanelBytes + 16 * (p ^ ((j >> 1) & 7))) =
           *reinterpret_cast<const uint4*>(lc + j * 128 + 16 * p);

@@ -92,7 +92,10 @@ __device__ __forceinline__ void put1(void* y, int64_t at, float v) {
 
 // ---- one or two tokens --------------------------------------------------------
 constexpr int kStep = 64 * 32;            // elements of a row that a wave takes at a time
-constexpr int kGemvWaves = 8, kGemvRows = 2;   // rows of W a wave
+constexpr int kGemvWaves = 8;
+// Rows of W a wave: of BF16 x one (11008 x 4096 7.9 us, two 8.1, four 8.25; 4096 x
+// 11008 7.6, 7.8, 9.9), of FP32 x two, which share the reads of its three parts.
+template <class X> constexpr int kGemvRows = Parts<X>::kParts == 1 ? 1 : 2;
 constexpr int kGemvLds = 65536;           // bytes of x a workgroup holds at most
 
 // The sum over a wave's lanes, in every lane.
@@ -124,7 +127,7 @@ __device__ __forceinline__ float dot8(uint32_t c, wordx4 x, float sum) {
 // lanes reading their j-th hit distinct banks.
 template <class X, int T, Dt OT>
 __global__ __launch_bounds__(64 * kGemvWaves) void gemv_kernel(const Nv a, int span) {
-  constexpr int P = Parts<X>::kParts, R = kGemvRows;
+  constexpr int P = Parts<X>::kParts, R = kGemvRows<X>;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   wordx4* xs = reinterpret_cast<wordx4*>(lds);
   const int lane = threadIdx.x & 63;
@@ -350,7 +353,7 @@ hipError_t gemv(Nv a, hipStream_t s) {
   constexpr int kBytes = 2 * T * Parts<X>::kParts;           // of LDS an element of K
   const int64_t most = kGemvLds / kBytes / kStep * kStep, all = (a.K + kStep - 1) / kStep * kStep;
   const int span = (int)(all < most ? all : most);
-  a.groups = (a.N + kGemvWaves * kGemvRows - 1) / (kGemvWaves * kGemvRows);
+  a.groups = (a.N + kGemvWaves * kGemvRows<X> - 1) / (kGemvWaves * kGemvRows<X>);
   gemv_kernel<X, T, OT><<<dim3((unsigned)a.groups), 64 * kGemvWaves, (size_t)span * kBytes, s>>>(a, span);
   return hipGetLastError();
 }
