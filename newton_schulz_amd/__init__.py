@@ -1024,13 +1024,8 @@ def ns_muon_step(Ws, Ms, Gs, coeffs, lr, momentum=0.95, weight_decay=0.0, nester
 # Calls of a few microseconds on the GPU: a tensor made here is not checked
 # again, and a stream or device object is not made where a number serves.
 
-def _new(shape, dtype, dev, stream):
-    """As _empty; strides given, for a call that takes half the time."""
-    stride, strides = 1, []
-    for n in reversed(shape):
-        strides.append(stride)
-        stride *= n
-    strides.reverse()
+def _new(shape, strides, dtype, dev, stream):
+    """As _empty; with its strides given, a tensor takes half the time."""
     if stream is None:
         return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
     if stream.device != dev:
@@ -1068,7 +1063,7 @@ def _need_on(dev, *ts):
 def _scratch(need, workspace, dev, stream):
     """The given workspace, or a new one where the call needs any."""
     if workspace is None:
-        return _new((need,), torch.uint8, dev, stream) if need else None
+        return _new((need,), (1,), torch.uint8, dev, stream) if need else None
     _need(workspace, "workspace", (torch.uint8,), 0)
     _need_on(dev, workspace)
     return workspace
@@ -1123,7 +1118,8 @@ def _blocks(wanted, name, rows, cols, width, dev, stream, written):
         return None
     if wanted is True:
         p = _mx_panels(cols)
-        return (_new((p, rows, width), torch.uint8, dev, stream), _new((p, rows, 8), torch.uint8, dev, stream))
+        return (_new((p, rows, width), (rows * width, width, 1), torch.uint8, dev, stream),
+                _new((p, rows, 8), (rows * 8, 8, 1), torch.uint8, dev, stream))
     _need_on(dev, *wanted)
     _need_blocks(wanted, name, rows, cols, width)
     written += wanted
@@ -1141,7 +1137,7 @@ def mx_dropout(x, drop, rng, out=None, stream=None):
     _need_rng(rng, dev)
     given = out
     if out is None:
-        out = _new((rows, cols), x.dtype, dev, stream)
+        out = _new((rows, cols), (cols, 1), x.dtype, dev, stream)
     else:
         _need_on(dev, out)
         _need_like(out, "out", x.shape, (x.dtype,))
@@ -1190,7 +1186,7 @@ def mx_rms_norm(x, weight, eps=1e-6, residual=None, drop=0.0, rng=None, y=None, 
     if residual is not None or drop:
         kind = x.dtype if residual is None else residual.dtype
         if h is None:
-            h = _new(shape, kind, dev, stream)
+            h = _new(shape, (C, 1), kind, dev, stream)
         else:
             _need_on(dev, h)
             _need_like(h, "h", shape, (kind,))
@@ -1208,7 +1204,7 @@ def mx_rms_norm(x, weight, eps=1e-6, residual=None, drop=0.0, rng=None, y=None, 
     if pk is not None:
         a.kept_codes, a.kept_scales = pk[0].data_ptr(), pk[1].data_ptr()
     if y is None and p8 is None and p4 is None and pk is None or y is True:
-        y = _new(shape, x.dtype, dev, stream)
+        y = _new(shape, (C, 1), x.dtype, dev, stream)
     elif y is False:
         y = None
     elif y is not None:
@@ -1218,9 +1214,9 @@ def mx_rms_norm(x, weight, eps=1e-6, residual=None, drop=0.0, rng=None, y=None, 
     if y is not None:
         a.y, a.yt = y.data_ptr(), _TYPES[y.dtype]
     if rstd is None or rstd is False:
-        rstd = None if pk is None else _new((T,), torch.float32, dev, stream)
+        rstd = None if pk is None else _new((T,), (1,), torch.float32, dev, stream)
     elif rstd is True:
-        rstd = _new((T,), torch.float32, dev, stream)
+        rstd = _new((T,), (1,), torch.float32, dev, stream)
     else:
         _need_on(dev, rstd)
         _need_like(rstd, "rstd", (T,), (torch.float32,))
@@ -1268,7 +1264,7 @@ def mx_rms_norm_backward(dy, h, rstd, weight, dh=None, drop=0.0, rng=None, out=N
         _need_rng(rng, dev)
         a.rng = rng.data_ptr()
     if out is None:
-        out = _new(shape, h.dtype, dev, stream)
+        out = _new(shape, (C, 1), h.dtype, dev, stream)
     else:
         _need_on(dev, out)
         _need_like(out, "out", shape, (h.dtype,))
@@ -1281,14 +1277,14 @@ def mx_rms_norm_backward(dy, h, rstd, weight, dh=None, drop=0.0, rng=None, out=N
         _need_like(dx, "dx", shape, (x_dtype,))
         written.append(dx)
     elif drop or x_dtype != h.dtype:
-        dx = _new(shape, x_dtype, dev, stream)
+        dx = _new(shape, (C, 1), x_dtype, dev, stream)
     if dx is not None:
         a.dx, a.xt = dx.data_ptr(), _type_of(dx)
     if not need_dw:
         dw = workspace = None
     else:
         if dw is None:
-            dw = _new((C,), torch.float32, dev, stream)
+            dw = _new((C,), (1,), torch.float32, dev, stream)
         else:
             _need_on(dev, dw)
             _need_like(dw, "dw", (C,), (torch.float32,))
@@ -1311,9 +1307,9 @@ def mxfp8_quantize(x, codes=None, scales=None, stream=None):
     p = _mx_panels(cols)
     given = codes, scales
     if codes is None:
-        codes = _new((p, rows, 256), torch.uint8, dev, stream)
+        codes = _new((p, rows, 256), (rows * 256, 256, 1), torch.uint8, dev, stream)
     if scales is None:
-        scales = _new((p, rows, 8), torch.uint8, dev, stream)
+        scales = _new((p, rows, 8), (rows * 8, 8, 1), torch.uint8, dev, stream)
     _need_on(dev, x, codes, scales)
     _need_blocks((codes, scales), "out", rows, cols, 256)
     _launch(_lib.mxfp8_quantize, "mxfp8_quantize", dev, stream, x.data_ptr(), t, rows, cols, codes.data_ptr(),
@@ -1329,7 +1325,7 @@ def mxfp8_dequantize(codes, scales, rows, cols, out_dtype=NS_F32, out=None, stre
     _need_blocks((codes, scales), "in", rows, cols, 256)
     given = out
     if out is None:
-        out = _new((rows, cols), _out_dtype(out_dtype), dev, stream)
+        out = _new((rows, cols), (cols, 1), _out_dtype(out_dtype), dev, stream)
     else:
         _need(out, "out", _KINDS, rows * cols)
     _launch(_lib.mxfp8_dequantize, "mxfp8_dequantize", dev, stream, codes.data_ptr(), scales.data_ptr(), rows, cols,
@@ -1359,7 +1355,7 @@ def mxfp8_gemm(p, q, M, N, K, alpha=1.0, beta=0.0, addend=None, out_dtype=NS_F32
     _need_mx(qc, qs, "q", N, K)
     given = out
     if out is None:
-        out = _new((M, N), _out_dtype(out_dtype), dev, stream)
+        out = _new((M, N), (N, 1), _out_dtype(out_dtype), dev, stream)
     else:
         _need(out, "out", _KINDS, M * N)
     add = None
@@ -1391,7 +1387,7 @@ def nvfp4_linear(x, w, N, out=None, stream=None):
     _need(sg, "global_scale", (torch.float32,), 1)
     given = out
     if out is None:
-        out = _new((T, N), x.dtype, dev, stream)
+        out = _new((T, N), (N, 1), x.dtype, dev, stream)
     else:
         _need(out, "out", _KINDS, T * N)
     _launch(_lib.nvfp4_linear, "nvfp4_linear", dev, stream, x.data_ptr(), t, T, K, codes.data_ptr(),
