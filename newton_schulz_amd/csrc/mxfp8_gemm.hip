@@ -160,7 +160,7 @@ struct Tile {
   static constexpr int kScaleGroups = (BM + BN) / 32;              // 256 bytes each
   static constexpr int kScaleLoads = (kScaleGroups + kWaves - 1) / kWaves;
   static constexpr int kStage = kCodeBytes + kScaleGroups * 256;
-  static constexpr int kScratch = 2304;                            // of a wave's epilogue: 16 rows of 36 floats
+  static constexpr int kScratch = 2304;                            // of a wave's epilogue: 576 floats
   static constexpr int kLds = NST * kStage + kWaves * kScratch;
   static_assert(kCodeLoads * 8 * kWaves == kLines && BM % 8 == 0, "uneven loads");
 };
@@ -349,33 +349,35 @@ __device__ __forceinline__ void put8(const Product8& g, int64_t at, int n, float
 }
 
 // acc[i][j][4 q + t] of a lane is row (wm FM + i) 32 + 8 q + 4 (lane / 32) + t,
-// column (wn FN + j) 32 + lane % 32 of the tile.  Sixteen rows of a block at a
-// time pass through the wave's own LDS, from where a lane takes eight neighbours
-// of a row.
+// column (wn FN + j) 32 + lane % 32 of the tile.  Eight rows of two blocks, or
+// sixteen of one, at a time pass through the wave's own LDS, from where a lane
+// takes eight neighbours of a row.
 // PART: as they are, to a part's own [M][N].
 template <class C, Dt OT, bool PART>
 __device__ __forceinline__ void epilogue(const Product8& g, float* part, const floatx16 (&acc)[C::FM][C::FN], int64_t m0, int64_t n0, int wm,
                                          int wn, int lane, uint8_t* lds) {
-  constexpr int kPitch = 36;
+  constexpr int kPair = C::FN % 2 == 0 ? 2 : 1, kPitch = kPair == 2 ? 72 : 36, kQs = 2 / kPair, kLanes = 4 * kPair;
   float* t = reinterpret_cast<float*>(lds);
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j)
+    for (int q0 = 0; q0 < 4; q0 += kQs)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int el = renewed(lane), h = el >> 5, c = el & 31, r = el >> 2, c8 = (el & 3) * 8;
+      for (int j = 0; j < C::FN; j += kPair) {
+        const int el = renewed(lane), h = el >> 5, c = el & 31, r = el / kLanes, c8 = el % kLanes * 8;
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < kQs; ++q)
 #pragma unroll
-          for (int s = 0; s < 4; ++s) t[(8 * q + 4 * h + s) * kPitch + c] = acc[i][j][8 * half + 4 * q + s];
+          for (int u = 0; u < kPair; ++u)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) t[(8 * q + 4 * h + s) * kPitch + 32 * u + c] = acc[i][j + u][4 * (q0 + q) + s];
         wave_sync();
         float v[8];
         const float4 lo = *reinterpret_cast<const float4*>(t + r * kPitch + c8);
         const float4 hi = *reinterpret_cast<const float4*>(t + r * kPitch + c8 + 4);
         v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
         v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
-        const int64_t row = m0 + (wm * C::FM + i) * 32 + 16 * half + r, col = n0 + (wn * C::FN + j) * 32 + c8;
+        const int64_t row = m0 + (wm * C::FM + i) * 32 + 8 * q0 + r, col = n0 + (wn * C::FN + j) * 32 + c8;
         if (row < g.M && col < g.N) {
           const int64_t at = row * g.N + col;
           const int n = g.N - col < 8 ? (int)(g.N - col) : 8;
