@@ -72,6 +72,21 @@ def test_two_tokens_element_by_element(dtype):
         assert np.all(np.abs(y - want) <= 3 * U * np.abs(want))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N,K", [(1, 19, 2064), (2, 5, 2064), (1, 40, 70032), (2, 33, 40016), (1, 777, 1520), (2, 16, 48), (1, 3, 4112)])
+def test_rows_that_end_inside_a_lane(T, N, K, dtype):
+    """K an odd multiple of 16: random rows, then the last elements one by one."""
+    op, w = weights(N + K, N, K)
+    x = torch.from_numpy(np.random.default_rng(T).standard_t(3, (T, K)).astype(np.float32)).to(TYPES[dtype]).to(DEV)
+    check(ns.nvfp4_linear(x, op, N), x, w, x.dtype)
+    for k in range(K - 48, K):
+        x = torch.zeros(T, K, device=DEV)
+        x[:, k] = 3.0
+        y = host(ns.nvfp4_linear(x.to(TYPES[dtype]), op, N, out=torch.empty(T, N, device=DEV)))
+        want = host(x).astype(np.float64) @ w.T
+        assert np.all(np.abs(y - want) <= 3 * U * np.abs(want))
+
+
 def test_graph_and_streams():
     op, _ = weights(7, 100, 512)
     xs = [torch.randn(T, 512, device=DEV).bfloat16() for T in (1, 2, 5, 40)]
