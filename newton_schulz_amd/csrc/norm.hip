@@ -23,16 +23,19 @@ namespace nvfp4 {
 namespace {
 using namespace mx;
 
-// w[c .. c + 7] of either type, zeros from n on.
-__device__ __forceinline__ void load_weights(const void* w, Dt t, int c, int n, float (&v)[8]) {
+// w[c .. c + 7] of either type, zeros behind its C.
+template <bool TURNS>
+__device__ __forceinline__ void load_weights(const void* w, Dt t, int c, int C, float (&v)[8]) {
   if (t == Dt::F32) {
     Raw8<float> r;
-    r.load(static_cast<const float*>(w) + c, n);
+    r.template load_row<TURNS>(static_cast<const float*>(w), c, C);
+    r.template turn<TURNS>(c, C);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = r.get(i);
   } else {
     Raw8<uint16_t> r;
-    r.load(static_cast<const uint16_t*>(w) + c, n);
+    r.template load_row<TURNS>(static_cast<const uint16_t*>(w), c, C);
+    r.template turn<TURNS>(c, C);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = r.get(i);
   }
@@ -52,7 +55,7 @@ __device__ __forceinline__ V wave_sum(V v) {
 // LPR lanes a row, NV vectors of eight neighbours a lane: vector k of a lane
 // holds columns 8 (k LPR + lane) on, so that 32 lanes hold a panel's 256
 // columns of the row and four of them a block.
-template <class X, class H, int LPR, int NV>
+template <class X, class H, int LPR, int NV, bool TURNS>
 __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_kernel(const NormForward a) {
   constexpr int kThreads = LPR < 256 ? 256 : LPR, kRows = kThreads / LPR, kWaves = LPR / 64;
   static_assert(kRows == 1 || kWaves == 1, "rows that share a workgroup take a wave each");
@@ -69,8 +72,8 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_kernel(const NormF
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = 8 * (k * LPR + lane);
-      x[k].load(static_cast<const X*>(a.x) + at + c, C - c);
-      if (a.residual) r[k].load(static_cast<const H*>(a.residual) + at + c, C - c);
+      x[k].template load_row<TURNS>(static_cast<const X*>(a.x) + at, c, C);
+      if (a.residual) r[k].template load_row<TURNS>(static_cast<const H*>(a.residual) + at, c, C);
     }
     uint64_t seed = 0, offset = 0;
     if (a.drop.rng) {
@@ -80,6 +83,8 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_kernel(const NormF
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = 8 * (k * LPR + lane);
+      x[k].template turn<TURNS>(c, C);
+      if (a.residual) r[k].template turn<TURNS>(c, C);
       if (a.drop.rng) {
         const Mask8 m((uint32_t)(c >> 3), (uint32_t)t, seed, offset);
 #pragma unroll
@@ -120,7 +125,7 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_kernel(const NormF
     const int c = 8 * (k * LPR + lane);
     if (c >= padded) break;                  // whole 32-lane groups leave together
     float w[8];
-    load_weights(a.w, a.wt, c, C - c, w);
+    load_weights<TURNS>(a.w, a.wt, c, C, w);
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -271,7 +276,7 @@ __device__ __forceinline__ void put_gradients(const NormBackward& a, int64_t t, 
   store_as(a.dx, a.xt, at, a.C - c, d);
 }
 
-template <class D, class H, int LPR, int NV>
+template <class D, class H, int LPR, int NV, bool TURNS>
 __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_backward_kernel(const NormBackward a) {
   constexpr int kThreads = LPR < 256 ? 256 : LPR, kRows = kThreads / LPR, kWaves = LPR / 64;
   __shared__ float sums[2][kWaves];
@@ -297,9 +302,9 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_backward_kernel(co
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = 8 * (k * LPR + lane);
-      dy[k].load(static_cast<const D*>(a.dy) + at + c, C - c);
-      h[k].load(static_cast<const H*>(a.h) + at + c, C - c);
-      if (a.dh_in) in[k].load(static_cast<const H*>(a.dh_in) + at + c, C - c);
+      dy[k].template load_row<TURNS>(static_cast<const D*>(a.dy) + at, c, C);
+      h[k].template load_row<TURNS>(static_cast<const H*>(a.h) + at, c, C);
+      if (a.dh_in) in[k].template load_row<TURNS>(static_cast<const H*>(a.dh_in) + at, c, C);
     }
     const float r = a.rstd[t];
     float m = 0.0f;
@@ -307,7 +312,10 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_backward_kernel(co
     for (int k = 0; k < NV; ++k) {
       const int c = 8 * (k * LPR + lane);
       float w[8];
-      load_weights(a.w, a.wt, c, C - c, w);
+      load_weights<TURNS>(a.w, a.wt, c, C, w);
+      dy[k].template turn<TURNS>(c, C);
+      h[k].template turn<TURNS>(c, C);
+      if (a.dh_in) in[k].template turn<TURNS>(c, C);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float xhat = h[k].get(i) * r, p = dy[k].get(i) * xhat;
@@ -335,7 +343,7 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_backward_kernel(co
       const int c = 8 * (k * LPR + lane);
       if (c >= C) break;
       float w[8], d[8];
-      load_weights(a.w, a.wt, c, C - c, w);
+      load_weights<TURNS>(a.w, a.wt, c, C, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float v = r * (dy[k].get(i) * w[i] - h[k].get(i) * r * m);
@@ -398,7 +406,7 @@ __global__ __launch_bounds__(1024) void norm_backward_wide_kernel(const NormBack
       dy.load(static_cast<const D*>(a.dy) + at + c, C - c);
       h.load(static_cast<const H*>(a.h) + at + c, C - c);
       float w[8];
-      load_weights(a.w, a.wt, c, C - c, w);
+      load_weights<false>(a.w, a.wt, c, C, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (c + i >= C) break;
@@ -425,7 +433,7 @@ __global__ __launch_bounds__(1024) void norm_backward_wide_kernel(const NormBack
       h.load(static_cast<const H*>(a.h) + at + c, C - c);
       if (a.dh_in) in.load(static_cast<const H*>(a.dh_in) + at + c, C - c);
       float w[8], d[8];
-      load_weights(a.w, a.wt, c, C - c, w);
+      load_weights<false>(a.w, a.wt, c, C, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float v = r * (dy.get(i) * w[i] - h.get(i) * r * m);
@@ -517,7 +525,9 @@ hipError_t dropout(const X* x, int64_t rows, int64_t cols, const Drop& d, X* out
 template <class X, class H, int LPR, int NV>
 hipError_t forward(const NormForward& a, hipStream_t s) {
   constexpr int kThreads = LPR < 256 ? 256 : LPR, kRows = kThreads / LPR;
-  norm_kernel<X, H, LPR, NV><<<dim3((unsigned)((a.T + kRows - 1) / kRows)), kThreads, 0, s>>>(a);
+  const dim3 grid((unsigned)((a.T + kRows - 1) / kRows));
+  if (turns(a.C)) norm_kernel<X, H, LPR, NV, true><<<grid, kThreads, 0, s>>>(a);
+  else norm_kernel<X, H, LPR, NV, false><<<grid, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 // Lanes and vectors that hold a row: a wave up to 1024 columns, then a
@@ -543,7 +553,9 @@ int64_t backward_groups(int64_t T, int64_t C) {
 
 template <class D, class H, int LPR, int NV>
 hipError_t backward(const NormBackward& a, hipStream_t s) {
-  norm_backward_kernel<D, H, LPR, NV><<<dim3((unsigned)backward_groups(a.T, a.C)), LPR < 256 ? 256 : LPR, 0, s>>>(a);
+  const dim3 grid((unsigned)backward_groups(a.T, a.C)), block(LPR < 256 ? 256 : LPR);
+  if (turns(a.C)) norm_backward_kernel<D, H, LPR, NV, true><<<grid, block, 0, s>>>(a);
+  else norm_backward_kernel<D, H, LPR, NV, false><<<grid, block, 0, s>>>(a);
   return hipGetLastError();
 }
 template <class D, class H>
