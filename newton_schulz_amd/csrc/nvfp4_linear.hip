@@ -42,15 +42,25 @@ struct Nv {
 // Eight neighbours of a row of x, and the BF16 operands that sum to them.
 template <class X> struct Parts;
 template <> struct Parts<uint16_t> {
-  static constexpr int kParts = 1;
+  static constexpr int kParts = 1, kWords = 1;     // sixteen bytes each, as in memory
   wordx4 w;
+  __device__ __forceinline__ wordx4 word(int) const { return w; }
+  __device__ __forceinline__ void set(int, wordx4 v) { w = v; }
   __device__ __forceinline__ void load(const uint16_t* p) { w = *reinterpret_cast<const wordx4*>(p); }
   __device__ __forceinline__ void clear() { w = wordx4{0, 0, 0, 0}; }
   __device__ __forceinline__ void split(wordx4 (&parts)[1]) const { parts[0] = w; }
 };
 template <> struct Parts<float> {
-  static constexpr int kParts = 3;
+  static constexpr int kParts = 3, kWords = 2;
   floatx4 a, b;
+  __device__ __forceinline__ wordx4 word(int i) const {
+    union { floatx4 f; wordx4 u; } r{i ? b : a};
+    return r.u;
+  }
+  __device__ __forceinline__ void set(int i, wordx4 v) {
+    union { wordx4 u; floatx4 f; } r{v};
+    (i ? b : a) = r.f;
+  }
   __device__ __forceinline__ void load(const float* p) {
     a = *reinterpret_cast<const floatx4*>(p);
     b = *reinterpret_cast<const floatx4*>(p + 4);
@@ -238,15 +248,16 @@ __device__ __forceinline__ bf16x8 weights8(uint32_t w, float s) {
 // Of a step of 128 elements lane (q, r) = (l / 16, l % 16) multiplies row r's
 // elements 32 q .. + 31, eight an instruction.  Its codes are 16 bytes of W's row;
 // x comes in whole lines (four rows an instruction) and turns in LDS of the
-// wave's own: chunk c (eight elements) of row r at position c ^ r.
+// wave's own, as it lies in memory: chunk c (eight elements) of row r at position
+// c ^ r, FP32's halves apart.
 // Everything that DEEP steps read goes out before the first is used, from
 // clamped places instead of behind branches, which would wait for each other;
 // the places are 32-bit offsets from scalar bases.
 // K32: K is a multiple of 32, a lane's 32 elements all in or all behind the end.
 template <class X, int TG, Dt OT, int WAVES, int DEEP, bool K32>
 __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
-  constexpr int P = Parts<X>::kParts;
-  __shared__ wordx4 turn[WAVES][P * TG][16][16];
+  constexpr int P = Parts<X>::kParts, W = Parts<X>::kWords;
+  __shared__ wordx4 turn[WAVES][W * TG][16][16];
   __shared__ floatx4 sums[WAVES][TG][64];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -315,24 +326,27 @@ __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
 #pragma unroll
       for (int g = 0; g < TG; ++g)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          wordx4 parts[P];
-          v[i][g][j].split(parts);
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int p = 0; p < P; ++p) turn[wave][g * P + p][4 * j + q][r ^ (4 * j + q)] = parts[p];
-        }
+          for (int p = 0; p < W; ++p) turn[wave][g * W + p][4 * j + q][r ^ (4 * j + q)] = v[i][g][j].word(p);
       wave_sync();
       const float f[2] = {__builtin_amdgcn_cvt_f32_fp8((int)sc[i], 0), __builtin_amdgcn_cvt_f32_fp8((int)sc[i], 1)};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const bf16x8 w = weights8(c[i][j], f[j >> 1]);
 #pragma unroll
-        for (int g = 0; g < TG; ++g)
+        for (int g = 0; g < TG; ++g) {
+          Parts<X> e;
+#pragma unroll
+          for (int p = 0; p < W; ++p) e.set(p, turn[wave][g * W + p][r][(4 * q + j) ^ r]);
+          wordx4 parts[P];
+          e.split(parts);
 #pragma unroll
           for (int p = 0; p < P; ++p) {
-            union { wordx4 u; bf16x8 v; } b{turn[wave][g * P + p][r][(4 * q + j) ^ r]};
+            union { wordx4 u; bf16x8 v; } b{parts[p]};
             acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, b.v, acc[g], 0, 0, 0);
           }
+        }
       }
       wave_sync();
     }
@@ -374,12 +388,12 @@ template <class X, int TG, Dt OT, bool K32>
 hipError_t launch(const Nv& a, hipStream_t s) {
   const unsigned grid = (unsigned)a.groups * (unsigned)((a.T + 16 * TG - 1) / (16 * TG));
   constexpr int kDeep = sizeof(X) == 2 && TG == 1 ? 2 : 1;
-  // FP32's parts take 13 KB of LDS a wave: with more than one workgroup a CU
-  // four waves each leave room for three of them (8 tokens, 11008 x 4096: 21 us
-  // against 26 with eight; 5 tokens, 777 x 1504: 6.2 against 5.9)
+  // FP32 rows cost a wave three times the instructions: while each workgroup has a
+  // CU to itself sixteen waves share K (10 tokens, 938 x 3664: 8.3 us, with eight
+  // 9.2; 16 tokens, 4000 x 4096: 8.7, 9.3; BF16 there 6.3, 5.8)
   if constexpr (sizeof(X) == 4)
-    if (grid > 256) {
-      nv_kernel<X, TG, OT, 4, kDeep, K32><<<grid, 256, 0, s>>>(a);
+    if (grid <= 256) {
+      nv_kernel<X, TG, OT, 16, kDeep, K32><<<grid, 1024, 0, s>>>(a);
       return hipGetLastError();
     }
   nv_kernel<X, TG, OT, 8, kDeep, K32><<<grid, 512, 0, s>>>(a);
