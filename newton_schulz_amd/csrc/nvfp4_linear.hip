@@ -11,7 +11,7 @@
 // One or two tokens (gemv_kernel): a wave takes rows of W whole, 32 codes a
 // lane, x in LDS; v_dot2_f32_bf16 adds a block's sixteen products without its
 // scale, which one fused multiply-add a block applies.
-// More (nv_kernel): a workgroup takes 16 rows of W, its waves divide K; codes
+// More (nv_kernel): a workgroup takes 16 or 32 rows of W, its waves divide K; codes
 // times scales feed v_mfma_f32_16x16x32_bf16.
 #include <type_traits>
 
@@ -254,23 +254,28 @@ __device__ __forceinline__ bf16x8 weights8(uint32_t w, float s) {
 // clamped places instead of behind branches, which would wait for each other;
 // the places are 32-bit offsets from scalar bases.
 // K32: K is a multiple of 32, a lane's 32 elements all in or all behind the end.
-template <class X, int TG, Dt OT, int WAVES, int DEEP, bool K32>
+template <class X, int TG, int NG, Dt OT, int WAVES, int DEEP, bool K32>
 __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
   constexpr int P = Parts<X>::kParts, W = Parts<X>::kWords;
   __shared__ wordx4 turn[WAVES][W * TG][16][16];
-  __shared__ floatx4 sums[WAVES][TG][64];
+  __shared__ floatx4 sums[WAVES][NG * TG][64];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = (int)(blockIdx.x % (unsigned)a.groups) * 16, t0 = (int)(blockIdx.x / (unsigned)a.groups) * 16 * TG;
+  const int n0 = (int)(blockIdx.x % (unsigned)a.groups) * 16 * NG, t0 = (int)(blockIdx.x / (unsigned)a.groups) * 16 * TG;
   const int64_t K = a.K;
   const int steps = (int)((K + 127) / 128), last = (int)(K - 128 * (int64_t)(steps - 1));   // elements of the last step
   const int s0 = (int)((int64_t)steps * wave / WAVES), s1 = (int)((int64_t)steps * (wave + 1) / WAVES);
   // rows behind an operand's end: its last row, into values that are not written
-  const uint32_t row = (uint32_t)(n0 + r < a.N ? r : a.N - 1 - n0);
   const uint8_t* codes = a.codes + (int64_t)n0 * (K / 2);
   const uint8_t* scales = a.scales + (int64_t)n0 * (K / 16);
   const X* x = static_cast<const X*>(a.x) + (int64_t)t0 * K;
-  const uint32_t crow = row * (uint32_t)(K / 2), srow = row * (uint32_t)(K / 16);
+  uint32_t crow[NG], srow[NG];
+#pragma unroll
+  for (int n = 0; n < NG; ++n) {
+    const uint32_t row = (uint32_t)(n0 + 16 * n + r < a.N ? 16 * n + r : a.N - 1 - n0);
+    crow[n] = row * (uint32_t)(K / 2);
+    srow[n] = row * (uint32_t)(K / 16);
+  }
   uint32_t xrow[TG][4];
 #pragma unroll
   for (int g = 0; g < TG; ++g)
@@ -279,12 +284,14 @@ __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
       const int t = 16 * g + 4 * i + q;
       xrow[g][i] = (uint32_t)(t0 + t < a.T ? t : a.T - 1 - t0) * (uint32_t)K;
     }
-  floatx4 acc[TG];
+  floatx4 acc[NG][TG];
 #pragma unroll
-  for (int g = 0; g < TG; ++g) acc[g] = floatx4{0, 0, 0, 0};
+  for (int n = 0; n < NG; ++n)
+#pragma unroll
+    for (int g = 0; g < TG; ++g) acc[n][g] = floatx4{0, 0, 0, 0};
   for (int s = s0; s < s1; s += DEEP) {
-    wordx4 c[DEEP];
-    uint32_t sc[DEEP];
+    wordx4 c[DEEP][NG];
+    uint32_t sc[DEEP][NG];
     Parts<X> v[DEEP][TG][4];
 #pragma unroll
     for (int i = 0; i < DEEP; ++i) {
@@ -292,16 +299,18 @@ __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
       const int end = at == steps - 1 ? last : 128;           // elements of this step
       const uint8_t* cs = codes + (int64_t)at * 64;
       const uint8_t* ss = scales + (int64_t)at * 8;
-      if constexpr (K32) {
-        const uint32_t e = 32 * q < end ? 32u * q : 0u;
-        c[i] = *reinterpret_cast<const wordx4*>(cs + (crow + e / 2));
-        sc[i] = *reinterpret_cast<const uint16_t*>(ss + (srow + e / 16));
-      } else {
-        const uint32_t e0 = 32 * q < end ? 32u * q : 0u, e1 = 32 * q + 16 < end ? 32u * q + 16 : 0u;
-        const uint2 lo = *reinterpret_cast<const uint2*>(cs + (crow + e0 / 2)), hi = *reinterpret_cast<const uint2*>(cs + (crow + e1 / 2));
-        c[i] = wordx4{lo.x, lo.y, hi.x, hi.y};
-        sc[i] = ss[srow + e0 / 16] | (uint32_t)ss[srow + e1 / 16] << 8;
-      }
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+        if constexpr (K32) {
+          const uint32_t e = 32 * q < end ? 32u * q : 0u;
+          c[i][n] = *reinterpret_cast<const wordx4*>(cs + (crow[n] + e / 2));
+          sc[i][n] = *reinterpret_cast<const uint16_t*>(ss + (srow[n] + e / 16));
+        } else {
+          const uint32_t e0 = 32 * q < end ? 32u * q : 0u, e1 = 32 * q + 16 < end ? 32u * q + 16 : 0u;
+          const uint2 lo = *reinterpret_cast<const uint2*>(cs + (crow[n] + e0 / 2)), hi = *reinterpret_cast<const uint2*>(cs + (crow[n] + e1 / 2));
+          c[i][n] = wordx4{lo.x, lo.y, hi.x, hi.y};
+          sc[i][n] = ss[srow[n] + e0 / 16] | (uint32_t)ss[srow[n] + e1 / 16] << 8;
+        }
       const X* xc = x + (int64_t)at * 128;
       const uint32_t e = 8 * r < end ? 8u * r : 0u;
 #pragma unroll
@@ -314,7 +323,8 @@ __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
     for (int i = 0; i < DEEP; ++i) {
       if (s + i >= s1) break;
       if (s + i == steps - 1 && last < 128) {                 // nothing behind K
-        sc[i] = 32 * q + 32 <= last ? sc[i] : 32 * q < last ? sc[i] & 0xFFu : 0u;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) sc[i][n] = 32 * q + 32 <= last ? sc[i][n] : 32 * q < last ? sc[i][n] & 0xFFu : 0u;
         if (8 * r >= last) {
 #pragma unroll
           for (int g = 0; g < TG; ++g)
@@ -330,10 +340,17 @@ __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
 #pragma unroll
           for (int p = 0; p < W; ++p) turn[wave][g * W + p][4 * j + q][r ^ (4 * j + q)] = v[i][g][j].word(p);
       wave_sync();
-      const float f[2] = {__builtin_amdgcn_cvt_f32_fp8((int)sc[i], 0), __builtin_amdgcn_cvt_f32_fp8((int)sc[i], 1)};
+      float f[NG][2];
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        f[n][0] = __builtin_amdgcn_cvt_f32_fp8((int)sc[i][n], 0);
+        f[n][1] = __builtin_amdgcn_cvt_f32_fp8((int)sc[i][n], 1);
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bf16x8 w = weights8(c[i][j], f[j >> 1]);
+        bf16x8 w[NG];
+#pragma unroll
+        for (int n = 0; n < NG; ++n) w[n] = weights8(c[i][n][j], f[n][j >> 1]);
 #pragma unroll
         for (int g = 0; g < TG; ++g) {
           Parts<X> e;
@@ -344,7 +361,8 @@ __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
 #pragma unroll
           for (int p = 0; p < P; ++p) {
             union { wordx4 u; bf16x8 v; } b{parts[p]};
-            acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, b.v, acc[g], 0, 0, 0);
+#pragma unroll
+            for (int n = 0; n < NG; ++n) acc[n][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[n], b.v, acc[n][g], 0, 0, 0);
           }
         }
       }
@@ -352,11 +370,13 @@ __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
     }
   }
 #pragma unroll
-  for (int g = 0; g < TG; ++g) sums[wave][g][lane] = acc[g];
+  for (int n = 0; n < NG; ++n)
+#pragma unroll
+    for (int g = 0; g < TG; ++g) sums[wave][n * TG + g][lane] = acc[n][g];
   __syncthreads();
-  // lane: rows n0 + 4 q .. + 3 of W, row r of x's group `wave`
-  if (wave >= TG) return;
-  const int t = t0 + 16 * wave + r, n = n0 + 4 * q;
+  // wave: rows of W and tokens number `wave`; lane: four rows of W, a token
+  if (wave >= NG * TG) return;
+  const int t = t0 + 16 * (wave % TG) + r, n = n0 + 16 * (wave / TG) + 4 * q;
   if (t >= a.T || n >= a.N) return;
   floatx4 v = sums[0][wave][lane];
   for (int w = 1; w < WAVES; ++w) v += sums[w][wave][lane];
@@ -385,18 +405,29 @@ hipError_t gemv(Nv a, hipStream_t s) {
 }
 
 template <class X, int TG, Dt OT, bool K32>
-hipError_t launch(const Nv& a, hipStream_t s) {
-  const unsigned grid = (unsigned)a.groups * (unsigned)((a.T + 16 * TG - 1) / (16 * TG));
+hipError_t launch(Nv a, hipStream_t s) {
+  const unsigned tokens = (unsigned)((a.T + 16 * TG - 1) / (16 * TG)), grid = (unsigned)a.groups * tokens;
   constexpr int kDeep = sizeof(X) == 2 && TG == 1 ? 2 : 1;
   // FP32 rows cost a wave three times the instructions: while each workgroup has a
   // CU to itself sixteen waves share K (10 tokens, 938 x 3664: 8.3 us, with eight
   // 9.2; 16 tokens, 4000 x 4096: 8.7, 9.3; BF16 there 6.3, 5.8)
   if constexpr (sizeof(X) == 4)
     if (grid <= 256) {
-      nv_kernel<X, TG, OT, 16, kDeep, K32><<<grid, 1024, 0, s>>>(a);
+      nv_kernel<X, TG, 1, OT, 16, kDeep, K32><<<grid, 1024, 0, s>>>(a);
       return hipGetLastError();
     }
-  nv_kernel<X, TG, OT, 8, kDeep, K32><<<grid, 512, 0, s>>>(a);
+  // Pairs of row groups share x's way through LDS (and its split): a workgroup of
+  // two takes 1.6 times as long as one (FP32 1.4), which pays unless the CUs are
+  // then loaded unevenly (us, there / one by one; BF16: 5 x 6000 x 4096 7.7 / 8.3,
+  // 16 x 8192 x 2048 5.3 / 5.6, 100 x 4096 x 4096 16.4 / 18.5, but 16 x 11008 x 4096
+  // 13.7 / 11.9; FP32: 5 x 6000 x 4096 11.9 / 12.7, 32 x 11008 x 4096 24.8 / 32.4)
+  const unsigned pairs = (unsigned)(a.groups + 1) / 2 * tokens;
+  if (grid > 256 && (pairs + 255) / 256 * (sizeof(X) == 4 ? 7 : 8) < (grid + 255) / 256 * 5) {
+    a.groups = (a.groups + 1) / 2;
+    nv_kernel<X, TG, 2, OT, 8, 1, K32><<<pairs, 512, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  nv_kernel<X, TG, 1, OT, 8, kDeep, K32><<<grid, 512, 0, s>>>(a);
   return hipGetLastError();
 }
 template <class X, int TG, Dt OT>

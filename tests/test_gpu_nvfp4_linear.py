@@ -73,6 +73,15 @@ def test_two_tokens_element_by_element(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N,K", [(3, 4113, 160), (5, 6001, 272), (16, 8192, 144), (33, 2100, 336), (100, 2096, 128), (40, 11000, 48), (7, 4112, 1040)])
+def test_pairs_of_row_groups(T, N, K, dtype):
+    """More workgroups than CUs: rows of W by 16 or 32, N that ends inside either."""
+    op, w = weights(N + K, N, K)
+    x = torch.from_numpy(np.random.default_rng(T).standard_t(3, (T, K)).astype(np.float32)).to(TYPES[dtype]).to(DEV)
+    check(ns.nvfp4_linear(x, op, N), x, w, x.dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T,N,K", [(1, 19, 2064), (2, 5, 2064), (1, 40, 70032), (2, 33, 40016), (1, 777, 1520), (2, 16, 48), (1, 3, 4112)])
 def test_rows_that_end_inside_a_lane(T, N, K, dtype):
     """K an odd multiple of 16: random rows, then the last elements one by one."""
