@@ -55,6 +55,9 @@ __device__ __forceinline__ V wave_sum(V v) {
 // LPR lanes a row, NV vectors of eight neighbours a lane: vector k of a lane
 // holds columns 8 (k LPR + lane) on, so that 32 lanes hold a panel's 256
 // columns of the row and four of them a block.
+// 8192 x 4096: BF16 x on an FP32 residual to h and MXFP8 370 MB in 73 us (5.1 TB/s,
+// 98% of a large copy); BF16 with dropout to h and MXFP4 220 MB in 46 us.  One row
+// of 4096: 3.6 us, a launch and two trips to memory behind each other.
 template <class X, class H, int LPR, int NV, bool TURNS>
 __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_kernel(const NormForward a) {
   constexpr int kThreads = LPR < 256 ? 256 : LPR, kRows = kThreads / LPR, kWaves = LPR / 64;
@@ -156,7 +159,7 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_kernel(const NormF
 // The normed rows in MXFP4 along the tokens.  A workgroup takes 256 tokens (one
 // panel of y^T) x 128 columns: a wave a block of 32 tokens, a lane two
 // neighbouring columns of it, whose codes and scales pass through LDS so that
-// each column's 128-byte line leaves whole.
+// each column's 128-byte line leaves whole.  8192 x 4096 BF16: 87 MB in 15.7 us.
 constexpr int kTileCols = 128;
 
 // Two neighbouring columns of a row, as they lie in memory.
@@ -216,7 +219,7 @@ __global__ __launch_bounds__(512) void norm_cols_kernel(const H* h, const float*
   for (int i = 0; i < 32; ++i) r[i] = t0 + i < T ? rstd[t0 + i] : 0.0f;
   // y is computed for its maximum and again for its codes: kept in between, its
   // 64 values a lane cost more than 128 products do (8192 x 4096 BF16: 28.7 us
-  // kept, 18 so)
+  // kept, 15.7 so)
   uint4 k[2];
   uint32_t b[2];
 #pragma unroll
@@ -260,7 +263,9 @@ __global__ __launch_bounds__(512) void norm_cols_kernel(const H* h, const float*
 //   dh = dh_in + r (g - xhat m);  dx = k dh / (1 - p);  dw = sum over tokens of dy xhat
 // A workgroup takes every gridDim-th group of rows and keeps its columns' share
 // of dw in registers; the shares are summed by norm_weight_kernel in a fixed
-// order, so that the result is the same every time.
+// order, so that the result is the same every time.  8192 x 4096 BF16 with dh in and
+// dropout: 347 MB in 72 us (4.8 TB/s) and 4.6 us for the shares of 768 workgroups,
+// three a CU; 333 x 1111 FP32 5.2 and 3.6 us, each a launch and its trips to memory.
 // dh and, through the dropout, dx of eight columns of row t.
 template <class H>
 __device__ __forceinline__ void put_gradients(const NormBackward& a, int64_t t, int c, uint64_t seed, uint64_t offset,
@@ -476,6 +481,9 @@ __global__ __launch_bounds__(1024) void norm_weight_kernel(const float* part, in
 // A lane's vectors are eight neighbours of a row, `nv` to a row; a workgroup
 // takes a run of kDropVectors of them.  inv: 2^32 / nv rounded up, exact for
 // quotients below 2 kDropVectors / nv where nv < kDropVectors.
+// 8192 x 11008 BF16: 361 MB in 69 us, 5.2 TB/s as a copy; vector instructions, most
+// of them the generator's (one call for eight elements), fill 63% of the cycles
+// behind it.  777 x 1501 FP32 5.4 us.
 constexpr int kDropUnroll = 4, kDropVectors = 256 * kDropUnroll;
 
 template <class X>
