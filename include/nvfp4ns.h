@@ -573,9 +573,9 @@ ns_status mx_dropout(const void* x, ns_dtype xt, int64_t rows, int64_t cols, dou
  *            mxfp4_linear_backward takes it for the weights' gradient; or NULL.
  *            Needs rstd.
  *   eps      > 0, finite.  drop, rng: as above; rng may be NULL when drop is 0.
- * C is at most 32768.  At least one output is needed.  A NaN or infinity in h
- * makes NaN of it (0 of its row's finite values beside an infinity), and of the
- * blocks that hold one.
+ * C is at most 32768, T below 2^22 where C is more than 1024.  At least one
+ * output is needed.  A NaN or infinity in h makes NaN of it (0 of its row's
+ * finite values beside an infinity), and of the blocks that hold one.
  */
 typedef struct {
   const void* x;
@@ -658,7 +658,8 @@ ns_status mxfp8_gemm(const uint8_t* codes_p, const uint8_t* scales_p, const uint
  * (codes, scales and global scale as nvfp4_quantize writes them for
  * NVFP4_ROWS), x [T][K] FP32 or BF16 as it is: the layer of a program that
  * serves from NVFP4 weights, built for few tokens (the weights are read once
- * for every 32).  K is a multiple of 16, N of any size.  Products are exact for
+ * for every 32, or 16 in FP32).  K is a multiple of 16, N of any size, T * N at
+ * most 2^30.  Products are exact for
  * BF16 x and within FP32's own rounding otherwise, sums in FP32.
  */
 ns_status nvfp4_linear(const void* x, ns_dtype xt, int64_t T, int64_t K, const uint8_t* w_codes,

@@ -12,6 +12,9 @@ using nvfp4::Dt;
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 24, kMaxCount = (int64_t)1 << 36;
+// A launch has fewer than 2^32 threads: the norm's have a workgroup of up to 1024
+// for a row, the NVFP4 product's one of 512 for 256 results or more.
+constexpr int64_t kMaxWideRows = (int64_t)1 << 22, kMaxNvOutputs = (int64_t)1 << 30;
 inline bool dim_ok(int64_t a) { return a > 0 && a <= kMaxDim; }
 inline bool dims_ok(int64_t r, int64_t c) { return dim_ok(r) && dim_ok(c) && r * c <= kMaxCount; }
 inline int64_t panels(int64_t n) { return (n + nvfp4::mx::kPanel - 1) / nvfp4::mx::kPanel; }
@@ -70,7 +73,7 @@ ns_status mx_rms_norm(const mx_norm_args* a, void* stream) {
   if (!a->h && !a->y && !a->codes8 && !a->codes4 && !a->kept_codes && !a->rstd) return NS_ERR_ARG;
   if (a->kept_codes && !a->rstd) return NS_ERR_ARG;
   const int64_t T = a->T, C = a->C;
-  if (!dims_ok(T, C) || C > nvfp4::kNormMaxCols) return NS_ERR_SHAPE;
+  if (!dims_ok(T, C) || C > nvfp4::kNormMaxCols || (C > 1024 && T >= kMaxWideRows)) return NS_ERR_SHAPE;
   for (const void* p : {a->x, a->residual, a->weight, (const void*)a->h, (const void*)a->y, (const void*)a->codes8,
                         (const void*)a->scales8, (const void*)a->codes4, (const void*)a->scales4,
                         (const void*)a->kept_codes, (const void*)a->kept_scales, (const void*)a->rstd})
@@ -189,7 +192,7 @@ ns_status nvfp4_linear(const void* x, ns_dtype xt, int64_t T, int64_t K, const u
                        const uint8_t* w_scales, const float* w_global_scale, int64_t N, void* y, ns_dtype yt,
                        void* stream) {
   if (!x || !w_codes || !w_scales || !w_global_scale || !y || !dtype_ok(xt) || !dtype_ok(yt)) return NS_ERR_ARG;
-  if (!dims_ok(T, N) || !dims_ok(T, K) || !dims_ok(N, K) || K % 16 != 0) return NS_ERR_SHAPE;
+  if (!dims_ok(T, N) || !dims_ok(T, K) || !dims_ok(N, K) || K % 16 != 0 || T * N > kMaxNvOutputs) return NS_ERR_SHAPE;
   if (!al(x, 16) || !al(w_codes, 16) || !al(w_scales, 16) || !al(w_global_scale, 4) || !al(y, 16)) return NS_ERR_ARG;
   const Span Y{y, (size_t)(T * N) * dtype_size(yt)};
   if (hits(Y, {Span{x, (size_t)(T * K) * dtype_size(xt)}, Span{w_codes, (size_t)(N * K) / 2},

@@ -159,3 +159,14 @@ def test_binding():
         ns.mx_dropout(x, 0.5, None)
     with pytest.raises(ValueError):
         ns.mx_rms_norm_backward(x, x, torch.zeros(3), torch.ones(4), beta=1.0)
+
+
+def test_more_threads_than_a_launch_takes():
+    """A row a workgroup, or 256 results one, beyond 2^32 threads."""
+    assert norm(T=1 << 22, C=1025) == SHAPE and norm(T=1 << 24, C=1025) == SHAPE
+    assert norm(T=1 << 22, C=16384) == SHAPE
+
+    def linear(T, N, K=16):
+        return lib.nvfp4_linear(at(0), 0, T, K, at(1), at(2), at(3), N, at(4), 0, None)
+    assert linear(1 << 20, 1025) == SHAPE
+    assert linear(BIG, 65) == SHAPE
