@@ -45,10 +45,11 @@ __device__ __forceinline__ void store_as(void* p, Dt t, int64_t at, int n, const
   else store8u(static_cast<uint16_t*>(p) + at, n, v);
 }
 
-template <class V>
+// The sum over groups of N lanes, in every lane.
+template <int N = 64, class V>
 __device__ __forceinline__ V wave_sum(V v) {
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  for (int d = N / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
   return v;
 }
 
@@ -61,8 +62,8 @@ __device__ __forceinline__ V wave_sum(V v) {
 template <class X, class H, int LPR, int NV, bool TURNS>
 __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_kernel(const NormForward a) {
   constexpr int kThreads = LPR < 256 ? 256 : LPR, kRows = kThreads / LPR, kWaves = LPR / 64;
-  static_assert(kRows == 1 || kWaves == 1, "rows that share a workgroup take a wave each");
-  __shared__ double sums[kWaves];
+  static_assert(kRows == 1 || kWaves <= 1, "rows that share a workgroup take a wave each at most");
+  __shared__ double sums[kWaves > 0 ? kWaves : 1];
   const int lane = threadIdx.x % LPR;
   const int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / LPR;
   if (kRows > 1 && t >= a.T) return;
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_kernel(const NormF
       s0 = fma((double)v[k][i], (double)v[k][i], s0);
       s1 = fma((double)v[k][i + 1], (double)v[k][i + 1], s1);
     }
-  double sum = wave_sum(s0 + s1);
+  double sum = wave_sum<(LPR < 64 ? LPR : 64)>(s0 + s1);
   if constexpr (kWaves > 1) {
     if ((lane & 63) == 0) sums[lane >> 6] = sum;
     __syncthreads();
@@ -284,7 +285,7 @@ __device__ __forceinline__ void put_gradients(const NormBackward& a, int64_t t, 
 template <class D, class H, int LPR, int NV, bool TURNS>
 __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_backward_kernel(const NormBackward a) {
   constexpr int kThreads = LPR < 256 ? 256 : LPR, kRows = kThreads / LPR, kWaves = LPR / 64;
-  __shared__ float sums[2][kWaves];
+  __shared__ float sums[2][kWaves > 0 ? kWaves : 1];
   const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   const int C = a.C;
   const float inv = 1.0f / (float)C;
@@ -331,7 +332,7 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_backward_kernel(co
         }
       }
     }
-    m = wave_sum(m);
+    m = wave_sum<(LPR < 64 ? LPR : 64)>(m);
     if constexpr (kWaves > 1) {
       // two buffers: a wave writes one again only behind the barrier of the
       // row between, when all have read it
@@ -538,10 +539,11 @@ hipError_t forward(const NormForward& a, hipStream_t s) {
   else norm_kernel<X, H, LPR, NV, false><<<grid, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
-// Lanes and vectors that hold a row: a wave up to 1024 columns, then a
-// workgroup, which needs a barrier but leaves registers for other workgroups.
+// Lanes and vectors that hold a row: half a wave up to a panel, a wave up to 1024
+// columns, then a workgroup, which needs a barrier but leaves registers for other workgroups.
 template <class X, class H>
 hipError_t forward_by_width(const NormForward& a, hipStream_t s) {
+  if (a.C <= kPanel) return forward<X, H, 32, 1>(a, s);
   if (a.C <= 512) return forward<X, H, 64, 1>(a, s);
   if (a.C <= 1024) return forward<X, H, 64, 2>(a, s);
   if (a.C <= 2048) return forward<X, H, 256, 1>(a, s);
@@ -554,7 +556,7 @@ hipError_t forward_by_width(const NormForward& a, hipStream_t s) {
 constexpr int64_t kBackwardGroups = 768;     // workgroups at most, three a CU
 int64_t backward_groups(int64_t T, int64_t C) {
   if (C > 8192) return T < 256 ? T : 256;    // of 1024 lanes, one a CU
-  const int rows = C <= 1024 ? 4 : 1;
+  const int rows = C <= kPanel ? 8 : C <= 1024 ? 4 : 1;
   const int64_t n = (T + rows - 1) / rows;
   return n < kBackwardGroups ? n : kBackwardGroups;
 }
@@ -568,6 +570,7 @@ hipError_t backward(const NormBackward& a, hipStream_t s) {
 }
 template <class D, class H>
 hipError_t backward_by_width(const NormBackward& a, hipStream_t s) {
+  if (a.C <= kPanel) return backward<D, H, 32, 1>(a, s);
   if (a.C <= 512) return backward<D, H, 64, 1>(a, s);
   if (a.C <= 1024) return backward<D, H, 64, 2>(a, s);
   if (a.C <= 2048) return backward<D, H, 256, 1>(a, s);
