@@ -659,8 +659,8 @@ ns_status mxfp8_gemm(const uint8_t* codes_p, const uint8_t* scales_p, const uint
  * NVFP4_ROWS), x [T][K] FP32 or BF16 as it is: the layer of a program that
  * serves from NVFP4 weights, built for few tokens (the weights are read once
  * for every 32, or 16 in FP32).  K is a multiple of 16, N of any size, T * N at
- * most 2^30.  Products are exact for
- * BF16 x and within FP32's own rounding otherwise, sums in FP32.
+ * most 2^30.  Products are exact for BF16 x and within FP32's own rounding
+ * otherwise, sums in FP32.
  */
 ns_status nvfp4_linear(const void* x, ns_dtype xt, int64_t T, int64_t K, const uint8_t* w_codes,
                        const uint8_t* w_scales, const float* w_global_scale, int64_t N, void* y,

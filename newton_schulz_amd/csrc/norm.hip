@@ -142,7 +142,7 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_kernel(const NormF
     if (a.codes8 || a.codes4) {
       top = quad_amax(top);
       const int64_t line = (int64_t)(c / kPanel) * a.T + t;
-      const int l = lane & 31;
+      const int l = (c >> 3) & 31;
       if (a.codes8) {
         const uint32_t byte = scale_byte8(top);
         *reinterpret_cast<uint2*>(a.codes8 + line * kPanelBytes8 + 8 * l) = encode8_e4m3(v[k], byte);
@@ -152,6 +152,19 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_kernel(const NormF
         const uint32_t byte = scale_byte(top);
         *reinterpret_cast<uint32_t*>(a.codes4 + line * kPanelBytes + 4 * l) = encode8(v[k], byte);
         if ((l & 3) == 0) a.scales4[line * kPanelScales + (l >> 2)] = (uint8_t)byte;
+      }
+    }
+  }
+  if constexpr (LPR < 32) {
+    // the rest of the row's one panel
+    for (int l = LPR + lane; l < 32; l += LPR) {
+      if (a.codes8) {
+        *reinterpret_cast<uint2*>(a.codes8 + t * kPanelBytes8 + 8 * l) = make_uint2(0, 0);
+        if ((l & 3) == 0) a.scales8[t * kPanelScales + (l >> 2)] = 0;
+      }
+      if (a.codes4) {
+        *reinterpret_cast<uint32_t*>(a.codes4 + t * kPanelBytes + 4 * l) = 0;
+        if ((l & 3) == 0) a.scales4[t * kPanelScales + (l >> 2)] = 0;
       }
     }
   }
@@ -539,10 +552,13 @@ hipError_t forward(const NormForward& a, hipStream_t s) {
   else norm_kernel<X, H, LPR, NV, false><<<grid, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
-// Lanes and vectors that hold a row: half a wave up to a panel, a wave up to 1024
-// columns, then a workgroup, which needs a barrier but leaves registers for other workgroups.
+// Lanes and vectors that hold a row: an eighth, a quarter or half of a wave up to a
+// panel (262144 x 128 BF16: a wave 95 us, half 53, a quarter 31, of 134 MB), a wave
+// up to 1024 columns, then a workgroup, which needs a barrier but leaves registers for other workgroups.
 template <class X, class H>
 hipError_t forward_by_width(const NormForward& a, hipStream_t s) {
+  if (a.C <= 64) return forward<X, H, 8, 1>(a, s);
+  if (a.C <= 128) return forward<X, H, 16, 1>(a, s);
   if (a.C <= kPanel) return forward<X, H, 32, 1>(a, s);
   if (a.C <= 512) return forward<X, H, 64, 1>(a, s);
   if (a.C <= 1024) return forward<X, H, 64, 2>(a, s);
@@ -556,7 +572,7 @@ hipError_t forward_by_width(const NormForward& a, hipStream_t s) {
 constexpr int64_t kBackwardGroups = 768;     // workgroups at most, three a CU
 int64_t backward_groups(int64_t T, int64_t C) {
   if (C > 8192) return T < 256 ? T : 256;    // of 1024 lanes, one a CU
-  const int rows = C <= kPanel ? 8 : C <= 1024 ? 4 : 1;
+  const int rows = C <= 64 ? 32 : C <= 128 ? 16 : C <= kPanel ? 8 : C <= 1024 ? 4 : 1;
   const int64_t n = (T + rows - 1) / rows;
   return n < kBackwardGroups ? n : kBackwardGroups;
 }
@@ -570,6 +586,8 @@ hipError_t backward(const NormBackward& a, hipStream_t s) {
 }
 template <class D, class H>
 hipError_t backward_by_width(const NormBackward& a, hipStream_t s) {
+  if (a.C <= 64) return backward<D, H, 8, 1>(a, s);
+  if (a.C <= 128) return backward<D, H, 16, 1>(a, s);
   if (a.C <= kPanel) return backward<D, H, 32, 1>(a, s);
   if (a.C <= 512) return backward<D, H, 64, 1>(a, s);
   if (a.C <= 1024) return backward<D, H, 64, 2>(a, s);

@@ -272,3 +272,30 @@ def test_other_streams():
     torch.cuda.synchronize()
     for g in got:
         assert torch.equal(g.y, want.y) and torch.equal(g.kept[0], want.kept[0]) and torch.equal(g.h, want.h)
+
+
+NARROW = [(1, 2), (37, 8), (300, 9), (65, 40), (33, 63), (64, 64), (31, 65), (300, 100), (17, 127), (16, 128), (15, 129), (9, 200), (70, 255), (8, 256)]
+
+
+@pytest.mark.parametrize("types", ["f32 f32 f32", "bf16 f32 bf16"])
+@pytest.mark.parametrize("T,C", NARROW)
+def test_several_rows_a_wave(T, C, types):
+    """Widths around 64, 128 and 256, the last workgroup part full."""
+    test_forward(T, C, types)
+    test_forward_with_dropout(T, C, " ".join(types.split()[:2]), 0.25)
+    test_backward(T, C, types)
+
+
+@pytest.mark.parametrize("T,C", [(1, 9), (300, 15), (7, 63), (300, 257), (7, 1001), (300, 2049), (7, 4095), (2, 8195), (1, 20001)])
+def test_in_place_at_widths_that_end_inside_eight(T, C):
+    """The residual stream and its gradient overwritten: what is written is what
+    apart tensors hold, bit for bit."""
+    x, r, w = heavy(1, T, C, torch.bfloat16), heavy(2, T, C, torch.float32), weight(3, C, torch.bfloat16)
+    apart = ns.mx_rms_norm(x, w, EPS, residual=r, y=True, rstd=True, mxfp8=True)
+    h = r.clone()
+    n = ns.mx_rms_norm(x, w, EPS, residual=h, h=h, y=True, rstd=True, mxfp8=True)
+    assert n.h is h and torch.equal(h, apart.h) and torch.equal(n.y, apart.y) and torch.equal(n.mxfp8[0], apart.mxfp8[0])
+    dy, dh = heavy(4, T, C, torch.bfloat16), heavy(5, T, C, torch.float32)
+    a = ns.mx_rms_norm_backward(dy, h, n.rstd, w, dh=dh)
+    b = ns.mx_rms_norm_backward(dy, h, n.rstd, w, dh=dh, out=dh)
+    assert b.dh is dh and torch.equal(a.dh, dh) and torch.equal(a.dx, b.dx) and torch.equal(a.dw, b.dw)
