@@ -554,7 +554,8 @@ hipError_t forward(const NormForward& a, hipStream_t s) {
 }
 // Lanes and vectors that hold a row: an eighth, a quarter or half of a wave up to a
 // panel (262144 x 128 BF16: a wave 95 us, half 53, a quarter 31, of 134 MB), a wave
-// up to 1024 columns, then a workgroup, which needs a barrier but leaves registers for other workgroups.
+// up to 1024 columns, then a workgroup, which needs a barrier but leaves registers
+// for other workgroups.
 template <class X, class H>
 hipError_t forward_by_width(const NormForward& a, hipStream_t s) {
   if (a.C <= 64) return forward<X, H, 8, 1>(a, s);
