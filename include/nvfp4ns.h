@@ -660,7 +660,8 @@ ns_status mxfp8_gemm(const uint8_t* codes_p, const uint8_t* scales_p, const uint
  * serves from NVFP4 weights, built for few tokens (the weights are read once
  * for every 32, or 16 in FP32).  K is a multiple of 16, N of any size, T * N at
  * most 2^30.  Products are exact for BF16 x and within FP32's own rounding
- * otherwise, sums in FP32.
+ * otherwise (of an FP32 x, what lies below 2^-133 is cut off), sums in FP32 and
+ * of s_g's magnitude: they leave FP32 where sums of x W do.
  */
 ns_status nvfp4_linear(const void* x, ns_dtype xt, int64_t T, int64_t K, const uint8_t* w_codes,
                        const uint8_t* w_scales, const float* w_global_scale, int64_t N, void* y,

@@ -6,7 +6,13 @@
 // x enters as BF16 operands that sum to it: BF16 rows as they are, FP32 rows in
 // three parts of eight bits each, which hold all 24.  E2M1 codes, and codes
 // times their E4M3 scale (at most six significant bits), are exact in BF16 too,
-// so every product is exact and sums are FP32.
+// so every product is exact and sums are FP32.  What lies below 2^-133, BF16's
+// last bit, of an FP32 x is cut off.
+//
+// Codes times block scales reach 2688, and s_g brings them back: a sum without
+// s_g would leave FP32 where y does not (from |x| = 2^128 / 2688 on).  So the
+// power of two of s_g is in the blocks' scales (products stay exact), and what is
+// left of s_g, 1 to 2, follows the sum (Global).
 //
 // One or two tokens (gemv_kernel): a wave takes rows of W whole, 32 codes a
 // lane, x in LDS; v_dot2_f32_bf16 adds a block's sixteen products without its
@@ -103,6 +109,30 @@ template <> struct Parts<float> {
   }
 };
 
+// s_g = unit * rest: unit a power of two, as large as s_g's but for scales that
+// would take a block's factor out of FP32 or its weights below BF16's normal
+// numbers; rest carries the sign, NaN, infinities and zero.
+struct Global {
+  float sg;
+  __device__ __forceinline__ explicit Global(const float* p)
+      : sg(*(const __attribute__((address_space(4))) float*)(uintptr_t)p) {}
+  // To be used from here on: taken before the loads of x and W go out, a wave
+  // would wait for it first (1 x 11008 x 4096 FP32 9.8 us, so 9.4).
+  __device__ __forceinline__ void landed() { asm volatile("" : "+s"(sg)); }
+  __device__ __forceinline__ int bits() const {
+    const int e = (int)(__float_as_uint(sg) >> 23 & 255u) - 127;
+    return e < -116 ? -116 : e > 111 ? 111 : e;
+  }
+  // 2^more unit
+  __device__ __forceinline__ float unit(int more) const { return __uint_as_float((uint32_t)(127 + bits() + more) << 23); }
+  __device__ __forceinline__ float rest() const { return sg * __uint_as_float((uint32_t)(127 - bits()) << 23); }
+};
+
+// Two blocks' scales in the low bytes of b, times a power of two.
+__device__ __forceinline__ floatx2 scales2(uint32_t b, float unit) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b, unit, false);
+}
+
 template <Dt OT>
 __device__ __forceinline__ void put1(void* y, int64_t at, float v) {
   if constexpr (OT == Dt::F32) static_cast<float*>(y)[at] = v;
@@ -127,10 +157,12 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-// Two codes in byte SEL of w, as BF16.
+// Two codes in byte SEL of w, as BF16, over 2^7: a block's sum of sixteen times x,
+// at most 96 |x|, stays in FP32.
+constexpr int kCodeBits = 7;
 template <int SEL>
 __device__ __forceinline__ bf16x2 pair_of(uint32_t w) {
-  return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, SEL);
+  return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f / (1 << kCodeBits), SEL);
 }
 __device__ __forceinline__ float dot8(uint32_t c, wordx4 x, float sum) {
   union { uint32_t u; bf16x2 v; } x0{x[0]}, x1{x[1]}, x2{x[2]}, x3{x[3]};
@@ -166,6 +198,7 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_kernel(const Nv a, int s
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[r][t] = 0.0f;
   const int chunks = span / 8;            // of a part in LDS
+  Global sg(a.sg);
   typedef std::conditional_t<K32, wordx4, wordx4u> Codes;
   typedef std::conditional_t<K32, uint16_t, half_u> Scales;
   Codes c[R];
@@ -195,6 +228,8 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_kernel(const Nv a, int s
       for (int p = 0; p < P; ++p) xs[(t * P + p) * chunks + at] = parts[p];
     }
     __syncthreads();
+    sg.landed();
+    const float unit = sg.unit(kCodeBits);
     const int64_t k1 = k0 + span < a.K ? k0 + span : a.K;
     for (int64_t k = k0; k < k1; k += kStep) {
       wordx4 u[R];
@@ -207,8 +242,9 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_kernel(const Nv a, int s
       for (int r = 0; r < R; ++r) {
         u[r] = half ? wordx4{c[r][2], c[r][3], 0, 0} : wordx4{c[r][0], c[r][1], c[r][2], c[r][3]};
         const uint32_t b = here <= 0 ? 0u : half ? sc[r] >> 8 : sc[r];
-        s[r][0] = __builtin_amdgcn_cvt_f32_fp8((int)b, 0);
-        s[r][1] = __builtin_amdgcn_cvt_f32_fp8((int)b, 1);
+        const floatx2 f = scales2(b, unit);
+        s[r][0] = f.x;
+        s[r][1] = f.y;
       }
       fetch(k + kStep < a.K ? k + kStep : k);
 #pragma unroll
@@ -227,12 +263,11 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_kernel(const Nv a, int s
         }
     }
   }
-  const float sg = *a.sg;
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int t = 0; t < T; ++t) {
-      const float v = lane_sum(acc[r][t]) * sg;
+      const float v = lane_sum(acc[r][t]) * sg.rest();
       if (lane == r * T + t && n0 + r < a.N) put1<OT>(a.y, (int64_t)t * a.N + n0 + r, v);
     }
 }
@@ -293,6 +328,7 @@ __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
   for (int n = 0; n < NG; ++n)
 #pragma unroll
     for (int g = 0; g < TG; ++g) acc[n][g] = floatx4{0, 0, 0, 0};
+  Global sg(a.sg);
   for (int s = s0; s < s1; s += DEEP) {
     wordx4 c[DEEP][NG];
     uint32_t sc[DEEP][NG];
@@ -323,6 +359,8 @@ __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
         for (int j = 0; j < 4; ++j) v[i][g][j].load(xc + (xrow[g][j] + e));
     }
     __builtin_amdgcn_sched_barrier(0);
+    sg.landed();
+    const float unit = sg.unit(0);
 #pragma unroll
     for (int i = 0; i < DEEP; ++i) {
       if (s + i >= s1) break;
@@ -347,8 +385,9 @@ __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
       float f[NG][2];
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        f[n][0] = __builtin_amdgcn_cvt_f32_fp8((int)sc[i][n], 0);
-        f[n][1] = __builtin_amdgcn_cvt_f32_fp8((int)sc[i][n], 1);
+        const floatx2 t = scales2(sc[i][n], unit);
+        f[n][0] = t.x;
+        f[n][1] = t.y;
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -384,7 +423,7 @@ __global__ __launch_bounds__(64 * WAVES) void nv_kernel(const Nv a) {
   if (t >= a.T || n >= a.N) return;
   floatx4 v = sums[0][wave][lane];
   for (int w = 1; w < WAVES; ++w) v += sums[w][wave][lane];
-  v *= *a.sg;
+  v *= sg.rest();
   const int64_t at = (int64_t)t * a.N + n;
   if (a.N % 4 == 0) {
     if constexpr (OT == Dt::F32) *reinterpret_cast<floatx4*>(static_cast<float*>(a.y) + at) = v;
