@@ -1371,6 +1371,19 @@ def mxfp8_gemm(p, q, M, N, K, alpha=1.0, beta=0.0, addend=None, out_dtype=NS_F32
     return out
 
 
+def _need_nv_rows(codes, scales, N, K):
+    """NVFP4 weights of N rows: matrices have to be the call's, since a transposed
+    operand (quantized along the other axis) has as many elements; other views
+    need its size."""
+    for t, what, n in ((codes, "codes", K // 2), (scales, "scales", K // 16)):
+        if t.dtype != torch.uint8:
+            raise TypeError("w: codes and scales are uint8")
+        if t.dim() == 2:
+            _need_shape(t, f"w {what}", (N, n))
+        elif t.numel() != N * n:
+            raise ValueError(f"w {what}: {t.numel()} elements, {N * n} needed")
+
+
 def nvfp4_linear(x, w, N, out=None, stream=None):
     """y = x W^T for x [T][K] (float32/bfloat16, not quantized) and NVFP4 weights
     w = (codes, scales, global_scale) of [N][K] as nvfp4_quantize returns them;
@@ -1380,10 +1393,7 @@ def nvfp4_linear(x, w, N, out=None, stream=None):
     T, K = x.shape
     dev, t = x.device, _type_of(x)
     _need_on(dev, x, codes, scales, sg, out)
-    if codes.numel() != N * K // 2 or scales.numel() != N * K // 16:
-        raise ValueError(f"w: codes and scales of {N} x {K} needed")
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
-        raise TypeError("w: codes and scales are uint8")
+    _need_nv_rows(codes, scales, N, K)
     _need(sg, "global_scale", (torch.float32,), 1)
     given = out
     if out is None:
