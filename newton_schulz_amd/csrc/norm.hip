@@ -208,8 +208,10 @@ __global__ __launch_bounds__(512) void norm_cols_kernel(const H* h, const float*
   const int64_t t0 = g * kPanel + 32 * wave;
   const int64_t c = c0 + 2 * lane;
   const int n = c < C ? (C - c < 2 ? 1 : 2) : 0;
+  // blocks behind the last token are zero whatever the weight is (in one with a
+  // token an infinite or NaN weight makes the block NaN anyway)
   float w[2] = {0.0f, 0.0f};
-  if (n) {
+  if (n && t0 < T) {
     if (wt == Dt::F32) {
       Two<float> t;
       t.template load<false>(static_cast<const float*>(weight) + c, n);
