@@ -15,6 +15,8 @@ constexpr int64_t kMaxDim = (int64_t)1 << 24, kMaxCount = (int64_t)1 << 36;
 // A launch has fewer than 2^32 threads: the norm's have a workgroup of up to 1024
 // for a row, the NVFP4 product's one of 512 for 256 results or more.
 constexpr int64_t kMaxWideRows = (int64_t)1 << 22, kMaxNvOutputs = (int64_t)1 << 30;
+// 2^-254: up to there r of a row without values is finite in FP32, and y zero.
+constexpr double kMinEps = 0x1p-254;
 inline bool dim_ok(int64_t a) { return a > 0 && a <= kMaxDim; }
 inline bool dims_ok(int64_t r, int64_t c) { return dim_ok(r) && dim_ok(c) && r * c <= kMaxCount; }
 inline int64_t panels(int64_t n) { return (n + nvfp4::mx::kPanel - 1) / nvfp4::mx::kPanel; }
@@ -64,7 +66,7 @@ ns_status mx_rms_norm(const mx_norm_args* a, void* stream) {
   Drop d;
   if (!a || !a->x || !a->weight || !dtype_ok(a->xt) || !dtype_ok(a->ht) || !dtype_ok(a->wt) || !dtype_ok(a->yt))
     return NS_ERR_ARG;
-  if (!std::isfinite(a->eps) || a->eps <= 0.0 || !drop_of(a->drop, a->rng, d)) return NS_ERR_ARG;
+  if (!std::isfinite(a->eps) || !(a->eps >= kMinEps) || !drop_of(a->drop, a->rng, d)) return NS_ERR_ARG;
   const bool own_h = a->residual || d.rng;             // h is not x itself
   if (own_h ? !a->h : a->h != nullptr || a->ht != a->xt) return NS_ERR_ARG;
   if ((a->codes8 == nullptr) != (a->scales8 == nullptr) || (a->codes4 == nullptr) != (a->scales4 == nullptr) ||

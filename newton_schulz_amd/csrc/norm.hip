@@ -134,7 +134,7 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_kernel(const NormF
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       v[k][i] = v[k][i] * rstd * w[i];
-      // behind the row's end 0, also beside an infinite rstd
+      // behind the row's end 0, also beside a rstd of NaN
       if (c + i >= C) v[k][i] = 0.0f;
       top = umax(top, mag_bits(v[k][i]));
     }
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_backward_kernel(co
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float xhat = h[k].get(i) * r, p = dy[k].get(i) * xhat;
-        // behind the row's end nothing, also beside an infinite r
+        // behind the row's end nothing, also beside an r that is not finite
         if (c + i < C) {
           m = fmaf(p, w[i], m);
           dw[k][i] += p;

@@ -30,3 +30,15 @@ def test_weights_that_are_not_finite(T, C, types):
     assert torch.equal(n.y.cpu().isnan(), torch.from_numpy(np.isnan(y)))
     for got, (codes, scales) in ((n.mxfp8, L.mx8_quantize(y)), (n.mxfp4, M4.quantize(y)), (n.kept, M4.quantize(y.T))):
         assert np.array_equal(host(got[0]), codes) and np.array_equal(host(got[1]), scales)
+
+
+@pytest.mark.parametrize("C", [9, 64, 300, 5000])
+def test_the_smallest_eps(C):
+    """2^-254: rows without values are zero, the smallest values meet r = 2^127."""
+    x = torch.zeros(3, C, device=DEV)
+    x[1], x[2] = 2.0 ** -149, 3.0
+    n = ns.mx_rms_norm(x, torch.ones(C, device=DEV), 2.0 ** -254, y=True, rstd=True, mxfp8=True)
+    y, r = host(n.y), host(n.rstd)
+    assert not y[0].any() and not host(n.mxfp8[0])[:, 0].any() and not host(n.mxfp8[1])[:, 0].any()
+    assert np.all(y[1] == 2.0 ** -22) and np.all(r[:2] == 2.0 ** 127)
+    assert np.all(np.abs(y[2] - 1.0) <= 3 * 2.0 ** -24)
