@@ -575,8 +575,8 @@ ns_status mx_dropout(const void* x, ns_dtype xt, int64_t rows, int64_t cols, dou
  *   eps      at least 2^-254 (so that r is finite), finite.  drop, rng: as above;
  *            rng may be NULL when drop is 0.
  * C is at most 32768, T below 2^22 where C is more than 1024.  At least one
- * output is needed.  A NaN or infinity in h makes NaN of it (0 of its row's
- * finite values beside an infinity), and of the blocks that hold one.
+ * output is needed.  A NaN in h makes NaN of its whole row of y; an infinity
+ * becomes NaN and its row's finite values 0; a block that holds a NaN is NaN.
  */
 typedef struct {
   const void* x;

@@ -12,8 +12,11 @@ using nvfp4::Dt;
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 24, kMaxCount = (int64_t)1 << 36;
-// A launch has fewer than 2^32 threads: the norm's have a workgroup of up to 1024
-// for a row, the NVFP4 product's one of 512 for 256 results or more.
+// A launch has fewer than 2^32 threads.  The norm's have a workgroup of up to 1024
+// for a row.  The NVFP4 product's are workgroups of 512 (1024 where there are up
+// to 256 of them): ceil(N / 8) for one or two tokens, 2^30 threads at most, else at
+// most ceil(N / 16) ceil(T / 16) <= T N / 256 + N / 16 + T / 16 + 1, with T and N up to
+// 2^24 and T N up to 2^30 no more than 2^22 + 2^21 + 1.
 constexpr int64_t kMaxWideRows = (int64_t)1 << 22, kMaxNvOutputs = (int64_t)1 << 30;
 // 2^-254: up to there r of a row without values is finite in FP32, and y zero.
 constexpr double kMinEps = 0x1p-254;
