@@ -42,3 +42,72 @@ def test_the_smallest_eps(C):
     assert not y[0].any() and not host(n.mxfp8[0])[:, 0].any() and not host(n.mxfp8[1])[:, 0].any()
     assert np.all(y[1] == 2.0 ** -22) and np.all(r[:2] == 2.0 ** 127)
     assert np.all(np.abs(y[2] - 1.0) <= 3 * 2.0 ** -24)
+
+
+U = 2.0 ** -24
+HALF = {torch.float32: U, torch.bfloat16: 2.0 ** -8}
+
+
+def weight_depth(T, C):
+    """FP32 additions behind a column's dw: the rows of a workgroup that a lane
+    takes, those that share it, the workgroups of a thread of the last sum and its
+    32 threads; and 4 for the products."""
+    rows, most = (1, 256) if C > 8192 else (32 if C <= 64 else 16 if C <= 128 else 8 if C <= 256 else 4 if C <= 1024 else 1, 768)
+    groups = min(most, -(-T // rows))
+    return -(-T // (rows * groups)) + rows + -(-groups // 32) + 32 + 4
+
+
+@pytest.mark.parametrize("types", ["f32 f32 f32", "bf16 bf16 bf16", "bf16 f32 bf16"])
+@pytest.mark.parametrize("T,C", [(50000, 24), (25601, 63), (26000, 100), (13000, 255), (6500, 200), (7000, 700), (3500, 1024), (1600, 1500),
+                                 (1537, 2049), (800, 4099), (2400, 6000), (770, 8192), (257, 8193), (600, 8200), (513, 16384), (600, 16385),
+                                 (520, 32768)])
+def test_gradients_of_more_rows_than_workgroups(T, C, types):
+    """Every workgroup walks over rows, with and without the stream's gradient in
+    place and dropout; FP64 on the device, dropout's factors from mx_dropout."""
+    xt, ht, wt = (TYPES[t] for t in types.split())
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T + C)
+    rand = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    h, dy, din = rand(T, C).to(ht), (1e-2 * rand(T, C)).to(xt), (1e-2 * rand(T, C)).to(ht)
+    w = (1 + 0.2 * rand(C)).to(wt)
+    rstd = ns.mx_rms_norm(h, w, rstd=True).rstd
+    r = rstd.double()[:, None]
+    u, G = h.double() * r, dy.double() * w.double()
+    m, size = (G * u).mean(1, keepdim=True), (G * u).abs().mean(1, keepdim=True)
+    dh = r * (G - u * m)
+    # products of up to four roundings, and a row's sum of depth 70: 32 values a
+    # lane, a wave's tree and up to 16 waves
+    bound = r * (6 * U * (G.abs() + u.abs() * size) + 75 * U * u.abs() * size)
+    dw = (dy.double() * u).sum(0)
+    bw = weight_depth(T, C) * U * (dy.double() * u).abs().sum(0)
+    near = lambda got, want, b: bool(((got.double() - want).abs() <= b).all())  # noqa: E731
+    a = ns.mx_rms_norm_backward(dy, h, rstd, w)
+    assert near(a.dh, dh, bound + HALF[ht] * (dh.abs() + bound))
+    assert near(a.dw, dw, bw)
+    b = ns.mx_rms_norm_backward(dy, h, rstd, w)
+    assert torch.equal(a.dh, b.dh) and torch.equal(a.dw, b.dw)
+    rng = torch.tensor([T, C], dtype=torch.int64, device=DEV)
+    f = ns.mx_dropout(torch.ones(T, C, device=DEV), 0.25, rng).double()
+    acc, stream = torch.full((C,), 0.5, device=DEV), din.clone()
+    c = ns.mx_rms_norm_backward(dy, h, rstd, w, dh=stream, out=stream, drop=0.25, rng=rng, dw=acc, beta=2.0)
+    want = din.double() + dh
+    bound = bound + U * want.abs()
+    assert c.dh is stream and near(stream, want, bound + HALF[ht] * (want.abs() + bound))
+    assert near(c.dx, f * want, f * (bound + U * want.abs()) + HALF[xt] * f * (want.abs() + bound))
+    assert c.dw is acc and near(acc, dw + 1.0, bw + U * (dw.abs() + 1.0))
+
+
+@pytest.mark.parametrize("T,C", [(50000, 24), (3500, 700), (800, 4099), (600, 8200), (520, 32768)])
+def test_a_row_without_values_among_many(T, C):
+    """A NaN or an infinity in one row stays there, and in its own columns of dw."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T)
+    h, dy, w = torch.randn(T, C, generator=g, device=DEV), torch.randn(T, C, generator=g, device=DEV), torch.ones(C, device=DEV)
+    clean = ns.mx_rms_norm_backward(dy, h, ns.mx_rms_norm(h, w, rstd=True).rstd, w)
+    at = T - 2
+    dy[at, C // 2] = float("nan")
+    got = ns.mx_rms_norm_backward(dy, h, ns.mx_rms_norm(h, w, rstd=True).rstd, w)
+    rest = torch.arange(T, device=DEV) != at
+    assert torch.isnan(got.dh[at]).all() and torch.equal(got.dh[rest], clean.dh[rest])
+    bad = torch.isnan(got.dw)
+    assert bool(bad[C // 2]) and int(bad.sum()) == 1 and torch.equal(got.dw[~bad], clean.dw[~bad])
