@@ -400,7 +400,8 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_backward_kernel(co
 
 // The same for rows of more than 8192 columns, for which a lane's registers
 // would not do: 1024 lanes walk a row twice, the second time from the caches, and
-// hold its columns' share of dw in LDS.
+// hold its columns' share of dw in LDS.  2048 x 16384 with dh in, both launches: BF16
+// 67.5 us for 268 MB, FP32 131 us for 537 MB (4.0 and 4.1 TB/s); 2048 x 10240 BF16 51.
 template <class D, class H, int V>
 __global__ __launch_bounds__(1024) void norm_backward_wide_kernel(const NormBackward a) {
   __shared__ float share[V * 8 * 1024];

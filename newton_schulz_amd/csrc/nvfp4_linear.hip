@@ -17,8 +17,8 @@
 // One or two tokens (gemv_kernel): a wave takes rows of W whole, 32 codes a
 // lane, x in LDS; v_dot2_f32_bf16 adds a block's sixteen products without its
 // scale, which one fused multiply-add a block applies.  1 x 11008 x 4096 BF16: 25 MB
-// in 7.4 to 7.9 us, 3.2 of them a launch; vector instructions fill two thirds of the
-// cycles that are left.
+// in 7.5 to 8.0 us, 3.2 of them a launch; vector instructions fill 72% of the CUs'
+// busy cycles.
 // More (nv_kernel): a workgroup takes 16 or 32 rows of W, its waves divide K; codes
 // times scales feed v_mfma_f32_16x16x32_bf16.  16 x 4096 x 11008 BF16: 11.3 us, each
 // CU drawing all of x (352 KB, from L2) beside its 100 KB of codes; LDS is busy a
