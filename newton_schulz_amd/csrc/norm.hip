@@ -233,6 +233,13 @@ __global__ __launch_bounds__(512) void norm_cols_kernel(const H* h, const float*
   float r[32];                                   // the tokens' rstd, 0 behind the last
 #pragma unroll
   for (int i = 0; i < 32; ++i) r[i] = t0 + i < T ? rstd[t0 + i] : 0.0f;
+  // codes of tokens behind the last are 0, where 0 * 0 * w is -0 beside w < 0
+  uint32_t mask[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int64_t left = T - t0 - 8 * s;
+    mask[s] = left >= 8 ? 0xFFFFFFFFu : left > 0 ? (1u << (4 * (int)left)) - 1u : 0u;
+  }
   // y is computed for its maximum and again for its codes: kept in between, its
   // 64 values a lane cost more than 128 products do (8192 x 4096 BF16: 28.7 us
   // kept, 15.7 so)
@@ -250,7 +257,7 @@ __global__ __launch_bounds__(512) void norm_cols_kernel(const H* h, const float*
       float e[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) e[i] = u[8 * s + i].get(j) * r[8 * s + i] * w[j];
-      q[s] = encode8(e, b[j]);
+      q[s] = encode8(e, b[j]) & mask[s];
     }
     k[j] = make_uint4(q[0], q[1], q[2], q[3]);
     __builtin_amdgcn_sched_barrier(0);

@@ -32,6 +32,20 @@ def test_weights_that_are_not_finite(T, C, types):
         assert np.array_equal(host(got[0]), codes) and np.array_equal(host(got[1]), scales)
 
 
+@pytest.mark.parametrize("types", ["f32 f32", "bf16 bf16"])
+@pytest.mark.parametrize("T,C", [(1, 70), (5, 8), (31, 33), (32, 40), (33, 128), (40, 256), (249, 129), (256, 48), (257, 64), (300, 300)])
+def test_negative_weights(T, C, types):
+    """What lies behind the last token or column is zero to the bit."""
+    ht, wt = (TYPES[t] for t in types.split())
+    g = np.random.default_rng(T + C)
+    x = torch.from_numpy(g.standard_normal((T, C)).astype(np.float32)).to(ht).to(DEV)
+    w = torch.from_numpy(g.standard_normal(C).astype(np.float32)).to(wt).to(DEV)
+    n = ns.mx_rms_norm(x, w, mxfp8=True, mxfp4=True, kept=True, rstd=True)
+    y = (host(x).astype(np.float32) * host(n.rstd).astype(np.float32)[:, None]) * host(w).astype(np.float32)
+    for got, (codes, scales) in ((n.mxfp8, L.mx8_quantize(y)), (n.mxfp4, M4.quantize(y)), (n.kept, M4.quantize(y.T))):
+        assert np.array_equal(host(got[0]), codes) and np.array_equal(host(got[1]), scales)
+
+
 @pytest.mark.parametrize("C", [9, 64, 300, 5000])
 def test_the_smallest_eps(C):
     """2^-254: rows without values are zero, the smallest values meet r = 2^127."""
